@@ -57,6 +57,8 @@ extern "C" {
 /* logits element type */
 #define SMCSD_DTYPE_F32 0
 #define SMCSD_DTYPE_BF16 1
+/* element type of queries, keys and values beside bf16 (smcsd_qk_norm_rope, smcsd_tree_attention) */
+#define SMCSD_DTYPE_F16 2
 
 /* verify mode */
 #define SMCSD_MODE_SMC 0
@@ -85,6 +87,10 @@ extern "C" {
 #define SMCSD_OP_KV 2
 #define SMCSD_OP_DRAFT 3
 #define SMCSD_OP_KV_CHECK 4
+#define SMCSD_OP_TREE_ATTN 5
+#define SMCSD_OP_LOGPROBS 6
+#define SMCSD_OP_KV_FREE 7
+#define SMCSD_OP_KV_COMPACT 8
 
 /* kinds of violation counted by smcsd_kv_check */
 #define SMCSD_KV_CHECK_KINDS 5
@@ -101,6 +107,12 @@ const char *smcsd_status_string(int code);
  *   SMCSD_OP_VERIFY_SMC / _SPS: B, N, K, V as passed to smcsd_verify (P ignored).
  *   SMCSD_OP_DRAFT: B = number of rows, N = 1, V as passed to smcsd_draft_sample.
  *   SMCSD_OP_KV_CHECK: the pool size P (B, N, K, V ignored); no initial contents needed.
+ *   SMCSD_OP_TREE_ATTN: B, N as passed to smcsd_tree_attention, K = R, V = Hq * D and
+ *   P = Hkv; no initial contents needed.
+ *   SMCSD_OP_LOGPROBS: B = number of rows, N = 1, K = k (the number of alternatives), V;
+ *   no initial contents needed.
+ *   SMCSD_OP_KV_FREE, SMCSD_OP_KV_COMPACT: the pool size P (B, N, K, V ignored); no initial
+ *   contents needed.
  *   SMCSD_OP_KV: B, N and the pool size P (K, V ignored).  The KV workspace must be
  *   zero-filled before its first use and then passed, unmodified, to every later call
  *   with the same B, N and P: calls keep its contents consistent (it alternates two
@@ -362,6 +374,186 @@ int smcsd_kv_check(const int32_t *block_tables, int64_t S, int M_cap, int slots,
                    const int32_t *refcounts, const int32_t *free_list, const int32_t *free_top,
                    int64_t P, int32_t *violations, int32_t *status, void *workspace,
                    size_t workspace_bytes, void *stream);
+
+/*
+ * smcsd_kv_fork - a prompt's admission: the prompt is prefilled into particle 0's table and
+ * the other particles share its blocks by pointer (SMC explainers, "system optimisation
+ * design": prefixes shared across particles, reference counts, no KV data copied).  For
+ * every prompt b with forked[b] != 0 and every slot s of its particle 0's table that holds
+ * a block id, the slot s of particles 1..N-1 takes that id and the block's refcount grows
+ * by the number of slots that took it.  A partial tail block is shared too: the next
+ * smcsd_kv_reassign copies it on write.
+ * forked [B] int32; block_tables [B*N, M_cap], refcounts [P] int32 in/out.  A destination
+ * slot that is not -1 (a table that was not freed) keeps its id, and an id outside [0, P)
+ * other than -1 is not shared; both set SMCSD_ST_BAD_INPUT.  Limits: 1 <= N <= 1024,
+ * B*N*M_cap < 2^31, 1 <= P <= 2^31 - 1.  One launch.
+ */
+int smcsd_kv_fork(const int32_t *forked, int B, int N, int32_t *block_tables, int M_cap,
+                  int32_t *refcounts, int64_t P, int32_t *status, void *stream);
+
+/*
+ * smcsd_kv_free - sequences retire: every sequence g with freed[g] != 0 drops its blocks
+ * (release by reference count).  Each block id in its table costs that block one
+ * reference, the table becomes all -1, and the blocks that reach 0 are pushed on the free
+ * stack in descending id order, as smcsd_kv_reassign pushes.
+ * freed [S] int32; block_tables [S, M_cap], refcounts [P], free_list [P], free_top [1]
+ * int32 in/out, as in smcsd_kv_reassign.  An id outside [0, P) other than -1, a block
+ * that loses more references than it has (its count ends at 0, and it is pushed once if
+ * it had any), and a free_top outside [0, P] (then clamped) or pushed past P (the entries
+ * that do not fit are dropped) set SMCSD_ST_BAD_INPUT.  Limits: 0 <= S, S*M_cap < 2^31,
+ * 1 <= P <= SMCSD_POOL_OPS_MAX_BLOCKS.
+ * workspace: smcsd_workspace_bytes(SMCSD_OP_KV_FREE, 0, 0, 0, 0, P).
+ */
+#define SMCSD_POOL_OPS_MAX_BLOCKS (1LL << 26)
+int smcsd_kv_free(const int32_t *freed, int64_t S, int32_t *block_tables, int M_cap,
+                  int32_t *refcounts, int32_t *free_list, int32_t *free_top, int64_t P,
+                  int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * smcsd_kv_compact - a fragmented pool made dense.  With n live blocks (refcount > 0), the
+ * live blocks with ids >= n move, in ascending order, to the ids < n that are not live, in
+ * ascending order; every table entry and refcount follows, and the free stack becomes
+ * P-1, ..., n (its top n: pops then return ascending ids).  The moves are written as
+ * (source, destination, block_size) to moves [P/2, 3] and their number to *move_count:
+ * running smcsd_kv_copy on that list moves the data of every layer (no destination is a
+ * source).  Entries of moves past the count are left as they were.
+ * block_tables [S, M_cap], refcounts [P], free_list [P], free_top [1] int32 in/out.  All
+ * slots of all tables are followed; an id outside [0, P) is left as it is, and an id of a
+ * block without references becomes -1; both set SMCSD_ST_BAD_INPUT (except -1 itself).
+ * Refcounts <= 0 count as free and end at 0.  Limits: S >= 0, S*M_cap < 2^31,
+ * block_size >= 1, 1 <= P <= SMCSD_POOL_OPS_MAX_BLOCKS.
+ * workspace: smcsd_workspace_bytes(SMCSD_OP_KV_COMPACT, 0, 0, 0, 0, P).
+ */
+int smcsd_kv_compact(int32_t *block_tables, int64_t S, int M_cap, int block_size,
+                     int32_t *refcounts, int32_t *free_list, int32_t *free_top, int64_t P,
+                     int32_t *moves, int32_t *move_count, int32_t *status, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * smcsd_kv_copy - copies pages: the data behind a list of (source block, destination
+ * block, tokens) entries, in every cache of the model with one call.  The lists are those
+ * of smcsd_kv_reassign (copy-on-write: the first seq_len mod block_size tokens of a shared
+ * tail) and smcsd_kv_compact (whole blocks).
+ * caches: a HOST array of n_caches device pointers (the keys' and the values' pages of
+ * each layer), read during the call.  Token t of segment h of block b lies at byte
+ *   caches[c] + b * block_stride + h * segment_stride + t * token_bytes;
+ * a [P, block_size, Hkv, D] cache has one segment of tokens of Hkv*D elements, a
+ * [P, Hkv, block_size, D] cache Hkv segments of tokens of D elements.
+ * list [capacity, 3] int32 and count [1] int32 in device memory; the first
+ * min(*count, capacity) entries run (a *count outside [0, capacity] sets
+ * SMCSD_ST_BAD_INPUT).  Entries with a destination of -1 are skipped (a copy-on-write that
+ * found no block); an entry with a source or destination outside [0, P), or tokens outside
+ * [0, block_size], copies nothing and sets SMCSD_ST_BAD_INPUT.  An entry whose source is
+ * its destination changes nothing.  Entries run in no order: a destination that is also
+ * another entry's source or destination holds undefined bytes of those entries.
+ * Limits: 0 <= n_caches <= SMCSD_KV_COPY_MAX_CACHES, segments >= 1, token_bytes >= 1,
+ * block_size >= 1, block_size * token_bytes < 2^31, strides >= 0, 1 <= P <= 2^31 - 1,
+ * 0 <= capacity < 2^31.  One launch.
+ */
+#define SMCSD_KV_COPY_MAX_CACHES 256
+int smcsd_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int segments,
+                  int64_t segment_stride, int64_t token_bytes, int block_size,
+                  const int32_t *list, const int32_t *count, int64_t capacity, int64_t P,
+                  int32_t *status, void *stream);
+
+/*
+ * smcsd_qk_norm_rope - the new tokens' way into the cache: RMS norms of queries and keys
+ * for each head, the position rotation, and the write of keys and values into the pages
+ * that the round reserved, in one pass (the Score step's batched pass over K+1 positions:
+ * SMC explainers, methodology "core flow").
+ * Token (s, j), j < R, of S sequences: q [S*R, q_stride], k, v [S*R, k_stride / v_stride]
+ * hold its Hq (Hkv) heads of D elements one after the other; dtype SMCSD_DTYPE_BF16 or
+ * SMCSD_DTYPE_F16.  Per head of q and k, in fp32, rounded once at the end:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (no norm where the weight is NULL)
+ *   z = y with its first rot_dim elements turned by the angles of position p
+ * with pairs (i, i + rot_dim/2), or (2i, 2i+1) if interleaved, and (cos, sin) of pair i =
+ * cos_sin[p, i], cos_sin[p, rot_dim/2 + i] (cos_sin [max_pos, rot_dim] fp32; a table,
+ * since angles of far positions want 64 bits).  p = positions[s, j], or ctx_lens[s] + j
+ * where positions is NULL.  q_out [S*R, Hq, D] gets z of the queries; token j's key and value go to
+ * page position ctx_lens[s] + j of sequence s: element d of head h of position t in block b lies at
+ *   cache + b * page_stride + t * token_stride + h * head_stride + d   (element units).
+ * num_nodes [S] (nullable): tokens j >= num_nodes[s] are left alone.  A token whose
+ * position is outside [0, max_pos) (when rot_dim > 0), whose page position is outside
+ * [0, M_cap * block_size) or whose block id is outside [0, P) is left alone altogether and sets SMCSD_ST_BAD_INPUT.
+ * Two tokens that name the same page position race (smcsd_kv_reassign makes tails private).
+ * q_out may be q itself if q_stride = Hq * D.
+ * Limits: Hq, Hkv >= 1, 8 <= D <= 256 and D a multiple of 8; 0 <= rot_dim <= D, a multiple
+ * of 16 (rot_dim = 0: no rotation, cos_sin may be NULL); eps >= 0 finite; 16-byte aligned
+ * pointers and strides of a multiple of 8 elements; M_cap * block_size < 2^31;
+ * S*R*(Hq + 2*Hkv) < 2^31.  One launch.
+ */
+int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, int S, int R, int Hq, int Hkv, int D,
+                       const void *q_weight, const void *k_weight, float eps,
+                       const float *cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                       const int32_t *positions, const int32_t *ctx_lens,
+                       const int32_t *num_nodes, const int32_t *block_tables, int M_cap,
+                       int block_size, int64_t P, void *k_cache, void *v_cache,
+                       int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                       void *q_out, int32_t *status, void *stream);
+
+/*
+ * smcsd_tree_attention - attention of the drafted tokens over the paged cache: the Score
+ * step's one pass over K+1 positions of every particle (SMC explainers, methodology "core
+ * flow"), for chains and for trees of drafts, down to a single token.
+ * Sequence s has ctx_lens[s] tokens in the cache, seen by all its queries, and its R new
+ * tokens (nodes) at page positions ctx_lens[s] + j, of which node i sees those with bit j
+ * of tree_mask[s, i] set (NULL: a chain, j <= i).  With c = scale:
+ *   z_t = c * <q_i, k_t>,  out_i = sum_t softmax(z)_t v_t,  lse_i = ln sum_t exp(z_t)
+ * over the tokens t that node i sees; query head h reads key/value head h / (Hq/Hkv).  A
+ * node that sees nothing gets out = 0 and lse = -inf.  Scores, the running maximum and sum and
+ * the output are held in fp32; the probabilities are rounded to dtype for the matrix
+ * product with v.
+ * q [S*R, q_stride] holds Hq heads of D elements per node (S = B*N sequences, prompt by
+ * prompt); out [S*R, Hq, D]; lse [S*R, Hq] fp32 (nullable); dtype bf16 or f16 for q, the
+ * caches and out; cache layout as in smcsd_qk_norm_rope; block_tables [S, M_cap].
+ * num_nodes [S] (nullable): nodes j >= num_nodes[s] are not seen and their rows of out and
+ * lse are left as they were.  Leading blocks that all N tables of a prompt share (as
+ * smcsd_kv_reassign and smcsd_kv_fork leave them) are read once for the prompt's N*R*Hq/Hkv
+ * rows instead of once per particle.
+ * What stands in the cache at positions that no node of the sequence sees is never used,
+ * nor is a block id outside [0, P): the tokens of such a block are not seen and set
+ * SMCSD_ST_BAD_INPUT.  So do a ctx_lens[s] that is negative or leaves no room for the
+ * nodes in M_cap * block_size positions (the sequence then sees nothing) and a
+ * num_nodes[s] outside [0, R] (then clamped).
+ * max_len: the largest ctx_lens[s] + R, as far as the caller knows it (0: M_cap *
+ * block_size); it steers how the keys are split over workgroups, and is no bound.
+ * Limits: B, N >= 0, 1 <= R <= 64, Hq a multiple of Hkv, 8 <= D <= 256 and D a multiple of
+ * 8; scale finite; 16-byte aligned pointers and strides of a multiple of 8 elements;
+ * M_cap * block_size < 2^31 - 4096, B*N*R*Hq < 2^31, B*N*M_cap < 2^31.
+ * workspace: smcsd_workspace_bytes(SMCSD_OP_TREE_ATTN, B, N, R, Hq * D, Hkv).
+ */
+int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                         const void *v_cache, int64_t page_stride, int64_t token_stride,
+                         int64_t head_stride, const int32_t *block_tables, int M_cap,
+                         int block_size, int64_t P, const int32_t *ctx_lens,
+                         const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N, int R,
+                         int Hq, int Hkv, int D, float scale, int64_t max_len, void *out,
+                         float *lse, int32_t *status, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * smcsd_token_logprobs - what a sampler reports about rows of logits, from one streaming
+ * read of them: the log-probabilities of given tokens, the entropy, the most probable
+ * alternatives and the log-normaliser (the log-softmax of smcsd_verify, on any rows).
+ * Row r: logits + r * row_stride (element units), V valid elements, bf16 or fp32; with
+ * z = logit / temperature, LSE = ln sum exp(z), p = exp(z - LSE):
+ *   out_logp[r, i] = z[tokens[r, i]] - LSE     (tokens [n, C] int32)
+ *   out_entropy[r] = -sum p ln p,   out_lse[r] = LSE
+ *   top_ids[r, i], top_logp[r, i]: the k largest logits, largest first, equal ones by the
+ *   smaller id; where a row has fewer than k finite logits the rest are -1 and -inf.
+ * A token outside [0, V) gets NaN and sets SMCSD_ST_BAD_INPUT.  A row with no finite logit
+ * gets -inf log-probabilities, entropy 0, LSE -inf and ids -1, and sets
+ * SMCSD_ST_EMPTY_ROW; a row with a NaN or +inf logit gets NaN and ids -1, and sets
+ * SMCSD_ST_NAN_INPUT.  Every output is nullable (C = 0 needs no tokens, k = 0 no top).
+ * Limits: n >= 0, 1 <= V <= 2^24, 0 <= C <= 1024, 0 <= k <= 64, k <= V, row_stride >= V,
+ * temperature finite > 0.  workspace: smcsd_workspace_bytes(SMCSD_OP_LOGPROBS, n, 1, k, V, 0).
+ */
+int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n, int V,
+                         float temperature, const int32_t *tokens, int C, int k,
+                         float *out_logp, float *out_entropy, float *out_lse, int32_t *top_ids,
+                         float *top_logp, int32_t *status, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 /*
  * smcsd_philox4x32_10 - the library's device Philox4x32-10 block function (SC'11),

@@ -10,16 +10,18 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmcsd.so")
 
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 MODE_SMC, MODE_SPS, MODE_SMC_RACE = 0, 1, 2  # MODE_SMC_RACE: SMC with the exponential-race bonus
 OP_VERIFY_SMC, OP_VERIFY_SPS, OP_KV, OP_DRAFT, OP_KV_CHECK = 0, 1, 2, 3, 4
+OP_TREE_ATTN, OP_LOGPROBS, OP_KV_FREE, OP_KV_COMPACT = 5, 6, 7, 8
+KV_COPY_MAX_CACHES = 256
 STATIC_SCRATCH_BYTES = 4 << 20  # smcsd_verify_static's per-GPU scratch array
 
 ST_NAN_INPUT = 1
@@ -37,9 +39,11 @@ KV_CHECK_NAMES = ("refcount != table references", "table id out of range",
 EXPORTED = ("smcsd_version", "smcsd_status_string", "smcsd_workspace_bytes", "smcsd_verify",
             "smcsd_verify_static", "smcsd_draft_sample", "smcsd_resample", "smcsd_kv_reassign",
             "smcsd_resample_kv_reassign", "smcsd_step", "smcsd_kv_check", "smcsd_philox4x32_10",
-            "smcsd_stream_read")
+            "smcsd_stream_read", "smcsd_kv_fork", "smcsd_kv_free", "smcsd_kv_compact",
+            "smcsd_kv_copy", "smcsd_qk_norm_rope", "smcsd_tree_attention", "smcsd_token_logprobs")
 
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_DT_KV = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
 class SmcsdError(RuntimeError):
@@ -90,6 +94,25 @@ def load_library(path: str = LIB_PATH):
     lib.smcsd_philox4x32_10.restype = i32
     lib.smcsd_stream_read.argtypes = [P, i64, P, P]
     lib.smcsd_stream_read.restype = i32
+    lib.smcsd_kv_fork.argtypes = [P, i32, i32, P, i32, P, i64, P, P]
+    lib.smcsd_kv_fork.restype = i32
+    lib.smcsd_kv_free.argtypes = [P, i64, P, i32, P, P, P, i64, P, P, sz, P]
+    lib.smcsd_kv_free.restype = i32
+    lib.smcsd_kv_compact.argtypes = [P, i64, i32, i32, P, P, P, i64, P, P, P, P, sz, P]
+    lib.smcsd_kv_compact.restype = i32
+    lib.smcsd_kv_copy.argtypes = [P, i32, i64, i32, i64, i64, i32, P, P, i64, i64, P, P]
+    lib.smcsd_kv_copy.restype = i32
+    lib.smcsd_qk_norm_rope.argtypes = [P, P, P, i32, i64, i64, i64, i32, i32, i32, i32, i32, P, P,
+                                       f32, P, i64, i32, i32, P, P, P, P, i32, i32, i64, P, P, i64,
+                                       i64, i64, P, P, P]
+    lib.smcsd_qk_norm_rope.restype = i32
+    lib.smcsd_tree_attention.argtypes = [P, i32, i64, P, P, i64, i64, i64, P, i32, i32, i64, P, P,
+                                         P, i32, i32, i32, i32, i32, i32, f32, i64, P, P, P, P, sz,
+                                         P]
+    lib.smcsd_tree_attention.restype = i32
+    lib.smcsd_token_logprobs.argtypes = [P, i32, i64, i32, i32, f32, P, i32, i32, P, P, P, P, P, P,
+                                         P, sz, P]
+    lib.smcsd_token_logprobs.restype = i32
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -402,3 +425,257 @@ def stream_read(buf: torch.Tensor, tile_xor: torch.Tensor, stream=None):
     rc = _L().smcsd_stream_read(ctypes.c_void_p(buf.data_ptr()), nbytes,
                                 _dev(tile_xor, "tile_xor", torch.int32, ntiles), _stream(stream))
     _check(rc, "smcsd_stream_read")
+
+
+# ---------------------------------------------------------------------------------------
+# The pages' own operations
+# ---------------------------------------------------------------------------------------
+def _tables(block_tables: torch.Tensor, rows: Optional[int] = None):
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2 or (
+            rows is not None and block_tables.shape[0] != rows):
+        raise SmcsdError("block_tables must be [%s, M_cap]" % ("S" if rows is None else rows))
+    return _dev(block_tables, "block_tables", torch.int32)
+
+
+def kv_fork(forked: torch.Tensor, B: int, N: int, block_tables: torch.Tensor,
+            refcounts: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """smcsd_kv_fork: the tables of the prompts with forked[b] != 0 from their particle 0's
+    (admission of a prefilled prompt).  block_tables [B*N, M_cap], refcounts [P] in/out."""
+    T = _tables(block_tables, B * N)
+    rc = _L().smcsd_kv_fork(
+        _dev(forked, "forked", torch.int32, B), B, N, T, block_tables.shape[1],
+        _dev(refcounts, "refcounts", torch.int32), refcounts.numel(),
+        _dev(status, "status", torch.int32, 1), _stream(stream))
+    _check(rc, "smcsd_kv_fork")
+
+
+def kv_free(freed: torch.Tensor, block_tables: torch.Tensor, refcounts: torch.Tensor,
+            free_list: torch.Tensor, free_top: torch.Tensor, status: torch.Tensor,
+            workspace: torch.Tensor, stream=None) -> None:
+    """smcsd_kv_free: the sequences with freed[g] != 0 drop their blocks.  workspace from
+    alloc_workspace(OP_KV_FREE, 0, 0, P=P)."""
+    T = _tables(block_tables)
+    S, M_cap = block_tables.shape
+    P = refcounts.numel()
+    rc = _L().smcsd_kv_free(
+        _dev(freed, "freed", torch.int32, S), S, T, M_cap, _dev(refcounts, "refcounts", torch.int32),
+        _dev(free_list, "free_list", torch.int32, P), _dev(free_top, "free_top", torch.int32, 1), P,
+        _dev(status, "status", torch.int32, 1), _dev(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check(rc, "smcsd_kv_free")
+    _debug_kv_check(block_tables, 1, M_cap, 0, refcounts, free_list, free_top, "smcsd_kv_free",
+                    stream)
+
+
+def kv_compact(block_tables: torch.Tensor, block_size: int, refcounts: torch.Tensor,
+               free_list: torch.Tensor, free_top: torch.Tensor, moves: torch.Tensor,
+               move_count: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+               stream=None) -> None:
+    """smcsd_kv_compact: live blocks to the lowest ids; moves [P // 2, 3] and move_count are
+    what kv_copy then runs on the data.  workspace from alloc_workspace(OP_KV_COMPACT, 0, 0,
+    P=P)."""
+    T = _tables(block_tables)
+    S, M_cap = block_tables.shape
+    P = refcounts.numel()
+    rc = _L().smcsd_kv_compact(
+        T, S, M_cap, int(block_size), _dev(refcounts, "refcounts", torch.int32),
+        _dev(free_list, "free_list", torch.int32, P), _dev(free_top, "free_top", torch.int32, 1), P,
+        _dev(moves, "moves", torch.int32, 3 * (P // 2)),
+        _dev(move_count, "move_count", torch.int32, 1), _dev(status, "status", torch.int32, 1),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(rc, "smcsd_kv_compact")
+    _debug_kv_check(block_tables, 1, M_cap, 0, refcounts, free_list, free_top, "smcsd_kv_compact",
+                    stream)
+
+
+def _pages(t: torch.Tensor, name: str, dtype=None):
+    """A cache seen as [P, block_size, Hkv, D]: rows of D contiguous elements, any strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SmcsdError("%s must be a device tensor" % name)
+    if t.dim() != 4 or t.shape[3] < 1 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise SmcsdError("%s must be [P, block_size, Hkv, D] with contiguous rows of D" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise SmcsdError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    return t
+
+
+def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Tensor,
+            status: torch.Tensor, stream=None) -> None:
+    """smcsd_kv_copy: runs a list of (source, destination, tokens) entries, as kv_reassign
+    (copy-on-write) and kv_compact write them, on every cache.  caches: tensors seen as
+    [P, block_size, Hkv, D], all of one shape, type and layout; a [P, Hkv, block_size, D]
+    cache is passed as its transpose(1, 2)."""
+    caches = list(caches)
+    if len(caches) > KV_COPY_MAX_CACHES:
+        raise SmcsdError("at most %d caches a call" % KV_COPY_MAX_CACHES)
+    if moves.dim() != 2 or moves.shape[1] != 3:
+        raise SmcsdError("moves must be [capacity, 3]")
+    mp = _dev(moves, "moves", torch.int32)
+    cp = _dev(count, "count", torch.int32, 1)
+    sp = _dev(status, "status", torch.int32, 1)
+    if not caches:
+        return
+    first = _pages(caches[0], "caches[0]")
+    for i, c in enumerate(caches):
+        _pages(c, "caches[%d]" % i, first.dtype)
+        if c.shape != first.shape or c.stride() != first.stride():
+            raise SmcsdError("caches must have one shape and layout")
+        if c.device != moves.device:
+            raise SmcsdError("caches and moves must be on one device")
+    P, bs, H, D = first.shape
+    e = first.element_size()
+    page, token, head = (s * e for s in first.stride()[:3])
+    if H == 1 or head == D * e:  # a token's heads lie one after the other
+        segments, seg, tok = 1, 0, H * D * e
+        if bs > 1 and token != tok:  # tokens apart: each is a segment of its own
+            raise SmcsdError("a token's heads, or a head's tokens, must be contiguous")
+    elif bs == 1 or token == D * e:
+        segments, seg, tok = H, head, D * e
+    else:
+        raise SmcsdError("a token's heads, or a head's tokens, must be contiguous")
+    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    rc = _L().smcsd_kv_copy(ptrs, len(caches), page, segments, seg, tok, bs, mp, cp,
+                            moves.shape[0], P, sp, _stream(stream))
+    _check(rc, "smcsd_kv_copy")
+
+
+# ---------------------------------------------------------------------------------------
+# The Score step's attention side
+# ---------------------------------------------------------------------------------------
+def _heads(t: torch.Tensor, name: str, S: int, R: int, D: int, dtype):
+    """[S, R, H, D] with a token's heads contiguous and one stride between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SmcsdError("%s must be a device tensor" % name)
+    if t.dim() != 4 or t.shape[0] != S or t.shape[1] != R or t.shape[3] != D:
+        raise SmcsdError("%s must be [%d, %d, heads, %d]" % (name, S, R, D))
+    if t.dtype != dtype:
+        raise SmcsdError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    H = t.shape[2]
+    tok = t.stride(1) if R > 1 else (t.stride(0) if S > 1 else H * D)
+    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or \
+            (S > 1 and t.stride(0) != R * tok):
+        raise SmcsdError("%s must hold each token's heads contiguously, tokens one stride apart"
+                         % name)
+    return ctypes.c_void_p(t.data_ptr()), tok
+
+
+def _cache_pair(k_cache, v_cache, dtype, D):
+    _pages(k_cache, "k_cache", dtype)
+    _pages(v_cache, "v_cache", dtype)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise SmcsdError("k_cache and v_cache must have one shape and layout")
+    if k_cache.shape[3] != D:
+        raise SmcsdError("the caches' heads must have %d elements" % D)
+    P, bs, H, _ = k_cache.shape
+    page, token, head = k_cache.stride()[:3]
+    # the stride of an axis of one entry says nothing
+    token = D if bs == 1 else token
+    head = D if H == 1 else head
+    page = D if P == 1 else page
+    return (ctypes.c_void_p(k_cache.data_ptr()), ctypes.c_void_p(v_cache.data_ptr()), P, bs, H, page,
+            token, head)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ctx_lens: torch.Tensor,
+                 block_tables: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 q_out: torch.Tensor, status: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 positions: Optional[torch.Tensor] = None,
+                 num_nodes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """smcsd_qk_norm_rope.  q [S, R, Hq, D], k, v [S, R, Hkv, D] (bf16 or f16; views into a
+    fused projection will do), q_out [S, R, Hq, D]; k_cache, v_cache seen as [P, block_size,
+    Hkv, D] with any strides between rows of D; cos_sin [max_pos, rot_dim] fp32 (None: no
+    rotation), positions [S, R] int32 (None: ctx_lens + j), num_nodes [S] int32."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise SmcsdError("q and k must be [S, R, heads, D]")
+    if q.dtype not in _DT_KV:
+        raise SmcsdError("queries, keys and values must be bfloat16 or float16")
+    S, R, Hq, D = q.shape
+    Hkv = k.shape[2]
+    qp, qs = _heads(q, "q", S, R, D, q.dtype)
+    kp, ks = _heads(k, "k", S, R, D, q.dtype)
+    vp, vs = _heads(v, "v", S, R, D, q.dtype)
+    if v.shape[2] != Hkv:
+        raise SmcsdError("k and v must have the same heads")
+    kc, vc, P, bs, H, page, token, head = _cache_pair(k_cache, v_cache, q.dtype, D)
+    if H != Hkv:
+        raise SmcsdError("the caches hold %d heads, k has %d" % (H, Hkv))
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise SmcsdError("cos_sin must be [max_pos, rot_dim]")
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    T = _tables(block_tables, S)
+    rc = _L().smcsd_qk_norm_rope(
+        qp, kp, vp, _DT_KV[q.dtype], qs, ks, vs, S, R, Hq, Hkv, D,
+        _dev(q_weight, "q_weight", q.dtype, D), _dev(k_weight, "k_weight", q.dtype, D), float(eps),
+        _dev(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(bool(interleaved)),
+        _dev(positions, "positions", torch.int32, S * R), _dev(ctx_lens, "ctx_lens", torch.int32, S),
+        _dev(num_nodes, "num_nodes", torch.int32, S), T, block_tables.shape[1], bs, P, kc, vc, page,
+        token, head, _dev(q_out, "q_out", q.dtype, S * R * Hq * D),
+        _dev(status, "status", torch.int32, 1), _stream(stream))
+    _check(rc, "smcsd_qk_norm_rope")
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, ctx_lens: torch.Tensor, B: int, N: int,
+                   scale: float, out: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                   tree_mask: Optional[torch.Tensor] = None,
+                   num_nodes: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   max_len: int = 0, stream=None) -> None:
+    """smcsd_tree_attention.  q [B*N, R, Hq, D] (bf16 or f16); k_cache, v_cache seen as [P,
+    block_size, Hkv, D] with any strides between rows of D; out [B*N, R, Hq, D]; tree_mask
+    [B*N, R] int64 (bit j of row i: node i sees node j; None: a chain); lse [B*N, R, Hq]
+    fp32.  workspace from alloc_workspace(OP_TREE_ATTN, B, N, K=R, V=Hq * D, P=Hkv)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != B * N:
+        raise SmcsdError("q must be [B*N, R, Hq, D]")
+    if q.dtype not in _DT_KV:
+        raise SmcsdError("queries and caches must be bfloat16 or float16")
+    S, R, Hq, D = q.shape
+    qp, qs = _heads(q, "q", S, R, D, q.dtype)
+    kc, vc, P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, q.dtype, D)
+    T = _tables(block_tables, S)
+    rc = _L().smcsd_tree_attention(
+        qp, _DT_KV[q.dtype], qs, kc, vc, page, token, head, T, block_tables.shape[1], bs, P,
+        _dev(ctx_lens, "ctx_lens", torch.int32, S), _dev(num_nodes, "num_nodes", torch.int32, S),
+        _dev(tree_mask, "tree_mask", torch.int64, S * R), B, N, R, Hq, Hkv, D, float(scale),
+        int(max_len), _dev(out, "out", q.dtype, S * R * Hq * D),
+        _dev(lse, "lse", torch.float32, S * R * Hq), _dev(status, "status", torch.int32, 1),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check(rc, "smcsd_tree_attention")
+
+
+def token_logprobs(logits: torch.Tensor, n: int, V: int, temperature: float, status: torch.Tensor,
+                   workspace: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                   out_logp: Optional[torch.Tensor] = None,
+                   out_entropy: Optional[torch.Tensor] = None,
+                   out_lse: Optional[torch.Tensor] = None,
+                   top_ids: Optional[torch.Tensor] = None,
+                   top_logp: Optional[torch.Tensor] = None, row_stride: Optional[int] = None,
+                   stream=None) -> None:
+    """smcsd_token_logprobs on logits [n, row_stride] (bf16 or fp32): tokens [n, C] int32 and
+    out_logp [n, C]; out_entropy, out_lse [n]; top_ids and top_logp [n, k] (k = their second
+    extent).  workspace from alloc_workspace(OP_LOGPROBS, n, 1, K=k, V=V)."""
+    if logits.dtype not in _DT:
+        raise SmcsdError("logits must be bfloat16 or float32")
+    rs = V if row_stride is None else int(row_stride)
+    C, k = 0, 0
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != n:
+            raise SmcsdError("tokens must be [n, C]")
+        C = tokens.shape[1]
+    for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] != n:
+                raise SmcsdError("%s must be [n, k]" % name)
+            if top_ids is not None and t.shape[1] != top_ids.shape[1]:
+                raise SmcsdError("top_ids and top_logp must have the same k")
+            k = t.shape[1]
+    rc = _L().smcsd_token_logprobs(
+        _dev(logits, "logits", logits.dtype, n * rs - (rs - V) if n else 0), _DT[logits.dtype], rs, n,
+        V, float(temperature), _dev(tokens, "tokens", torch.int32, n * C), C, k,
+        _dev(out_logp, "out_logp", torch.float32, n * C),
+        _dev(out_entropy, "out_entropy", torch.float32, n), _dev(out_lse, "out_lse", torch.float32, n),
+        _dev(top_ids, "top_ids", torch.int32), _dev(top_logp, "top_logp", torch.float32),
+        _dev(status, "status", torch.int32, 1), _dev(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check(rc, "smcsd_token_logprobs")

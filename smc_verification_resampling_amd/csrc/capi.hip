@@ -60,6 +60,20 @@ size_t smcsd_workspace_bytes(int op, int B, int N, int K, int V, int64_t P) {
     if (P < 1 || P > INT32_MAX) return 0;
     return kv_check_ws_bytes(P);
   }
+  if (op == SMCSD_OP_TREE_ATTN) {
+    if (K < 1 || K > kMaxNodes || V < 1 || P < 1 || V % P || S > INT32_MAX || S * K > INT32_MAX ||
+        S * K > INT64_MAX / 64 / V)
+      return 0;
+    return tree_attn_ws_bytes(S, K, V, P);
+  }
+  if (op == SMCSD_OP_LOGPROBS) {
+    if (V < 1 || V > kMaxV || K < 0 || K > kMaxTop || K > V || S > INT32_MAX) return 0;
+    return logprobs_ws_bytes(S, K, V);
+  }
+  if (op == SMCSD_OP_KV_FREE || op == SMCSD_OP_KV_COMPACT) {
+    if (P < 1 || P > SMCSD_POOL_OPS_MAX_BLOCKS) return 0;
+    return op == SMCSD_OP_KV_FREE ? kv_free_ws_bytes(P) : kv_compact_ws_bytes(P);
+  }
   return 0;
 }
 
@@ -378,6 +392,218 @@ int smcsd_kv_check(const int32_t *block_tables, int64_t S, int M_cap, int slots,
   return hip_rc(launch_kv_check(block_tables, S, M_cap, slots, refcounts, free_list, free_top, P,
                                 violations, status, static_cast<char *>(workspace),
                                 as_stream(stream)));
+}
+
+int smcsd_kv_fork(const int32_t *forked, int B, int N, int32_t *block_tables, int M_cap,
+                  int32_t *refcounts, int64_t P, int32_t *status, void *stream) {
+  if (B < 0 || N < 1 || N > kMaxN || M_cap < 1 || P < 1 || P > INT32_MAX) return SMCSD_EINVAL;
+  if (B == 0) return SMCSD_OK;
+  if ((int64_t)B * N * M_cap >= INT32_MAX) return SMCSD_EINVAL;
+  if (!forked || !block_tables || !refcounts || !status) return SMCSD_EINVAL;
+  return hip_rc(launch_kv_fork(forked, B, N, block_tables, M_cap, refcounts, P, status,
+                               as_stream(stream)));
+}
+
+int smcsd_kv_free(const int32_t *freed, int64_t S, int32_t *block_tables, int M_cap,
+                  int32_t *refcounts, int32_t *free_list, int32_t *free_top, int64_t P,
+                  int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
+  if (S < 0 || M_cap < 1 || P < 1 || P > SMCSD_POOL_OPS_MAX_BLOCKS || S >= INT32_MAX ||
+      S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if (S == 0) return SMCSD_OK;
+  if (!freed || !block_tables || !refcounts || !free_list || !free_top || !status)
+    return SMCSD_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kv_free_ws_bytes(P))
+    return SMCSD_EWORKSPACE;
+  return hip_rc(launch_kv_free(freed, S, block_tables, M_cap, refcounts, free_list, free_top, P,
+                               status, static_cast<char *>(workspace), as_stream(stream)));
+}
+
+int smcsd_kv_compact(int32_t *block_tables, int64_t S, int M_cap, int block_size,
+                     int32_t *refcounts, int32_t *free_list, int32_t *free_top, int64_t P,
+                     int32_t *moves, int32_t *move_count, int32_t *status, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  if (S < 0 || M_cap < 1 || block_size < 1 || P < 1 || P > SMCSD_POOL_OPS_MAX_BLOCKS ||
+      S >= INT32_MAX || S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if ((S > 0 && !block_tables) || !refcounts || !free_list || !free_top || (P > 1 && !moves) ||
+      !move_count || !status)
+    return SMCSD_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kv_compact_ws_bytes(P))
+    return SMCSD_EWORKSPACE;
+  return hip_rc(launch_kv_compact(block_tables, S, M_cap, block_size, refcounts, free_list,
+                                  free_top, P, moves, move_count, status,
+                                  static_cast<char *>(workspace), as_stream(stream)));
+}
+
+int smcsd_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int segments,
+                  int64_t segment_stride, int64_t token_bytes, int block_size,
+                  const int32_t *list, const int32_t *count, int64_t capacity, int64_t P,
+                  int32_t *status, void *stream) {
+  if (n_caches < 0 || n_caches > SMCSD_KV_COPY_MAX_CACHES || segments < 1 || token_bytes < 1 ||
+      block_size < 1 || token_bytes > INT32_MAX || block_size * token_bytes > INT32_MAX ||
+      block_stride < 0 || segment_stride < 0 || P < 1 || P > INT32_MAX || capacity < 0 ||
+      capacity > INT32_MAX)
+    return SMCSD_EINVAL;
+  if (n_caches == 0 || capacity == 0) return SMCSD_OK;
+  if (!caches || !list || !count || !status) return SMCSD_EINVAL;
+  for (int i = 0; i < n_caches; ++i)
+    if (!caches[i]) return SMCSD_EINVAL;
+  return hip_rc(launch_kv_copy(caches, n_caches, block_stride, segments, segment_stride,
+                               token_bytes, block_size, list, count, capacity, P, status,
+                               as_stream(stream)));
+}
+
+// Host checks of a paged cache of 16-bit elements.
+static bool paged_ok(const void *k, const void *v, int64_t page, int64_t token, int64_t head,
+                     const int32_t *tables, int M_cap, int block_size, int64_t P, int D) {
+  return k && v && aligned(k, 16) && aligned(v, 16) && page >= D && token >= D && head >= D &&
+         page % 8 == 0 && token % 8 == 0 && head % 8 == 0 && tables && M_cap >= 1 &&
+         block_size >= 1 && (int64_t)M_cap * block_size < INT32_MAX - 4096 && P >= 1 && P <= INT32_MAX;
+}
+
+int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, int S, int R, int Hq, int Hkv, int D,
+                       const void *q_weight, const void *k_weight, float eps,
+                       const float *cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                       const int32_t *positions, const int32_t *ctx_lens,
+                       const int32_t *num_nodes, const int32_t *block_tables, int M_cap,
+                       int block_size, int64_t P, void *k_cache, void *v_cache,
+                       int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                       void *q_out, int32_t *status, void *stream) {
+  if (dtype != SMCSD_DTYPE_BF16 && dtype != SMCSD_DTYPE_F16) return SMCSD_EDTYPE;
+  if (S < 0 || R < 1 || Hq < 1 || Hkv < 1 || Hq > INT32_MAX / 4 || Hkv > INT32_MAX / 8 || D < 8 ||
+      D > kMaxHeadDim || D % 8 || rot_dim < 0 || rot_dim > D || rot_dim % 16 || max_pos < 0 ||
+      !(eps >= 0.0f) || !std::isfinite(eps))
+    return SMCSD_EINVAL;
+  if (S == 0) return SMCSD_OK;
+  if ((int64_t)S * R >= INT32_MAX || (int64_t)S * R * (Hq + 2 * Hkv) >= INT32_MAX ||
+      (int64_t)S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D ||
+      q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return SMCSD_EINVAL;
+  if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+      !aligned(cos_sin, 16) || (rot_dim > 0 && !cos_sin) || !ctx_lens || !status)
+    return SMCSD_EINVAL;
+  if (!paged_ok(k_cache, v_cache, page_stride, token_stride, head_stride, block_tables, M_cap,
+                block_size, P, D))
+    return SMCSD_EINVAL;
+  QkNormRopeArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.S = S;
+  a.R = R;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.q_weight = static_cast<const uint16_t *>(q_weight);
+  a.k_weight = static_cast<const uint16_t *>(k_weight);
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  a.positions = positions;
+  a.ctx_lens = ctx_lens;
+  a.num_nodes = num_nodes;
+  a.cache = PagedCache{page_stride, token_stride, head_stride, block_tables, M_cap, block_size, P};
+  a.k_cache = static_cast<uint16_t *>(k_cache);
+  a.v_cache = static_cast<uint16_t *>(v_cache);
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.status = status;
+  return hip_rc(launch_qk_norm_rope(a, dtype, as_stream(stream)));
+}
+
+int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                         const void *v_cache, int64_t page_stride, int64_t token_stride,
+                         int64_t head_stride, const int32_t *block_tables, int M_cap,
+                         int block_size, int64_t P, const int32_t *ctx_lens,
+                         const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N, int R,
+                         int Hq, int Hkv, int D, float scale, int64_t max_len, void *out,
+                         float *lse, int32_t *status, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+  if (dtype != SMCSD_DTYPE_BF16 && dtype != SMCSD_DTYPE_F16) return SMCSD_EDTYPE;
+  if (B < 0 || N < 0 || R < 1 || R > kMaxNodes || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 8 ||
+      D > kMaxHeadDim || D % 8 || !std::isfinite(scale) || max_len < 0)
+    return SMCSD_EINVAL;
+  const int64_t S = (int64_t)B * N;
+  if (S == 0) return SMCSD_OK;
+  if (S >= INT32_MAX || S * R >= INT32_MAX || S * R * Hq >= INT32_MAX || (int64_t)Hq * D >= INT32_MAX ||
+      S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 || !q || !aligned(q, 16) || !out ||
+      !aligned(out, 16) || !ctx_lens || !status || !aligned(tree_mask, 8))
+    return SMCSD_EINVAL;
+  if (!paged_ok(k_cache, v_cache, page_stride, token_stride, head_stride, block_tables, M_cap,
+                block_size, P, D))
+    return SMCSD_EINVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < tree_attn_ws_bytes(S, R, (int64_t)Hq * D, Hkv))
+    return SMCSD_EWORKSPACE;
+  TreeAttnArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k_cache = static_cast<const uint16_t *>(k_cache);
+  a.v_cache = static_cast<const uint16_t *>(v_cache);
+  a.q_stride = q_stride;
+  a.cache = PagedCache{page_stride, token_stride, head_stride, block_tables, M_cap, block_size, P};
+  a.ctx_lens = ctx_lens;
+  a.num_nodes = num_nodes;
+  a.tree_mask = tree_mask;
+  a.B = B;
+  a.N = N;
+  a.R = R;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.scale = scale;
+  a.max_len = max_len;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = status;
+  a.ws = static_cast<char *>(workspace);
+  return hip_rc(launch_tree_attn(a, dtype, as_stream(stream)));
+}
+
+int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n, int V,
+                         float temperature, const int32_t *tokens, int C, int k,
+                         float *out_logp, float *out_entropy, float *out_lse, int32_t *top_ids,
+                         float *top_logp, int32_t *status, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  if (dtype != SMCSD_DTYPE_F32 && dtype != SMCSD_DTYPE_BF16) return SMCSD_EDTYPE;
+  if (n < 0 || V < 1 || V > kMaxV || row_stride < V || C < 0 || C > kMaxGiven || k < 0 ||
+      k > kMaxTop || k > V)
+    return SMCSD_EINVAL;
+  if (!(temperature > 0.0f) || !std::isfinite(temperature)) return SMCSD_EINVAL;
+  if (n == 0) return SMCSD_OK;
+  const size_t esz = dtype == SMCSD_DTYPE_BF16 ? 2 : 4;
+  if (!logits || !aligned(logits, esz) || !status || (C > 0 && out_logp && !tokens))
+    return SMCSD_EINVAL;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < logprobs_ws_bytes(n, k, V))
+    return SMCSD_EWORKSPACE;
+  LogprobsArgs a{};
+  a.logits = static_cast<const char *>(logits);
+  a.row_bytes = row_stride * (int64_t)esz;
+  a.n = n;
+  a.V = V;
+  a.c = (float)(1.4426950408889634073599246810018921 / (double)temperature);
+  a.T = temperature;
+  a.tokens = tokens;
+  a.C = C;
+  a.k = k;
+  a.logp = out_logp;
+  a.entropy = out_entropy;
+  a.lse = out_lse;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.status = status;
+  a.ws = static_cast<char *>(workspace);
+  return hip_rc(launch_logprobs(a, dtype, as_stream(stream)));
 }
 
 int smcsd_stream_read(const void *p, int64_t bytes, uint32_t *tile_xor, void *stream) {

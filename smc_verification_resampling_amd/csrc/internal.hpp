@@ -151,6 +151,87 @@ hipError_t launch_kv_check(const int32_t *T, int64_t S, int M_cap, int slots,
                            int64_t P, int32_t *viol, int32_t *status, char *ws,
                            hipStream_t stream);
 
+// The pages' own operations (kvpages.hip).
+size_t kv_free_ws_bytes(int64_t P);
+size_t kv_compact_ws_bytes(int64_t P);
+hipError_t launch_kv_fork(const int32_t *forked, int B, int N, int32_t *T, int M, int32_t *rc, int64_t P,
+                          int32_t *status, hipStream_t stream);
+hipError_t launch_kv_free(const int32_t *freed, int64_t S, int32_t *T, int M, int32_t *rc, int32_t *fl,
+                          int32_t *free_top, int64_t P, int32_t *status, char *ws, hipStream_t stream);
+hipError_t launch_kv_compact(int32_t *T, int64_t S, int M, int block_size, int32_t *rc, int32_t *fl,
+                             int32_t *free_top, int64_t P, int32_t *moves, int32_t *move_count,
+                             int32_t *status, char *ws, hipStream_t stream);
+hipError_t launch_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int segments,
+                          int64_t segment_stride, int64_t token_bytes, int block_size, const int32_t *list,
+                          const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
+                          hipStream_t stream);
+
+// A paged cache of 16-bit elements: element d of head h of token t of block b lies at
+// b * page + t * token + h * head + d (element units).
+struct PagedCache {
+  int64_t page, token, head;
+  const int32_t *tables;
+  int M_cap, block_size;
+  int64_t P;
+};
+
+// Norms, rotation and the write into the pages (qknorm.hip).
+struct QkNormRopeArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int S, R, Hq, Hkv, D;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float *cos_sin;
+  int64_t max_pos;
+  int rot_dim, interleaved;
+  const int32_t *positions, *ctx_lens, *num_nodes;
+  PagedCache cache;
+  uint16_t *k_cache, *v_cache, *q_out;
+  int32_t *status;
+};
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a, int dtype, hipStream_t stream);
+
+// Attention over the pages (treeattn.hip).
+constexpr int kMaxNodes = 64;
+constexpr int kMaxHeadDim = 256;
+struct TreeAttnArgs {
+  const uint16_t *q, *k_cache, *v_cache;
+  int64_t q_stride;
+  PagedCache cache;
+  const int32_t *ctx_lens, *num_nodes;
+  const uint64_t *tree_mask;
+  int B, N, R, Hq, Hkv, D;
+  float scale;
+  int64_t max_len;
+  uint16_t *out;
+  float *lse;
+  int32_t *status;
+  char *ws;
+};
+size_t tree_attn_ws_bytes(int64_t S, int R, int64_t HqD, int64_t Hkv);
+hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream);
+
+// Log-probabilities, entropy and alternatives (logprobs.hip).
+constexpr int kMaxTop = 64;
+constexpr int kMaxGiven = 1024;
+struct LogprobsArgs {
+  const char *logits;
+  int64_t row_bytes;
+  int n, V;
+  float c;     // log2(e) / T, rounded once on the host
+  double T;
+  const int32_t *tokens;
+  int C, k;
+  float *logp, *entropy, *lse;
+  int32_t *top_ids;
+  float *top_logp;
+  int32_t *status;
+  char *ws;
+};
+size_t logprobs_ws_bytes(int64_t n, int k, int V);
+hipError_t launch_logprobs(const LogprobsArgs &a, int dtype, hipStream_t stream);
+
 hipError_t launch_stream_read(const void *p, int64_t bytes, uint32_t *tile_xor,
                               hipStream_t stream);
 hipError_t launch_philox(const uint32_t *ctr, const uint32_t *key, int n, uint32_t *out,
