@@ -64,7 +64,7 @@ size_t smcsd_workspace_bytes(int op, int B, int N, int K, int V, int64_t P) {
     if (K < 1 || K > kMaxNodes || V < 1 || P < 1 || V % P || S > INT32_MAX || S * K > INT32_MAX ||
         S * K > INT64_MAX / 64 / V)
       return 0;
-    return tree_attn_ws_bytes(S, K, V, P);
+    return tree_attn_ws_bytes(B, N, K, V, P);
   }
   if (op == SMCSD_OP_LOGPROBS) {
     if (V < 1 || V > kMaxV || K < 0 || K > kMaxTop || K > V || S > INT32_MAX) return 0;
@@ -534,7 +534,7 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
     return SMCSD_EINVAL;
   const int64_t S = (int64_t)B * N;
   if (S == 0) return SMCSD_OK;
-  if (S >= INT32_MAX || S * R >= INT32_MAX || S * R * Hq >= INT32_MAX || (int64_t)Hq * D >= INT32_MAX ||
+  if (S >= INT32_MAX || S * R >= INT32_MAX || S * R * Hq > kMaxAttnRows || (int64_t)Hq * D >= INT32_MAX ||
       S * M_cap >= INT32_MAX)
     return SMCSD_EINVAL;
   if (q_stride < (int64_t)Hq * D || q_stride % 8 || !q || !aligned(q, 16) || !out ||
@@ -544,7 +544,7 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
                 block_size, P, D))
     return SMCSD_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < tree_attn_ws_bytes(S, R, (int64_t)Hq * D, Hkv))
+      workspace_bytes < tree_attn_ws_bytes(B, N, R, (int64_t)Hq * D, Hkv))
     return SMCSD_EWORKSPACE;
   TreeAttnArgs a{};
   a.q = static_cast<const uint16_t *>(q);

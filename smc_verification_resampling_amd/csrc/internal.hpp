@@ -195,6 +195,7 @@ hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a, int dtype, hipStream_t s
 // Attention over the pages (treeattn.hip).
 constexpr int kMaxNodes = 64;
 constexpr int kMaxHeadDim = 256;
+constexpr int64_t kMaxAttnRows = 1 << 25;  // a wave takes at least one row: 2^31 threads
 struct TreeAttnArgs {
   const uint16_t *q, *k_cache, *v_cache;
   int64_t q_stride;
@@ -209,7 +210,7 @@ struct TreeAttnArgs {
   int32_t *status;
   char *ws;
 };
-size_t tree_attn_ws_bytes(int64_t S, int R, int64_t HqD, int64_t Hkv);
+size_t tree_attn_ws_bytes(int64_t B, int64_t N, int R, int64_t HqD, int64_t Hkv);
 hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream);
 
 // Log-probabilities, entropy and alternatives (logprobs.hip).

@@ -1,4 +1,23 @@
 // treeattn.hip - attention of drafted trees over the paged cache (gfx950).
+//
+// The query rows of one key/value head - R nodes x Hq/Hkv heads of a sequence, or those of
+// all N particles of a prompt over the blocks that their tables share - go through the keys
+// together, 32 rows to a wave.  Scores are formed transposed, S^T = K Q^T, with
+// mfma 32x32x16: a lane then holds one query row and 16 of a step's 32 keys, so that the
+// running maximum and sum need one exchange between the wave's halves, and its 16
+// probabilities, rounded to 16 bits, are at once the second operand of O^T = V^T P^T: that
+// product's order of keys is free, so the first operand takes the same order, four keys at
+// a time, with the transposing LDS read.  Probabilities never leave the registers, and the
+// rescaling of O is one factor per lane.
+// Keys and values go through LDS in tiles of 32 or 64 tokens, shared by a workgroup's
+// waves: the next tile's loads are in flight, in registers, while the present one is
+// computed, and the block ids of the tile after it are fetched meanwhile.  Rows of a tile
+// are stored with their 16-byte chunks permuted by the row number, so that reads of one
+// chunk over many rows fall on different banks.
+// Long contexts are split over workgroups (each a range of keys of equal length) and the
+// parts (m, l, O) joined in fp32.
+#include <cmath>
+
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "half.hpp"
@@ -8,111 +27,590 @@ namespace smcsd {
 
 namespace {
 
-constexpr int kAttnBlock = 256;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// The nodes that node i of sequence s sees, as bits.
-__device__ __forceinline__ uint64_t node_bits(const TreeAttnArgs &a, int s, int i, int nodes) {
-  const uint64_t all = nodes >= 64 ? ~0ull : (1ull << nodes) - 1;
-  const uint64_t m = a.tree_mask ? a.tree_mask[(int64_t)s * a.R + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-  return m & all;
+template <int DT> struct Mma;
+template <> struct Mma<SMCSD_DTYPE_BF16> {
+  typedef Half<SMCSD_DTYPE_BF16>::V8 V8;
+  __device__ __forceinline__ static f32x16 run(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Mma<SMCSD_DTYPE_F16> {
+  typedef Half<SMCSD_DTYPE_F16>::V8 V8;
+  __device__ __forceinline__ static f32x16 run(V8 a, V8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// ---------------------------------------------------------------------------------
+// Launch plan
+// ---------------------------------------------------------------------------------
+constexpr int kRowsWave = 32;
+constexpr int kPartItems = 1024;  // workgroups that the splits of a launch aim at
+constexpr int kMinShared = 128;   // shorter shared prefixes are read per particle
+
+// How the rows of one key/value head and the keys are cut: `tiles` workgroups of `waves`
+// waves over the rows, `splits` over the keys.
+struct Cut {
+  int rows, tiles, tile_rows, waves, splits;
+};
+inline int pad_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+inline int max_splits(int64_t heads) { return (int)ceil_div(kPartItems, std::max<int64_t>(heads, 1)); }
+inline Cut cut_of(int rows, int64_t heads, int64_t max_len, int DP) {
+  Cut c;
+  c.rows = rows;
+  const int most = (DP == 256 ? 4 : 8) * kRowsWave;
+  c.tiles = (int)ceil_div(rows, most);
+  c.tile_rows = (int)ceil_div(rows, c.tiles);
+  c.waves = (int)ceil_div(c.tile_rows, kRowsWave);
+  // enough workgroups to fill the chip, but a split's keys outweigh the part it leaves
+  const int64_t most_splits = ceil_div(max_len, std::max(256, 4 * std::min(rows, most)));
+  c.splits = (int)std::max<int64_t>(
+      1, std::min<int64_t>(max_splits(heads) / std::min(c.waves * c.tiles, 4), most_splits));
+  return c;
 }
 
-// One wave per query row (sequence, node, head): 64 tokens at a time, one per lane for the
-// scores, then D elements over the lanes for the values.
-template <int DT>
-__global__ __launch_bounds__(kAttnBlock) void k_attn_row(TreeAttnArgs a, int64_t rows) {
-  typedef typename Half<DT>::T T;
-  __shared__ float sq[kAttnBlock / kWave][256];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  for (int64_t r0 = (int64_t)blockIdx.x * (kAttnBlock / kWave); r0 < rows;
-       r0 += (int64_t)gridDim.x * (kAttnBlock / kWave)) {
-    const int64_t r = r0 + wave;
-    if (r >= rows) continue;
-    const int64_t t = r / a.Hq;
-    const int hq = (int)(r - t * a.Hq), s = (int)(t / a.R), i = (int)(t - (int64_t)s * a.R);
-    const int hk = hq / (a.Hq / a.Hkv);
-    int nodes = a.R;
-    bool bad = false;
-    if (a.num_nodes) {
-      nodes = a.num_nodes[s];
-      bad = nodes < 0 || nodes > a.R;
-      nodes = max(0, min(nodes, a.R));
-    }
-    int64_t ctx = a.ctx_lens[s];
-    const bool none = ctx < 0 || ctx + nodes > (int64_t)a.cache.M_cap * a.cache.block_size;
-    if (none) ctx = 0;
-    if (lane == 0 && (none || bad)) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-    if (i >= nodes) continue;
-    const uint64_t bits = node_bits(a, s, i, nodes);
-    const int len = none ? 0 : (int)ctx + nodes;
-    const T *q = reinterpret_cast<const T *>(a.q) + t * a.q_stride + (int64_t)hq * a.D;
-    for (int d = lane; d < a.D; d += kWave) sq[wave][d] = (float)q[d];
-    __builtin_amdgcn_wave_barrier();
-    float m = kNegInf, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p0 = 0; p0 < len; p0 += kWave) {
-      const int p = p0 + lane;
-      bool see = p < len && (p < ctx || ((bits >> (p - ctx)) & 1));
-      int64_t off = 0;
-      if (see) {
-        const int32_t page = a.cache.tables[(int64_t)s * a.cache.M_cap + p / a.cache.block_size];
-        see = page >= 0 && page < a.cache.P;
-        if (!see) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-        off = page * a.cache.page + (p % a.cache.block_size) * a.cache.token + hk * a.cache.head;
-      }
-      float z = kNegInf;
-      if (see) {
-        const uint16_t *k = a.k_cache + off;
-        float sum = 0.0f;
-        for (int d = 0; d < a.D; d += 8) {
-          const f32x8 x = widen8<DT>(*reinterpret_cast<const uint4 *>(k + d));
-#pragma unroll
-          for (int c = 0; c < 8; ++c) sum = fmaf(x[c], sq[wave][d + c], sum);
-        }
-        z = sum * a.scale;
-      }
-      float top = z;
-#pragma unroll
-      for (int x = 1; x < kWave; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
-      const float mn = fmaxf(m, top);
-      if (mn == kNegInf && !__any(see)) continue;
-      const float f = m == kNegInf ? 0.0f : expf(m - mn);
-      const float pr = see ? expf(z - mn) : 0.0f;
-      m = mn;
-      l = l * f + wave_sum_f32(pr);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] *= f;
-      const uint64_t seen = __ballot(see);
-      for (int x = 0; x < kWave; ++x) {
-        if (!((seen >> x) & 1)) continue;
-        const float w = __shfl(pr, x, kWave);
-        const int64_t o = __shfl((long long)off, x, kWave);
-        const T *v = reinterpret_cast<const T *>(a.v_cache) + o;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (lane + c * kWave < a.D) acc[c] = fmaf(w, (float)v[lane + c * kWave], acc[c]);
-      }
-    }
-    T *out = reinterpret_cast<T *>(a.out) + r * a.D;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (lane + c * kWave < a.D) out[lane + c * kWave] = (T)(l == 0.0f ? 0.0f : acc[c] / l);
-    if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? kNegInf : m + logf(l);
+// n / d for 0 <= n < 2^31: the high half of n * ceil(2^(31+s) / d), s = ceil(log2 d),
+// shifted by s - 1 (exact: the error n * (M*d - 2^(31+s)) < 2^31 * 2^s).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  if (d < 2) return f;
+  int s = 0;
+  while ((1ull << s) < d) ++s;
+  f.mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  f.shift = s - 1;
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(const FastDiv &f, uint32_t n) {
+  return f.d < 2 ? n : __umulhi(n, f.mul) >> f.shift;
+}
+
+struct Plan {
+  FastDiv page;
+  Cut prefix, suffix;          // prefix.splits = 0: no shared-prefix pass
+  const int32_t *shared_len;   // [B] (null: none shared)
+  float *ml;                   // [parts][rows of out] (max, sum) pairs; prefix parts first
+  float *acc;                  // [parts][rows of out][D]
+  float c;                     // |scale| * log2(e)
+  int negate;                  // a negative scale turns the queries' signs
+};
+
+// What a sequence's arrays say, within bounds: `none` if it sees nothing at all.
+struct Seq {
+  int ctx, nodes;
+  bool none, bad;
+};
+__device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int s) {
+  Seq q;
+  q.nodes = a.R;
+  q.bad = false;
+  if (a.num_nodes) {
+    const int n = a.num_nodes[s];
+    q.bad = n < 0 || n > a.R;
+    q.nodes = max(0, min(n, a.R));
   }
+  const int c = a.ctx_lens[s];
+  q.none = c < 0 || (int64_t)c + q.nodes > (int64_t)a.cache.M_cap * a.cache.block_size;
+  q.bad |= q.none;
+  q.ctx = q.none ? 0 : c;
+  return q;
+}
+
+// ---------------------------------------------------------------------------------
+// Shared prefix: per prompt, the length in whole blocks that all N tables name alike and
+// that every particle has as context.
+// ---------------------------------------------------------------------------------
+constexpr int kShareBlock = 512;
+
+__global__ __launch_bounds__(kShareBlock) void k_shared_len(TreeAttnArgs a, int32_t *__restrict__ out) {
+  __shared__ int s_first, s_ctx;
+  const int tid = threadIdx.x;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    __syncthreads();
+    if (tid == 0) {
+      s_first = INT32_MAX;
+      s_ctx = INT32_MAX;
+    }
+    __syncthreads();
+    int least = INT32_MAX;
+    for (int n = tid; n < a.N; n += kShareBlock) least = min(least, seq_of(a, b * a.N + n).ctx);
+    if (least != INT32_MAX) atomicMin(&s_ctx, least);
+    __syncthreads();
+    const int slots = s_ctx / a.cache.block_size;
+    const int32_t *T = a.cache.tables + (int64_t)b * a.N * a.cache.M_cap;
+    int done = slots;
+    for (int c0 = 0; c0 < slots; c0 += kShareBlock) {
+      const int c = c0 + tid;
+      if (c < slots) {
+        const int32_t id = T[c];
+        bool same = id >= 0 && id < a.cache.P;
+#pragma unroll 8
+        for (int n = 1; n < a.N; ++n) same &= T[(int64_t)n * a.cache.M_cap + c] == id;
+        if (!same) atomicMin(&s_first, c);
+      }
+      __syncthreads();
+      if (s_first != INT32_MAX) {
+        done = s_first;
+        break;
+      }
+    }
+    if (tid == 0) {
+      const int len = done * a.cache.block_size;
+      out[b] = len >= kMinShared ? len : 0;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// The main kernel
+// ---------------------------------------------------------------------------------
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, kWave); }
+
+// DP: head size padded to 64, 128 or 256.  KT: keys of a tile.  NB: LDS buffers.  CPT:
+// 16-byte chunks of a tile (keys and values) that a thread moves, at the fewest waves.
+template <int DT, int DP, int KT, int NB, int CPT, int MAXW, bool PREFIX>
+__global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
+  typedef typename Half<DT>::V8 V8;
+  typedef typename Half<DT>::V4 V4;
+  constexpr int CH = DP / 8;       // chunks of a row
+  constexpr int RB = DP * 2;       // bytes of a row
+  constexpr int NS = DP / 16;      // product steps of a score
+  constexpr int NA = DP / 32;      // accumulator tiles of an output row
+  constexpr int PAIRS = CPT / 2;
+  constexpr int SW = CH < 16 ? CH - 1 : 15;
+  __shared__ __attribute__((aligned(16))) char sK[NB][KT * RB];
+  __shared__ __attribute__((aligned(16))) char sV[NB][KT * RB];
+  __shared__ uint32_t sOk[NB][KT];  // a key's tile row may be read; bit 1: its values are not all finite
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int nt = blockDim.x;
+  const int hw = lane / 32, col = lane % 32;
+  const Cut &cut = PREFIX ? p.prefix : p.suffix;
+
+  // item: key/value head fastest (a page's heads lie together), then row tile, split, and
+  // sequence (or prompt)
+  int64_t it = blockIdx.x;
+  const int hk = (int)(it % a.Hkv);
+  it /= a.Hkv;
+  const int tile = (int)(it % cut.tiles);
+  it /= cut.tiles;
+  const int split = (int)(it % cut.splits);
+  const int unit = (int)(it / cut.splits);
+  const int s0 = PREFIX ? unit * a.N : unit;
+  const int G = a.Hq / a.Hkv;
+
+  Seq sq{0, 0, false, false};
+  int lo = 0, hi, ctx;
+  if (PREFIX) {
+    hi = p.shared_len[unit];
+    ctx = INT32_MAX;
+    if (hi == 0) return;
+  } else {
+    sq = seq_of(a, s0);
+    if (sq.bad && tid == 0 && hk == 0 && tile == 0 && split == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+    if (sq.nodes == 0) return;
+    ctx = sq.ctx;
+    hi = sq.none ? 0 : ctx + sq.nodes;
+    lo = p.shared_len ? min(hi, p.shared_len[s0 / a.N]) : 0;
+  }
+  // this split's keys: an equal share in whole tiles
+  const int per = (hi - lo + cut.splits - 1) / cut.splits;
+  const int64_t share = (int64_t)((per + KT - 1) / KT) * KT;
+  const int k0 = (int)min((int64_t)hi, lo + split * share), k1 = (int)min((int64_t)hi, k0 + share);
+
+  // this lane's query row
+  const int r = tile * cut.tile_rows + wave * kRowsWave + col;
+  const bool row_in = wave * kRowsWave + col < cut.tile_rows && r < cut.rows;
+  int n = 0, j = 0, g = 0;
+  if (row_in) {
+    n = PREFIX ? r / (a.R * G) : 0;
+    const int rest = r - n * a.R * G;
+    j = rest / G;
+    g = rest - j * G;
+  }
+  const int s = s0 + n;
+  const int64_t orow = ((int64_t)s * a.R + j) * a.Hq + hk * G + g;  // row of out
+  const bool live = row_in && (PREFIX || j < sq.nodes);
+  uint64_t bits = 0;
+  if (!PREFIX && live) {
+    bits = a.tree_mask ? a.tree_mask[(int64_t)s * a.R + j] : (j >= 63 ? ~0ull : (2ull << j) - 1);
+    if (sq.nodes < 64) bits &= (1ull << sq.nodes) - 1;
+  }
+  V8 q[NS];
+  {
+    const uint16_t *qp = a.q + ((int64_t)s * a.R + j) * a.q_stride + (int64_t)(hk * G + g) * a.D;
+    const uint32_t flip = p.negate ? 0x80008000u : 0u;
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      const int d = 16 * st + 8 * hw;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (live && d < a.D) w = *reinterpret_cast<const uint4 *>(qp + d);
+      w.x ^= flip;
+      w.y ^= flip;
+      w.z ^= flip;
+      w.w ^= flip;
+      q[st] = __builtin_bit_cast(V8, w);
+    }
+  }
+  f32x16 o[NA];
+#pragma unroll
+  for (int t = 0; t < NA; ++t) o[t] = f32x16{};
+  float m = kNegInf, l = 0.0f;
+
+  // staging: chunk `tid % CH` of rows `tid / CH + i * nt / CH`
+  const int chunk = tid % CH, row0 = tid / CH, rstep = nt / CH;
+  const bool chunk_in = chunk * 8 < a.D;
+  const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
+  const int64_t head_off = (int64_t)hk * a.cache.head + chunk * 8;
+  int32_t pg[PAIRS];
+  uint32_t okbits = 0;  // of the tile in flight: which of this thread's rows may be read
+  uint4 kr[PAIRS], vr[PAIRS];
+  auto fetch_pages = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int row = row0 + i * rstep, pos = base + row;
+      pg[i] = row < KT && pos < k1 ? table[div_by(p.page, pos)] : -1;
+    }
+  };
+  auto fetch_tile = [&](int base) {
+    okbits = 0;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int row = row0 + i * rstep, pos = base + row;
+      const bool ok = pg[i] >= 0 && pg[i] < a.cache.P;
+      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+      if (ok && chunk_in) {
+        const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
+        const int64_t off = pg[i] * a.cache.page + in * a.cache.token + head_off;
+        kr[i] = *reinterpret_cast<const uint4 *>(a.k_cache + off);
+        vr[i] = *reinterpret_cast<const uint4 *>(a.v_cache + off);
+      }
+      if (!ok && row < KT && pos < k1 && chunk == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+      okbits |= (uint32_t)ok << i;
+    }
+  };
+  // Values that are not finite are stored as 0: a probability of 0 then takes nothing from
+  // them, and the rows that do see them get them afterwards (below).
+  constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
+  auto finite = [&](uint32_t &w) {
+    bool bad = false;
+    if ((w & kExp) == kExp) {
+      w &= 0xFFFF0000u;
+      bad = true;
+    }
+    if (((w >> 16) & kExp) == kExp) {
+      w &= 0xFFFFu;
+      bad = true;
+    }
+    return bad;
+  };
+  auto store_tile = [&](int buf, int base) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int row = row0 + i * rstep;
+      if (row < KT) {
+        const int at = row * RB + ((chunk ^ (row & SW)) * 16);
+        uint4 v = vr[i];
+        if (chunk == 0) sOk[buf][row] = (okbits >> i) & 1;
+        *reinterpret_cast<uint4 *>(&sK[buf][at]) = kr[i];
+        if (base + KT > ctx) {  // only new tokens can be hidden from some rows
+          const bool b0 = finite(v.x), b1 = finite(v.y), b2 = finite(v.z), b3 = finite(v.w);
+          if (b0 || b1 || b2 || b3) atomicOr(&sOk[buf][row], 2);
+        }
+        *reinterpret_cast<uint4 *>(&sV[buf][at]) = v;
+      }
+    }
+  };
+
+  auto step = [&](int buf, int sub, int base) {
+    const char *K = sK[buf] + sub * 32 * RB;
+    const char *V = sV[buf] + sub * 32 * RB;
+    f32x16 z = f32x16{};
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      const V8 kf = *reinterpret_cast<const V8 *>(K + col * RB + (((2 * st + hw) ^ (col & SW)) * 16));
+      z = Mma<DT>::run(kf, q[st], z);
+    }
+    const uint32_t okw = sOk[buf][sub * 32 + col];
+    const uint32_t ok = (uint32_t)__ballot(okw & 1);
+    uint32_t see = 0xFFFFFFFFu;
+    if (ok != 0xFFFFFFFFu || base + 32 > ctx) {
+      const int nb = ctx - base;  // keys of this step that are context
+      see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
+      if (nb < 32) see |= nb >= 0 ? (uint32_t)(bits << nb) : (nb > -64 ? (uint32_t)(bits >> -nb) : 0u);
+      see &= ok;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!((see >> (8 * (i / 4) + 4 * hw + i % 4)) & 1)) z[i] = kNegInf;
+    }
+    float top = z[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
+    top = fmaxf(top, other_half(top)) * p.c;
+    if (__any(top > m)) {
+      const float mn = fmaxf(m, top);
+      const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] *= f;
+    }
+    const float ms = m == kNegInf ? 0.0f : m;
+    f32x8 e0, e1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e0[i] = fast_exp2(fmaf(z[i], p.c, -ms));
+      e1[i] = fast_exp2(fmaf(z[i + 8], p.c, -ms));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l += e0[i] + e1[i];
+    const V8 p0 = __builtin_convertvector(e0, V8), p1 = __builtin_convertvector(e1, V8);
+    // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
+    const int i16 = lane % 16, dh = (lane / 16) & 1;
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+#pragma unroll
+    for (int t = 0; t < NA; ++t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s16x4 v[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = 16 * h + 8 * x + 4 * hw + i16 / 4;
+          const int c = 4 * t + 2 * dh + (i16 % 4) / 2;
+          const char *at = V + key * RB + ((c ^ (key & SW)) * 16) + (i16 & 1) * 8;
+          v[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at);
+        }
+        struct Two { s16x4 a, b; } two{v[0], v[1]};
+        o[t] = Mma<DT>::run(__builtin_bit_cast(V8, two), h ? p1 : p0, o[t]);
+      }
+    }
+    if (!PREFIX) {
+      uint32_t odd = (uint32_t)__ballot((okw & 3) == 3);
+      while (odd) {  // a key whose values are not all finite: for the rows that see it
+        const int key = __builtin_ctz(odd);
+        odd &= odd - 1;
+        const int pos = base + key;
+        const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
+        const uint16_t *vp = a.v_cache + table[div_by(p.page, pos)] * a.cache.page +
+                             in * a.cache.token + (int64_t)hk * a.cache.head;
+        float w = 0.0f;  // this row's probability of the key, from the half that holds it
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (8 * (i / 4) + 4 * hw + i % 4 == key) w = i < 8 ? e0[i & 7] : e1[i & 7];
+        w += other_half(w);
+        if (!((see >> key) & 1)) continue;
+        for (int t = 0; t < NA; ++t)
+          for (int i = 0; i < 16; ++i) {
+            const int d = 32 * t + 8 * (i / 4) + 4 * hw + i % 4;
+            if (d >= a.D || (vp[d] & kExp) != kExp) continue;
+            o[t][i] += w * (float)__builtin_bit_cast(typename Half<DT>::T, vp[d]);
+          }
+      }
+    }
+  };
+
+  if (k0 < k1) {
+    fetch_pages(k0);
+    fetch_tile(k0);
+    fetch_pages(k0 + KT);
+    for (int base = k0, buf = 0; base < k1; base += KT, buf ^= NB - 1) {
+      if (NB == 1) __syncthreads();
+      store_tile(buf, base);
+      if (base + KT < k1) {
+        fetch_tile(base + KT);
+        fetch_pages(base + 2 * KT);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int sub = 0; sub < KT / 32; ++sub)
+        if (base + 32 * sub < k1) step(buf, sub, base + 32 * sub);
+    }
+  }
+  l += other_half(l);
+
+  // the row's part, or the row itself
+  const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
+  const int part = PREFIX ? split : p.prefix.splits + split;
+  if (PREFIX || cut.splits > 1) {
+    if (!live) return;
+    float *ml = p.ml + 2 * (part * rows + orow);
+    if (hw == 0) {
+      ml[0] = m;
+      ml[1] = l;
+    }
+    if (l == 0.0f) return;
+    float *acc = p.acc + (part * rows + orow) * a.D;
+#pragma unroll
+    for (int t = 0; t < NA; ++t)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int d = 32 * t + 8 * b + 4 * hw;
+        if (d < a.D)
+          *reinterpret_cast<float4 *>(acc + d) =
+              make_float4(o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]);
+      }
+    return;
+  }
+  if (!live) return;
+  if (p.prefix.splits > 0 && lo > 0) {  // the prompt's shared part of this row
+    for (int i = 0; i < p.prefix.splits; ++i) {
+      const float mp = p.ml[2 * (i * rows + orow)], lp = p.ml[2 * (i * rows + orow) + 1];
+      if (lp == 0.0f) continue;
+      const float mn = fmaxf(m, mp);
+      const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn), fp = mp == kNegInf ? 0.0f : fast_exp2(mp - mn);
+      const float *acc = p.acc + (i * rows + orow) * a.D;
+      m = mn;
+      l = l * f + lp * fp;
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int d = 32 * t + 8 * b + 4 * hw;
+          if (d >= a.D) continue;
+          const float4 x = *reinterpret_cast<const float4 *>(acc + d);
+          o[t][4 * b] = o[t][4 * b] * f + x.x * fp;
+          o[t][4 * b + 1] = o[t][4 * b + 1] * f + x.y * fp;
+          o[t][4 * b + 2] = o[t][4 * b + 2] * f + x.z * fp;
+          o[t][4 * b + 3] = o[t][4 * b + 3] * f + x.w * fp;
+        }
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t *out = a.out + orow * a.D;
+#pragma unroll
+  for (int t = 0; t < NA; ++t)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int d = 32 * t + 8 * b + 4 * hw;
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
+      const f32x4 x = {o[t][4 * b] * inv, o[t][4 * b + 1] * inv, o[t][4 * b + 2] * inv, o[t][4 * b + 3] * inv};
+      if (d < a.D)
+        *reinterpret_cast<uint2 *>(out + d) = __builtin_bit_cast(uint2, __builtin_convertvector(x, V4));
+    }
+  if (a.lse && hw == 0)
+    a.lse[orow] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
+}
+
+// ---------------------------------------------------------------------------------
+// The parts of a row joined: one wave per row of out.
+// ---------------------------------------------------------------------------------
+constexpr int kJoinBlock = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p, int64_t rows) {
+  typedef typename Half<DT>::V4 V4;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  const int lane = threadIdx.x % kWave;
+  for (int64_t r = (int64_t)blockIdx.x * (kJoinBlock / kWave) + threadIdx.x / kWave; r < rows;
+       r += (int64_t)gridDim.x * (kJoinBlock / kWave)) {
+    const int64_t t = r / a.Hq;
+    const int s = (int)(t / a.R), j = (int)(t - (int64_t)s * a.R);
+    const Seq sq = seq_of(a, s);
+    if (j >= sq.nodes) continue;
+    const int first = p.prefix.splits > 0 && p.shared_len[s / a.N] > 0 ? 0 : p.prefix.splits;
+    const int parts = p.prefix.splits + p.suffix.splits;
+    float m = kNegInf;
+    for (int i = first + lane; i < parts; i += kWave) {
+      const float *ml = p.ml + 2 * (i * rows + r);
+      if (ml[1] != 0.0f) m = fmaxf(m, ml[0]);
+    }
+    m = wave_max_f32(m);
+    float l = 0.0f;
+    f32x4 acc = {};
+    const int d = 4 * lane;
+    for (int i = first; i < parts; ++i) {
+      const float *ml = p.ml + 2 * (i * rows + r);
+      if (ml[1] == 0.0f) continue;
+      const float f = ml[0] == kNegInf ? 0.0f : fast_exp2(ml[0] - m);
+      l = fmaf(ml[1], f, l);
+      if (d < a.D) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(p.acc + (i * rows + r) * a.D + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = fmaf(x[c], f, acc[c]);
+      }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] *= inv;
+    if (d < a.D) *reinterpret_cast<uint2 *>(a.out + r * a.D + d) = __builtin_bit_cast(uint2, __builtin_convertvector(acc, V4));
+    if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
+  }
+}
+
+template <int DT, int DP, bool PREFIX>
+void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
+  const Cut &c = PREFIX ? p.prefix : p.suffix;
+  const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
+  const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
+  constexpr int CH = DP / 8;
+  if (c.waves == 1) {
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, 1, 2 * 32 * CH / kWave, 1, PREFIX>), grid, block, 0, stream, a, p);
+  } else if constexpr (DP == 256) {
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2 * 32 * CH / (2 * kWave), 4, PREFIX>), grid, block, 0, stream, a, p);
+  } else if (c.waves < 4) {
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2 * 32 * CH / (2 * kWave), 3, PREFIX>), grid, block, 0, stream, a, p);
+  } else {
+    hipLaunchKernelGGL((k_attn<DT, DP, 64, 2, 2 * 64 * CH / (4 * kWave), 8, PREFIX>), grid, block, 0, stream, a, p);
+  }
+}
+
+template <int DT, int DP>
+void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStream_t stream) {
+  const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
+  if (p.prefix.splits > 0) {
+    hipLaunchKernelGGL(k_shared_len, dim3(grid_blocks(a.B, kShareBlock)), dim3(kShareBlock), 0, stream, a, shared_len);
+    launch_part<DT, DP, true>(a, p, stream);
+  }
+  launch_part<DT, DP, false>(a, p, stream);
+  if (p.suffix.splits > 1)
+    hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(ceil_div(rows, kJoinBlock / kWave), kJoinBlock)),
+                       dim3(kJoinBlock), 0, stream, a, p, rows);
 }
 
 }  // namespace
 
-size_t tree_attn_ws_bytes(int64_t S, int R, int64_t HqD, int64_t Hkv) {
-  return align256(sizeof(float));
+// Workspace: [shared lengths int32 x B][(max, sum) x parts x rows][O fp32 x parts x rows x D], with
+// parts bounded by the splits that S*Hkv (B*Hkv) heads can ask for.  rows*2 <= rows*D / 4.
+size_t tree_attn_ws_bytes(int64_t B, int64_t N, int R, int64_t HqD, int64_t Hkv) {
+  const int64_t S = B * N;
+  const int ss = max_splits(S * Hkv), sp = N > 1 ? max_splits(B * Hkv) : 0;
+  const size_t floats = (size_t)((ss > 1 ? ss : 0) + sp) * (size_t)(S * R) * (size_t)HqD;
+  return align256(sizeof(int32_t) * (size_t)std::max<int64_t>(B, 1)) + align256(sizeof(float) * (floats / 4)) +
+         align256(sizeof(float) * floats);
 }
 
 hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream) {
-  const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
-  const dim3 grid(grid_blocks(ceil_div(rows, kAttnBlock / kWave), kAttnBlock)), block(kAttnBlock);
-  if (dtype == SMCSD_DTYPE_BF16)
-    hipLaunchKernelGGL(k_attn_row<SMCSD_DTYPE_BF16>, grid, block, 0, stream, a, rows);
-  else
-    hipLaunchKernelGGL(k_attn_row<SMCSD_DTYPE_F16>, grid, block, 0, stream, a, rows);
+  const int DP = pad_dim(a.D);
+  const int64_t S = (int64_t)a.B * a.N, cap = (int64_t)a.cache.M_cap * a.cache.block_size;
+  const int64_t longest = a.max_len > 0 ? std::min(a.max_len, cap) : cap;
+  const int G = a.Hq / a.Hkv;
+  Plan p{};
+  p.page = fast_div((uint32_t)a.cache.block_size);
+  p.suffix = cut_of(a.R * G, S * a.Hkv, longest, DP);
+  if (a.N > 1 && longest > kMinShared) p.prefix = cut_of(a.N * a.R * G, (int64_t)a.B * a.Hkv, longest, DP);
+  const int parts = p.prefix.splits + (p.suffix.splits > 1 ? p.suffix.splits : 0);
+  const int64_t rows = S * a.R * a.Hq;
+  int32_t *shared_len = reinterpret_cast<int32_t *>(a.ws);
+  char *at = a.ws + align256(sizeof(int32_t) * (size_t)a.B);
+  if (p.prefix.splits > 0) p.shared_len = shared_len;
+  p.ml = reinterpret_cast<float *>(at);
+  p.acc = reinterpret_cast<float *>(at + align256(sizeof(float) * 2 * (size_t)(parts * rows)));
+  p.c = std::max(std::fabs(a.scale) * 1.44269504088896340736f, 1e-30f);
+  p.negate = a.scale < 0.0f;
+  if (dtype == SMCSD_DTYPE_BF16) {
+    if (DP == 64) launch_dp<SMCSD_DTYPE_BF16, 64>(a, p, shared_len, stream);
+    else if (DP == 128) launch_dp<SMCSD_DTYPE_BF16, 128>(a, p, shared_len, stream);
+    else launch_dp<SMCSD_DTYPE_BF16, 256>(a, p, shared_len, stream);
+  } else {
+    if (DP == 64) launch_dp<SMCSD_DTYPE_F16, 64>(a, p, shared_len, stream);
+    else if (DP == 128) launch_dp<SMCSD_DTYPE_F16, 128>(a, p, shared_len, stream);
+    else launch_dp<SMCSD_DTYPE_F16, 256>(a, p, shared_len, stream);
+  }
   return hipGetLastError();
 }
 
