@@ -47,6 +47,7 @@ template <> struct Mma<SMCSD_DTYPE_F16> {
 // Launch plan
 // ---------------------------------------------------------------------------------
 constexpr int kRowsWave = 32;
+constexpr int kWavesMax = 4;      // two workgroups of four waves fill a compute unit's registers
 constexpr int kPartItems = 1024;  // workgroups that the splits of a launch aim at
 constexpr int kMinShared = 128;   // shorter shared prefixes are read per particle
 
@@ -57,13 +58,13 @@ struct Cut {
 };
 inline int pad_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 inline int max_splits(int64_t heads) { return (int)ceil_div(kPartItems, std::max<int64_t>(heads, 1)); }
-inline Cut cut_of(int rows, int64_t heads, int64_t max_len, int DP) {
+inline Cut cut_of(int rows, int64_t heads, int64_t max_len) {
   Cut c;
   c.rows = rows;
-  const int most = (DP == 256 ? 4 : 8) * kRowsWave;
+  const int most = kWavesMax * kRowsWave;
   c.tiles = (int)ceil_div(rows, most);
   c.tile_rows = (int)ceil_div(rows, c.tiles);
-  c.waves = (int)ceil_div(c.tile_rows, kRowsWave);
+  c.waves = c.tile_rows <= kRowsWave ? 1 : c.tile_rows <= 2 * kRowsWave ? 2 : kWavesMax;
   // enough workgroups to fill the chip, but a split's keys outweigh the part it leaves
   const int64_t most_splits = ceil_div(max_len, std::max(256, 4 * std::min(rows, most)));
   c.splits = (int)std::max<int64_t>(
@@ -168,37 +169,62 @@ __global__ __launch_bounds__(kShareBlock) void k_shared_len(TreeAttnArgs a, int3
 // ---------------------------------------------------------------------------------
 // The main kernel
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, kWave); }
+// The sum and the maximum of a lane and the lane 32 away.
+__device__ __forceinline__ float2 both_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const float2 h = both_halves(x);
+  return h.x + h.y;
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const float2 h = both_halves(x);
+  return fmaxf(h.x, h.y);
+}
 
-// DP: head size padded to 64, 128 or 256.  KT: keys of a tile.  NB: LDS buffers.  CPT:
-// 16-byte chunks of a tile (keys and values) that a thread moves, at the fewest waves.
-template <int DT, int DP, int KT, int NB, int CPT, int MAXW, bool PREFIX>
-__global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
+// A row's chunks are stored permuted: chunk c of row r in place c ^ place_of(r).  The row's
+// two low bits move the place furthest, since the transposing read takes two chunks of four
+// neighbouring rows, and any 16 rows (8 of 128 bytes) get different places, since a score
+// reads one chunk of every row.
+template <int CH>
+__device__ __forceinline__ int place_of(int r) {
+  return CH < 16 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
+}
+
+// A running maximum may fall behind by this much (a factor of 2^8) before O and l are
+// rescaled: probabilities up to 256 lose nothing in either type, and most steps then
+// rescale nothing.
+constexpr float kLag = 8.0f;
+
+// DP: head size padded to 64, 128 or 256.  KT: keys of a tile.  NB: LDS buffers.  NW: waves.
+template <int DT, int DP, int KT, int NB, int NW, bool PREFIX>
+__global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
-  constexpr int CH = DP / 8;       // chunks of a row
+  constexpr int CH = DP / 8;       // 16-byte chunks of a row
   constexpr int RB = DP * 2;       // bytes of a row
   constexpr int NS = DP / 16;      // product steps of a score
   constexpr int NA = DP / 32;      // accumulator tiles of an output row
-  constexpr int PAIRS = CPT / 2;
-  constexpr int SW = CH < 16 ? CH - 1 : 15;
-  __shared__ __attribute__((aligned(16))) char sK[NB][KT * RB];
-  __shared__ __attribute__((aligned(16))) char sV[NB][KT * RB];
-  __shared__ uint32_t sOk[NB][KT];  // a key's tile row may be read; bit 1: its values are not all finite
+  constexpr int TB = KT * RB;      // bytes of a tile
+  constexpr int RSTEP = NW * kWave / CH;     // rows that the workgroup moves at once
+  constexpr int PAIRS = KT / RSTEP;          // chunks of keys (and as many of values) of a thread
+  constexpr int SUBS = KT / 32;
+  __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
+  __shared__ uint32_t sOk[NB][KT];  // bit 0: the row may be read; bit 1: its values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int nt = blockDim.x;
   const int hw = lane / 32, col = lane % 32;
   const Cut &cut = PREFIX ? p.prefix : p.suffix;
 
   // item: key/value head fastest (a page's heads lie together), then row tile, split, and
   // sequence (or prompt)
-  int64_t it = blockIdx.x;
-  const int hk = (int)(it % a.Hkv);
-  it /= a.Hkv;
-  const int tile = (int)(it % cut.tiles);
-  it /= cut.tiles;
-  const int split = (int)(it % cut.splits);
-  const int unit = (int)(it / cut.splits);
+  uint32_t it = blockIdx.x;
+  const int hk = (int)(it % (uint32_t)a.Hkv);
+  it /= (uint32_t)a.Hkv;
+  const int tile = (int)(it % (uint32_t)cut.tiles);
+  it /= (uint32_t)cut.tiles;
+  const int split = (int)(it % (uint32_t)cut.splits);
+  const int unit = (int)(it / (uint32_t)cut.splits);
   const int s0 = PREFIX ? unit * a.N : unit;
   const int G = a.Hq / a.Hkv;
 
@@ -220,6 +246,41 @@ __global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
   const int per = (hi - lo + cut.splits - 1) / cut.splits;
   const int64_t share = (int64_t)((per + KT - 1) / KT) * KT;
   const int k0 = (int)min((int64_t)hi, lo + split * share), k1 = (int)min((int64_t)hi, k0 + share);
+
+  // staging: chunk `tid % CH` of rows `tid / CH + i * RSTEP`
+  const int chunk = tid % CH, row0 = tid / CH;
+  const bool chunk_in = chunk * 8 < a.D;
+  const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
+  const uint16_t *const kbase = a.k_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
+  const uint16_t *const vbase = a.v_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
+  int32_t pg[PAIRS];
+  uint4 kr[PAIRS], vr[PAIRS];
+  uint32_t okbits = 0;  // of the tile in flight: which of this thread's rows may be read
+  bool bad_page = false;
+  auto fetch_pages = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int pos = min(base + row0 + i * RSTEP, k1 - 1);
+      pg[i] = table[div_by(p.page, pos)];
+    }
+  };
+  // Every lane loads: one whose row may not be read loads block 0's first row instead and
+  // stores zeros.
+  auto fetch_tile = [&](int base) {
+    okbits = 0;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int pos = base + row0 + i * RSTEP;
+      const bool page_ok = pg[i] >= 0 && pg[i] < a.cache.P, ok = page_ok && pos < k1 && chunk_in;
+      bad_page |= !page_ok && pos < k1;
+      const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
+      const int64_t off = ok ? pg[i] * a.cache.page + in * a.cache.token : 0;
+      kr[i] = *reinterpret_cast<const uint4 *>(kbase + off);
+      vr[i] = *reinterpret_cast<const uint4 *>(vbase + off);
+      okbits |= (uint32_t)ok << i;
+    }
+  };
+  if (k0 < k1) fetch_pages(k0);
 
   // this lane's query row
   const int r = tile * cut.tile_rows + wave * kRowsWave + col;
@@ -260,97 +321,86 @@ __global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
   for (int t = 0; t < NA; ++t) o[t] = f32x16{};
   float m = kNegInf, l = 0.0f;
 
-  // staging: chunk `tid % CH` of rows `tid / CH + i * nt / CH`
-  const int chunk = tid % CH, row0 = tid / CH, rstep = nt / CH;
-  const bool chunk_in = chunk * 8 < a.D;
-  const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
-  const int64_t head_off = (int64_t)hk * a.cache.head + chunk * 8;
-  int32_t pg[PAIRS];
-  uint32_t okbits = 0;  // of the tile in flight: which of this thread's rows may be read
-  uint4 kr[PAIRS], vr[PAIRS];
-  auto fetch_pages = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int row = row0 + i * rstep, pos = base + row;
-      pg[i] = row < KT && pos < k1 ? table[div_by(p.page, pos)] : -1;
-    }
-  };
-  auto fetch_tile = [&](int base) {
-    okbits = 0;
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int row = row0 + i * rstep, pos = base + row;
-      const bool ok = pg[i] >= 0 && pg[i] < a.cache.P;
-      kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-      if (ok && chunk_in) {
-        const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
-        const int64_t off = pg[i] * a.cache.page + in * a.cache.token + head_off;
-        kr[i] = *reinterpret_cast<const uint4 *>(a.k_cache + off);
-        vr[i] = *reinterpret_cast<const uint4 *>(a.v_cache + off);
-      }
-      if (!ok && row < KT && pos < k1 && chunk == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-      okbits |= (uint32_t)ok << i;
-    }
-  };
-  // Values that are not finite are stored as 0: a probability of 0 then takes nothing from
-  // them, and the rows that do see them get them afterwards (below).
+  // Values of new tokens that are not finite are stored as 0: a probability of 0 then takes
+  // nothing from them, and the rows that do see them get them afterwards (below).
   constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
   auto finite = [&](uint32_t &w) {
-    bool bad = false;
-    if ((w & kExp) == kExp) {
-      w &= 0xFFFF0000u;
-      bad = true;
-    }
-    if (((w >> 16) & kExp) == kExp) {
-      w &= 0xFFFFu;
-      bad = true;
-    }
-    return bad;
+    const uint32_t lo16 = (w & kExp) == kExp ? 0xFFFF0000u : ~0u;
+    const uint32_t hi16 = (w & (kExp << 16)) == kExp << 16 ? 0xFFFFu : ~0u;
+    w &= lo16 & hi16;
+    return lo16 & hi16;
   };
   auto store_tile = [&](int buf, int base) {
+    if (__any(okbits != (1u << PAIRS) - 1)) {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i)
+        if (!((okbits >> i) & 1)) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i)
+      if (chunk == 0) sOk[buf][row0 + i * RSTEP] = (okbits >> i) & 1;
+    if (!PREFIX && base + KT > ctx) {  // only new tokens can be hidden from some rows
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        const uint32_t all = finite(vr[i].x) & finite(vr[i].y) & finite(vr[i].z) & finite(vr[i].w);
+        if (all != ~0u) atomicOr(&sOk[buf][row0 + i * RSTEP], 2);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
-      const int row = row0 + i * rstep;
-      if (row < KT) {
-        const int at = row * RB + ((chunk ^ (row & SW)) * 16);
-        uint4 v = vr[i];
-        if (chunk == 0) sOk[buf][row] = (okbits >> i) & 1;
-        *reinterpret_cast<uint4 *>(&sK[buf][at]) = kr[i];
-        if (base + KT > ctx) {  // only new tokens can be hidden from some rows
-          const bool b0 = finite(v.x), b1 = finite(v.y), b2 = finite(v.z), b3 = finite(v.w);
-          if (b0 || b1 || b2 || b3) atomicOr(&sOk[buf][row], 2);
-        }
-        *reinterpret_cast<uint4 *>(&sV[buf][at]) = v;
-      }
+      const int row = row0 + i * RSTEP;
+      const int at = row * RB + ((chunk ^ place_of<CH>(row)) * 16);
+      *reinterpret_cast<uint4 *>(&sKV[buf * TB + at]) = kr[i];
+      *reinterpret_cast<uint4 *>(&sKV[(NB + buf) * TB + at]) = vr[i];
     }
   };
 
-  auto step = [&](int buf, int sub, int base) {
-    const char *K = sK[buf] + sub * 32 * RB;
-    const char *V = sV[buf] + sub * 32 * RB;
+  // LDS offsets of a step's operands.  Keys: chunk 2 st + hw of row col.  Values: row 16h +
+  // 8x + 4hw + i16/4, chunk 4t + 2dh + (i16%4)/2.  The permuted places depend on the low bits
+  // of st, and of t and x; the rest are constants.
+  constexpr int NKA = NS < 8 ? NS : 8;
+  constexpr int NVT = NA < 4 ? NA : 4;
+  const int i16 = lane % 16, dh = (lane / 16) & 1;
+  int ka[NKA], va[NVT][2];
+#pragma unroll
+  for (int st = 0; st < NKA; ++st) ka[st] = col * RB + (((2 * st + hw) ^ place_of<CH>(col)) * 16);
+#pragma unroll
+  for (int t = 0; t < NVT; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 8 * x + 4 * hw + i16 / 4;
+      va[t][x] = NB * TB + row * RB + ((4 * t + 2 * dh + (i16 % 4) / 2) ^ place_of<CH>(row)) * 16 + (i16 & 1) * 8;
+    }
+  typedef __attribute__((address_space(3))) char lds_char;
+  lds_char *const lds = (lds_char *)sKV;
+
+  // 32 keys from position `base` on, group `u` of the tile; ok: which may be read, odd: whose
+  // values are not all finite.
+  auto step = [&](int u, int base, uint32_t ok, uint32_t odd) {
     f32x16 z = f32x16{};
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
-      const V8 kf = *reinterpret_cast<const V8 *>(K + col * RB + (((2 * st + hw) ^ (col & SW)) * 16));
+      const V8 kf = *(__attribute__((address_space(3))) const V8 *)(lds + ka[st % NKA] + (u * 32 * RB + (st / NKA) * 256));
       z = Mma<DT>::run(kf, q[st], z);
     }
-    const uint32_t okw = sOk[buf][sub * 32 + col];
-    const uint32_t ok = (uint32_t)__ballot(okw & 1);
-    uint32_t see = 0xFFFFFFFFu;
-    if (ok != 0xFFFFFFFFu || base + 32 > ctx) {
-      const int nb = ctx - base;  // keys of this step that are context
-      see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
+    auto sees = [&]() {  // the keys that this lane's row sees
+      const int nb = ctx - base;  // so many of them are context
+      uint32_t see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
       if (nb < 32) see |= nb >= 0 ? (uint32_t)(bits << nb) : (nb > -64 ? (uint32_t)(bits >> -nb) : 0u);
-      see &= ok;
+      return see & ok;
+    };
+    if (ok != 0xFFFFFFFFu || (!PREFIX && base + 32 > ctx)) {
+      asm volatile("");  // a branch, taken by few steps: not to be computed by all
+      const uint32_t mine = sees() >> (4 * hw);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (!((see >> (8 * (i / 4) + 4 * hw + i % 4)) & 1)) z[i] = kNegInf;
+      for (int i = 0; i < 16; ++i) z[i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[i] : kNegInf;
     }
     float top = z[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-    top = fmaxf(top, other_half(top)) * p.c;
-    if (__any(top > m)) {
+    top = max_halves(top) * p.c;
+    if (__any(top > m + kLag)) {
+      asm volatile("");
       const float mn = fmaxf(m, top);
       const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn);
       m = mn;
@@ -361,36 +411,29 @@ __global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
         for (int i = 0; i < 16; ++i) o[t][i] *= f;
     }
     const float ms = m == kNegInf ? 0.0f : m;
-    f32x8 e0, e1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e0[i] = fast_exp2(fmaf(z[i], p.c, -ms));
-      e1[i] = fast_exp2(fmaf(z[i + 8], p.c, -ms));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) l += e0[i] + e1[i];
-    const V8 p0 = __builtin_convertvector(e0, V8), p1 = __builtin_convertvector(e1, V8);
-    // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
-    const int i16 = lane % 16, dh = (lane / 16) & 1;
     typedef __attribute__((address_space(3))) s16x4 lds4;
+    V8 pr[2];
 #pragma unroll
-    for (int t = 0; t < NA; ++t) {
+    for (int h = 0; h < 2; ++h) {
+      f32x8 e;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[8 * h + i], p.c, -ms));
+      l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      pr[h] = __builtin_convertvector(e, V8);
+    }
+    // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
+#pragma unroll
+    for (int t = 0; t < NA; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        s16x4 v[2];
+        struct Two { s16x4 v[2]; } two;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = 16 * h + 8 * x + 4 * hw + i16 / 4;
-          const int c = 4 * t + 2 * dh + (i16 % 4) / 2;
-          const char *at = V + key * RB + ((c ^ (key & SW)) * 16) + (i16 & 1) * 8;
-          v[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at);
-        }
-        struct Two { s16x4 a, b; } two{v[0], v[1]};
-        o[t] = Mma<DT>::run(__builtin_bit_cast(V8, two), h ? p1 : p0, o[t]);
+        for (int x = 0; x < 2; ++x)
+          two.v[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds4 *)(lds + va[t % NVT][x] + ((32 * u + 16 * h) * RB + (t / 4) * 256)));
+        o[t] = Mma<DT>::run(__builtin_bit_cast(V8, two), pr[h], o[t]);
       }
-    }
     if (!PREFIX) {
-      uint32_t odd = (uint32_t)__ballot((okw & 3) == 3);
       while (odd) {  // a key whose values are not all finite: for the rows that see it
         const int key = __builtin_ctz(odd);
         odd &= odd - 1;
@@ -401,21 +444,27 @@ __global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
         float w = 0.0f;  // this row's probability of the key, from the half that holds it
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (8 * (i / 4) + 4 * hw + i % 4 == key) w = i < 8 ? e0[i & 7] : e1[i & 7];
-        w += other_half(w);
-        if (!((see >> key) & 1)) continue;
+          if (8 * (i / 4) + 4 * hw + i % 4 == key) w = (float)pr[i / 8][i % 8];
+        w = sum_halves(w);
+        const bool seen = (sees() >> key) & 1;
+#pragma unroll
         for (int t = 0; t < NA; ++t)
-          for (int i = 0; i < 16; ++i) {
-            const int d = 32 * t + 8 * (i / 4) + 4 * hw + i % 4;
-            if (d >= a.D || (vp[d] & kExp) != kExp) continue;
-            o[t][i] += w * (float)__builtin_bit_cast(typename Half<DT>::T, vp[d]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int d = 32 * t + 8 * b + 4 * hw;
+            uint16_t x[4] = {0, 0, 0, 0};
+            if (d < a.D) *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(vp + d);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float y = w * (float)__builtin_bit_cast(typename Half<DT>::T, x[c]);
+              o[t][4 * b + c] += seen && (x[c] & kExp) == kExp ? y : 0.0f;
+            }
           }
       }
     }
   };
 
   if (k0 < k1) {
-    fetch_pages(k0);
     fetch_tile(k0);
     fetch_pages(k0 + KT);
     for (int base = k0, buf = 0; base < k1; base += KT, buf ^= NB - 1) {
@@ -426,12 +475,25 @@ __global__ __launch_bounds__(MAXW * kWave) void k_attn(TreeAttnArgs a, Plan p) {
         fetch_pages(base + 2 * KT);
       }
       __syncthreads();
+      const uint32_t okw = sOk[buf][lane % KT];
+      const uint64_t ok = __ballot(okw & 1), odd = __ballot(okw & 2);
 #pragma unroll
-      for (int sub = 0; sub < KT / 32; ++sub)
-        if (base + 32 * sub < k1) step(buf, sub, base + 32 * sub);
+      for (int u = 0; u < SUBS; ++u)
+        step(u, base + 32 * u, (uint32_t)(ok >> (32 * u)), (uint32_t)(odd >> (32 * u)));
+      if (NB == 2) {  // the other buffer's offsets
+        const int d = buf ? -TB : TB;
+#pragma unroll
+        for (int st = 0; st < NKA; ++st) ka[st] += d;
+#pragma unroll
+        for (int t = 0; t < NVT; ++t) {
+          va[t][0] += d;
+          va[t][1] += d;
+        }
+      }
     }
   }
-  l += other_half(l);
+  if (bad_page && chunk == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+  l = sum_halves(l);
 
   // the row's part, or the row itself
   const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
@@ -547,16 +609,12 @@ void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const Cut &c = PREFIX ? p.prefix : p.suffix;
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
-  constexpr int CH = DP / 8;
-  if (c.waves == 1) {
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, 1, 2 * 32 * CH / kWave, 1, PREFIX>), grid, block, 0, stream, a, p);
-  } else if constexpr (DP == 256) {
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2 * 32 * CH / (2 * kWave), 4, PREFIX>), grid, block, 0, stream, a, p);
-  } else if (c.waves < 4) {
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2 * 32 * CH / (2 * kWave), 3, PREFIX>), grid, block, 0, stream, a, p);
-  } else {
-    hipLaunchKernelGGL((k_attn<DT, DP, 64, 2, 2 * 64 * CH / (4 * kWave), 8, PREFIX>), grid, block, 0, stream, a, p);
-  }
+  if (c.waves == 1)
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, 1, 1, PREFIX>), grid, block, 0, stream, a, p);
+  else if (c.waves == 2)
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2, PREFIX>), grid, block, 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((k_attn<DT, DP, DP == 256 ? 32 : 64, 2, 4, PREFIX>), grid, block, 0, stream, a, p);
 }
 
 template <int DT, int DP>
@@ -591,8 +649,8 @@ hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream
   const int G = a.Hq / a.Hkv;
   Plan p{};
   p.page = fast_div((uint32_t)a.cache.block_size);
-  p.suffix = cut_of(a.R * G, S * a.Hkv, longest, DP);
-  if (a.N > 1 && longest > kMinShared) p.prefix = cut_of(a.N * a.R * G, (int64_t)a.B * a.Hkv, longest, DP);
+  p.suffix = cut_of(a.R * G, S * a.Hkv, longest);
+  if (a.N > 1 && longest > kMinShared) p.prefix = cut_of(a.N * a.R * G, (int64_t)a.B * a.Hkv, longest);
   const int parts = p.prefix.splits + (p.suffix.splits > 1 ? p.suffix.splits : 0);
   const int64_t rows = S * a.R * a.Hq;
   int32_t *shared_len = reinterpret_cast<int32_t *>(a.ws);
