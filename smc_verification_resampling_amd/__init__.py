@@ -428,25 +428,76 @@ def stream_read(buf: torch.Tensor, tile_xor: torch.Tensor, stream=None):
 
 
 # ---------------------------------------------------------------------------------------
-# The pages' own operations
+# The serving operators around a round.  A call of theirs can be as short as a kernel of a
+# few microseconds, so their checks take the common case in one condition per tensor.
 # ---------------------------------------------------------------------------------------
-def _tables(block_tables: torch.Tensor, rows: Optional[int] = None):
-    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2 or (
-            rows is not None and block_tables.shape[0] != rows):
-        raise SmcsdError("block_tables must be [%s, M_cap]" % ("S" if rows is None else rows))
-    return _dev(block_tables, "block_tables", torch.int32)
+def _addr(t, name: str, dtype, n: int, dev: int) -> Optional[int]:
+    """The address of a contiguous tensor of `dtype` with at least n elements on device `dev`
+    (None for None)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtype, n)
+    raise SmcsdError("%s is on device %d, the call runs on device %d" % (name, t.get_device(), dev))
+
+
+def _need(t, name: str, dtype, n: int, dev: int) -> int:
+    if t is None:
+        raise SmcsdError("%s is missing" % name)
+    return _addr(t, name, dtype, n, dev)
+
+
+def _device_of(t, name: str) -> int:
+    """The index of the device that holds t, which must be the current one: kernels are
+    enqueued there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SmcsdError("%s must be a device tensor" % name)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise SmcsdError("%s is on device %d, the current device is %d" %
+                         (name, dev, torch.cuda.current_device()))
+    return dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _queue(stream, dev: int) -> int:
+    """The handle of `stream`, or of device `dev`'s current stream."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if stream.device_index != dev:
+        raise SmcsdError("the stream is on device %d, the tensors on device %d" %
+                         (stream.device_index, dev))
+    return stream.cuda_stream
+
+
+def _tables(block_tables, rows: Optional[int], dev: int):
+    """(address, rows, M_cap) of block tables [rows, M_cap]."""
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        raise SmcsdError("block_tables must be [S, M_cap]")
+    n, m = block_tables.shape
+    if rows is not None and n != rows:
+        raise SmcsdError("block_tables must be [%d, M_cap]" % rows)
+    return _addr(block_tables, "block_tables", torch.int32, 0, dev), n, m
 
 
 def kv_fork(forked: torch.Tensor, B: int, N: int, block_tables: torch.Tensor,
             refcounts: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     """smcsd_kv_fork: the tables of the prompts with forked[b] != 0 from their particle 0's
     (admission of a prefilled prompt).  block_tables [B*N, M_cap], refcounts [P] in/out."""
-    T = _tables(block_tables, B * N)
-    rc = _L().smcsd_kv_fork(
-        _dev(forked, "forked", torch.int32, B), B, N, T, block_tables.shape[1],
-        _dev(refcounts, "refcounts", torch.int32), refcounts.numel(),
-        _dev(status, "status", torch.int32, 1), _stream(stream))
-    _check(rc, "smcsd_kv_fork")
+    dev = _device_of(status, "status")
+    T, _, M_cap = _tables(block_tables, B * N, dev)
+    i32 = torch.int32
+    rc = _L().smcsd_kv_fork(_need(forked, "forked", i32, B, dev), B, N, T, M_cap,
+                            _need(refcounts, "refcounts", i32, 1, dev), refcounts.numel(),
+                            _need(status, "status", i32, 1, dev), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_kv_fork")
 
 
 def kv_free(freed: torch.Tensor, block_tables: torch.Tensor, refcounts: torch.Tensor,
@@ -454,15 +505,17 @@ def kv_free(freed: torch.Tensor, block_tables: torch.Tensor, refcounts: torch.Te
             workspace: torch.Tensor, stream=None) -> None:
     """smcsd_kv_free: the sequences with freed[g] != 0 drop their blocks.  workspace from
     alloc_workspace(OP_KV_FREE, 0, 0, P=P)."""
-    T = _tables(block_tables)
-    S, M_cap = block_tables.shape
+    dev = _device_of(status, "status")
+    T, S, M_cap = _tables(block_tables, None, dev)
+    i32 = torch.int32
+    R = _need(refcounts, "refcounts", i32, 1, dev)
     P = refcounts.numel()
     rc = _L().smcsd_kv_free(
-        _dev(freed, "freed", torch.int32, S), S, T, M_cap, _dev(refcounts, "refcounts", torch.int32),
-        _dev(free_list, "free_list", torch.int32, P), _dev(free_top, "free_top", torch.int32, 1), P,
-        _dev(status, "status", torch.int32, 1), _dev(workspace, "workspace", torch.uint8),
-        workspace.numel(), _stream(stream))
-    _check(rc, "smcsd_kv_free")
+        _need(freed, "freed", i32, S, dev), S, T, M_cap, R, _need(free_list, "free_list", i32, P, dev),
+        _need(free_top, "free_top", i32, 1, dev), P, _need(status, "status", i32, 1, dev),
+        _need(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_kv_free")
     _debug_kv_check(block_tables, 1, M_cap, 0, refcounts, free_list, free_top, "smcsd_kv_free",
                     stream)
 
@@ -474,29 +527,36 @@ def kv_compact(block_tables: torch.Tensor, block_size: int, refcounts: torch.Ten
     """smcsd_kv_compact: live blocks to the lowest ids; moves [P // 2, 3] and move_count are
     what kv_copy then runs on the data.  workspace from alloc_workspace(OP_KV_COMPACT, 0, 0,
     P=P)."""
-    T = _tables(block_tables)
-    S, M_cap = block_tables.shape
+    dev = _device_of(status, "status")
+    T, S, M_cap = _tables(block_tables, None, dev)
+    i32 = torch.int32
+    R = _need(refcounts, "refcounts", i32, 1, dev)
     P = refcounts.numel()
     rc = _L().smcsd_kv_compact(
-        T, S, M_cap, int(block_size), _dev(refcounts, "refcounts", torch.int32),
-        _dev(free_list, "free_list", torch.int32, P), _dev(free_top, "free_top", torch.int32, 1), P,
-        _dev(moves, "moves", torch.int32, 3 * (P // 2)),
-        _dev(move_count, "move_count", torch.int32, 1), _dev(status, "status", torch.int32, 1),
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check(rc, "smcsd_kv_compact")
+        T, S, M_cap, int(block_size), R, _need(free_list, "free_list", i32, P, dev),
+        _need(free_top, "free_top", i32, 1, dev), P, _need(moves, "moves", i32, 3 * (P // 2), dev),
+        _need(move_count, "move_count", i32, 1, dev), _need(status, "status", i32, 1, dev),
+        _need(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_kv_compact")
     _debug_kv_check(block_tables, 1, M_cap, 0, refcounts, free_list, free_top, "smcsd_kv_compact",
                     stream)
 
 
-def _pages(t: torch.Tensor, name: str, dtype=None):
-    """A cache seen as [P, block_size, Hkv, D]: rows of D contiguous elements, any strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise SmcsdError("%s must be a device tensor" % name)
-    if t.dim() != 4 or t.shape[3] < 1 or (t.shape[3] > 1 and t.stride(3) != 1):
+def _pages(t, name: str, dtype, dev: int):
+    """(shape, strides) of a cache seen as [P, block_size, Hkv, D]: rows of D contiguous
+    elements, any strides between them."""
+    try:
+        shape, strides = t.shape, t.stride()
+        if len(shape) == 4 and (dtype is None or t.dtype is dtype) and t.get_device() == dev and (
+                strides[3] == 1 or shape[3] == 1):
+            return shape, strides
+    except AttributeError:
+        pass
+    _dev(t, name, dtype, contiguous=False)
+    if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
         raise SmcsdError("%s must be [P, block_size, Hkv, D] with contiguous rows of D" % name)
-    if dtype is not None and t.dtype != dtype:
-        raise SmcsdError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    return t
+    raise SmcsdError("%s is on device %d, the call runs on device %d" % (name, t.get_device(), dev))
 
 
 def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Tensor,
@@ -505,75 +565,78 @@ def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Te
     (copy-on-write) and kv_compact write them, on every cache.  caches: tensors seen as
     [P, block_size, Hkv, D], all of one shape, type and layout; a [P, Hkv, block_size, D]
     cache is passed as its transpose(1, 2)."""
-    caches = list(caches)
-    if len(caches) > KV_COPY_MAX_CACHES:
+    n = len(caches)
+    if n > KV_COPY_MAX_CACHES:
         raise SmcsdError("at most %d caches a call" % KV_COPY_MAX_CACHES)
-    if moves.dim() != 2 or moves.shape[1] != 3:
+    dev = _device_of(status, "status")
+    if not isinstance(moves, torch.Tensor) or moves.dim() != 2 or moves.shape[1] != 3:
         raise SmcsdError("moves must be [capacity, 3]")
-    mp = _dev(moves, "moves", torch.int32)
-    cp = _dev(count, "count", torch.int32, 1)
-    sp = _dev(status, "status", torch.int32, 1)
-    if not caches:
+    i32 = torch.int32
+    mp, cp, sp = (_need(moves, "moves", i32, 0, dev), _need(count, "count", i32, 1, dev),
+                  _need(status, "status", i32, 1, dev))
+    if n == 0:
         return
-    first = _pages(caches[0], "caches[0]")
+    shape, strides = _pages(caches[0], "caches[0]", None, dev)
+    dtype = caches[0].dtype
+    ptrs = (ctypes.c_void_p * n)()
     for i, c in enumerate(caches):
-        _pages(c, "caches[%d]" % i, first.dtype)
-        if c.shape != first.shape or c.stride() != first.stride():
+        if _pages(c, "caches[%d]" % i, dtype, dev) != (shape, strides):
             raise SmcsdError("caches must have one shape and layout")
-        if c.device != moves.device:
-            raise SmcsdError("caches and moves must be on one device")
-    P, bs, H, D = first.shape
-    e = first.element_size()
-    page, token, head = (s * e for s in first.stride()[:3])
-    if H == 1 or head == D * e:  # a token's heads lie one after the other
+        ptrs[i] = c.data_ptr()
+    P, bs, H, D = shape
+    e = caches[0].element_size()
+    page, token, head = (s * e for s in strides[:3])
+    # a token's heads in one piece, or a head's tokens
+    if (H == 1 or head == D * e) and (bs == 1 or token == H * D * e):
         segments, seg, tok = 1, 0, H * D * e
-        if bs > 1 and token != tok:  # tokens apart: each is a segment of its own
-            raise SmcsdError("a token's heads, or a head's tokens, must be contiguous")
     elif bs == 1 or token == D * e:
         segments, seg, tok = H, head, D * e
     else:
         raise SmcsdError("a token's heads, or a head's tokens, must be contiguous")
-    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-    rc = _L().smcsd_kv_copy(ptrs, len(caches), page, segments, seg, tok, bs, mp, cp,
-                            moves.shape[0], P, sp, _stream(stream))
-    _check(rc, "smcsd_kv_copy")
+    rc = _L().smcsd_kv_copy(ptrs, n, page, segments, seg, tok, bs, mp, cp, moves.shape[0], P, sp,
+                            _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_kv_copy")
 
 
-# ---------------------------------------------------------------------------------------
-# The Score step's attention side
-# ---------------------------------------------------------------------------------------
-def _heads(t: torch.Tensor, name: str, S: int, R: int, D: int, dtype):
-    """[S, R, H, D] with a token's heads contiguous and one stride between tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise SmcsdError("%s must be a device tensor" % name)
+def _heads(t, name: str, S: int, R: int, D: int, dtype, dev: int):
+    """(address, heads, stride between tokens) of [S, R, H, D] with each token's heads
+    contiguous."""
+    try:
+        s, r, H, d = t.shape
+        a, tok, h, e = t.stride()
+        if R == 1:
+            tok = a if S > 1 else H * D
+        if s == S and r == R and d == D and t.dtype is dtype and t.get_device() == dev and (
+                h == D or H == 1) and (e == 1 or D == 1) and (a == R * tok or S == 1):
+            return t.data_ptr(), H, tok
+    except (AttributeError, ValueError):
+        pass
+    _dev(t, name, dtype, contiguous=False)
     if t.dim() != 4 or t.shape[0] != S or t.shape[1] != R or t.shape[3] != D:
         raise SmcsdError("%s must be [%d, %d, heads, %d]" % (name, S, R, D))
-    if t.dtype != dtype:
-        raise SmcsdError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    H = t.shape[2]
-    tok = t.stride(1) if R > 1 else (t.stride(0) if S > 1 else H * D)
-    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or \
-            (S > 1 and t.stride(0) != R * tok):
-        raise SmcsdError("%s must hold each token's heads contiguously, tokens one stride apart"
-                         % name)
-    return ctypes.c_void_p(t.data_ptr()), tok
+    if t.get_device() != dev:
+        raise SmcsdError("%s is on device %d, the call runs on device %d" % (name, t.get_device(), dev))
+    raise SmcsdError("%s must hold each token's heads contiguously, tokens one stride apart" % name)
 
 
-def _cache_pair(k_cache, v_cache, dtype, D):
-    _pages(k_cache, "k_cache", dtype)
-    _pages(v_cache, "v_cache", dtype)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _cache_pair(k_cache, v_cache, dtype, D: int, dev: int):
+    """(P, block_size, Hkv, strides of page, token and head) of two caches of one layout."""
+    kv = _pages(k_cache, "k_cache", dtype, dev)
+    if _pages(v_cache, "v_cache", dtype, dev) != kv:
         raise SmcsdError("k_cache and v_cache must have one shape and layout")
-    if k_cache.shape[3] != D:
+    (P, bs, H, d), (page, token, head, _) = kv
+    if d != D:
         raise SmcsdError("the caches' heads must have %d elements" % D)
-    P, bs, H, _ = k_cache.shape
-    page, token, head = k_cache.stride()[:3]
     # the stride of an axis of one entry says nothing
-    token = D if bs == 1 else token
-    head = D if H == 1 else head
-    page = D if P == 1 else page
-    return (ctypes.c_void_p(k_cache.data_ptr()), ctypes.c_void_p(v_cache.data_ptr()), P, bs, H, page,
-            token, head)
+    return P, bs, H, page if P > 1 else D, token if bs > 1 else D, head if H > 1 else D
+
+
+def _kv_dtype(q):
+    try:
+        return _DT_KV[q.dtype]
+    except (AttributeError, KeyError):
+        raise SmcsdError("queries, keys and values must be bfloat16 or float16") from None
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ctx_lens: torch.Tensor,
@@ -587,33 +650,35 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ctx_lens: to
     fused projection will do), q_out [S, R, Hq, D]; k_cache, v_cache seen as [P, block_size,
     Hkv, D] with any strides between rows of D; cos_sin [max_pos, rot_dim] fp32 (None: no
     rotation), positions [S, R] int32 (None: ctx_lens + j), num_nodes [S] int32."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise SmcsdError("q and k must be [S, R, heads, D]")
-    if q.dtype not in _DT_KV:
-        raise SmcsdError("queries, keys and values must be bfloat16 or float16")
+    dev = _device_of(status, "status")
+    dt = _kv_dtype(q)
+    dtype = q.dtype
+    if q.dim() != 4:
+        raise SmcsdError("q must be [S, R, heads, D]")
     S, R, Hq, D = q.shape
-    Hkv = k.shape[2]
-    qp, qs = _heads(q, "q", S, R, D, q.dtype)
-    kp, ks = _heads(k, "k", S, R, D, q.dtype)
-    vp, vs = _heads(v, "v", S, R, D, q.dtype)
-    if v.shape[2] != Hkv:
-        raise SmcsdError("k and v must have the same heads")
-    kc, vc, P, bs, H, page, token, head = _cache_pair(k_cache, v_cache, q.dtype, D)
-    if H != Hkv:
-        raise SmcsdError("the caches hold %d heads, k has %d" % (H, Hkv))
-    if cos_sin is not None and cos_sin.dim() != 2:
-        raise SmcsdError("cos_sin must be [max_pos, rot_dim]")
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    T = _tables(block_tables, S)
+    qp, _, qs = _heads(q, "q", S, R, D, dtype, dev)
+    kp, Hkv, ks = _heads(k, "k", S, R, D, dtype, dev)
+    vp, Hv, vs = _heads(v, "v", S, R, D, dtype, dev)
+    P, bs, H, page, token, head = _cache_pair(k_cache, v_cache, dtype, D, dev)
+    if Hv != Hkv or H != Hkv:
+        raise SmcsdError("k, v and the caches must have the same heads (%d, %d, %d)" % (Hkv, Hv, H))
+    max_pos, rot = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise SmcsdError("cos_sin must be [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+    T, _, M_cap = _tables(block_tables, S, dev)
+    i32 = torch.int32
     rc = _L().smcsd_qk_norm_rope(
-        qp, kp, vp, _DT_KV[q.dtype], qs, ks, vs, S, R, Hq, Hkv, D,
-        _dev(q_weight, "q_weight", q.dtype, D), _dev(k_weight, "k_weight", q.dtype, D), float(eps),
-        _dev(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(bool(interleaved)),
-        _dev(positions, "positions", torch.int32, S * R), _dev(ctx_lens, "ctx_lens", torch.int32, S),
-        _dev(num_nodes, "num_nodes", torch.int32, S), T, block_tables.shape[1], bs, P, kc, vc, page,
-        token, head, _dev(q_out, "q_out", q.dtype, S * R * Hq * D),
-        _dev(status, "status", torch.int32, 1), _stream(stream))
-    _check(rc, "smcsd_qk_norm_rope")
+        qp, kp, vp, dt, qs, ks, vs, S, R, Hq, Hkv, D, _addr(q_weight, "q_weight", dtype, D, dev),
+        _addr(k_weight, "k_weight", dtype, D, dev), eps, _addr(cos_sin, "cos_sin", torch.float32, 0, dev),
+        max_pos, rot, 1 if interleaved else 0, _addr(positions, "positions", i32, S * R, dev),
+        _need(ctx_lens, "ctx_lens", i32, S, dev), _addr(num_nodes, "num_nodes", i32, S, dev), T, M_cap,
+        bs, P, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head,
+        _need(q_out, "q_out", dtype, S * R * Hq * D, dev), _need(status, "status", i32, 1, dev),
+        _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_qk_norm_rope")
 
 
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -626,22 +691,25 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     block_size, Hkv, D] with any strides between rows of D; out [B*N, R, Hq, D]; tree_mask
     [B*N, R] int64 (bit j of row i: node i sees node j; None: a chain); lse [B*N, R, Hq]
     fp32.  workspace from alloc_workspace(OP_TREE_ATTN, B, N, K=R, V=Hq * D, P=Hkv)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[0] != B * N:
+    dev = _device_of(status, "status")
+    dt = _kv_dtype(q)
+    dtype = q.dtype
+    if q.dim() != 4 or q.shape[0] != B * N:
         raise SmcsdError("q must be [B*N, R, Hq, D]")
-    if q.dtype not in _DT_KV:
-        raise SmcsdError("queries and caches must be bfloat16 or float16")
     S, R, Hq, D = q.shape
-    qp, qs = _heads(q, "q", S, R, D, q.dtype)
-    kc, vc, P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, q.dtype, D)
-    T = _tables(block_tables, S)
+    qp, _, qs = _heads(q, "q", S, R, D, dtype, dev)
+    P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, dtype, D, dev)
+    T, _, M_cap = _tables(block_tables, S, dev)
+    i32 = torch.int32
     rc = _L().smcsd_tree_attention(
-        qp, _DT_KV[q.dtype], qs, kc, vc, page, token, head, T, block_tables.shape[1], bs, P,
-        _dev(ctx_lens, "ctx_lens", torch.int32, S), _dev(num_nodes, "num_nodes", torch.int32, S),
-        _dev(tree_mask, "tree_mask", torch.int64, S * R), B, N, R, Hq, Hkv, D, float(scale),
-        int(max_len), _dev(out, "out", q.dtype, S * R * Hq * D),
-        _dev(lse, "lse", torch.float32, S * R * Hq), _dev(status, "status", torch.int32, 1),
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
-    _check(rc, "smcsd_tree_attention")
+        qp, dt, qs, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, T, M_cap, bs, P,
+        _need(ctx_lens, "ctx_lens", i32, S, dev), _addr(num_nodes, "num_nodes", i32, S, dev),
+        _addr(tree_mask, "tree_mask", torch.int64, S * R, dev), B, N, R, Hq, Hkv, D, scale,
+        max_len, _need(out, "out", dtype, S * R * Hq * D, dev),
+        _addr(lse, "lse", torch.float32, S * R * Hq, dev), _need(status, "status", i32, 1, dev),
+        _need(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_tree_attention")
 
 
 def token_logprobs(logits: torch.Tensor, n: int, V: int, temperature: float, status: torch.Tensor,
@@ -655,7 +723,9 @@ def token_logprobs(logits: torch.Tensor, n: int, V: int, temperature: float, sta
     """smcsd_token_logprobs on logits [n, row_stride] (bf16 or fp32): tokens [n, C] int32 and
     out_logp [n, C]; out_entropy, out_lse [n]; top_ids and top_logp [n, k] (k = their second
     extent).  workspace from alloc_workspace(OP_LOGPROBS, n, 1, K=k, V=V)."""
-    if logits.dtype not in _DT:
+    dev = _device_of(status, "status")
+    dtype = getattr(logits, "dtype", None)
+    if dtype not in _DT:
         raise SmcsdError("logits must be bfloat16 or float32")
     rs = V if row_stride is None else int(row_stride)
     C, k = 0, 0
@@ -663,19 +733,21 @@ def token_logprobs(logits: torch.Tensor, n: int, V: int, temperature: float, sta
         if tokens.dim() != 2 or tokens.shape[0] != n:
             raise SmcsdError("tokens must be [n, C]")
         C = tokens.shape[1]
-    for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
-        if t is not None:
-            if t.dim() != 2 or t.shape[0] != n:
-                raise SmcsdError("%s must be [n, k]" % name)
-            if top_ids is not None and t.shape[1] != top_ids.shape[1]:
-                raise SmcsdError("top_ids and top_logp must have the same k")
-            k = t.shape[1]
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != n:
+            raise SmcsdError("top_ids must be [n, k]")
+        k = top_ids.shape[1]
+    if top_logp is not None:
+        if top_logp.dim() != 2 or top_logp.shape[0] != n or (top_ids is not None and top_logp.shape[1] != k):
+            raise SmcsdError("top_logp must be [n, k], with the k of top_ids")
+        k = top_logp.shape[1]
+    i32, f32 = torch.int32, torch.float32
     rc = _L().smcsd_token_logprobs(
-        _dev(logits, "logits", logits.dtype, n * rs - (rs - V) if n else 0), _DT[logits.dtype], rs, n,
-        V, float(temperature), _dev(tokens, "tokens", torch.int32, n * C), C, k,
-        _dev(out_logp, "out_logp", torch.float32, n * C),
-        _dev(out_entropy, "out_entropy", torch.float32, n), _dev(out_lse, "out_lse", torch.float32, n),
-        _dev(top_ids, "top_ids", torch.int32), _dev(top_logp, "top_logp", torch.float32),
-        _dev(status, "status", torch.int32, 1), _dev(workspace, "workspace", torch.uint8),
-        workspace.numel(), _stream(stream))
-    _check(rc, "smcsd_token_logprobs")
+        _need(logits, "logits", dtype, n * rs - (rs - V) if n else 0, dev), _DT[dtype], rs, n, V,
+        temperature, _addr(tokens, "tokens", i32, n * C, dev), C, k,
+        _addr(out_logp, "out_logp", f32, n * C, dev), _addr(out_entropy, "out_entropy", f32, n, dev),
+        _addr(out_lse, "out_lse", f32, n, dev), _addr(top_ids, "top_ids", i32, n * k, dev),
+        _addr(top_logp, "top_logp", f32, n * k, dev), _need(status, "status", i32, 1, dev),
+        _need(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_token_logprobs")

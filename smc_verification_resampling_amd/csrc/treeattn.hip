@@ -211,7 +211,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   constexpr int PAIRS = KT / RSTEP;          // chunks of keys (and as many of values) of a thread
   constexpr int SUBS = KT / 32;
   __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
-  __shared__ uint32_t sOk[NB][KT];  // bit 0: the row may be read; bit 1: its values are not all finite
+  __shared__ uint32_t sOdd[PREFIX ? 1 : NB][PREFIX ? 1 : KT];  // a new token whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int hw = lane / 32, col = lane % 32;
   const Cut &cut = PREFIX ? p.prefix : p.suffix;
@@ -247,40 +247,38 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   const int64_t share = (int64_t)((per + KT - 1) / KT) * KT;
   const int k0 = (int)min((int64_t)hi, lo + split * share), k1 = (int)min((int64_t)hi, k0 + share);
 
-  // staging: chunk `tid % CH` of rows `tid / CH + i * RSTEP`
+  // Staging: chunk `tid % CH` of rows `tid / CH + i * RSTEP`.  Every wave looks up a tile's
+  // rows itself, one to a lane (row lane % KT), and its lanes take their rows' places from
+  // there.
   const int chunk = tid % CH, row0 = tid / CH;
   const bool chunk_in = chunk * 8 < a.D;
   const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
   const uint16_t *const kbase = a.k_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
   const uint16_t *const vbase = a.v_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
-  int32_t pg[PAIRS];
+  int32_t pg = 0;           // of the next tile, this lane's row: its block
+  uint64_t okrows = 0;      // of the tile in flight: which rows may be read
   uint4 kr[PAIRS], vr[PAIRS];
-  uint32_t okbits = 0;  // of the tile in flight: which of this thread's rows may be read
   bool bad_page = false;
-  auto fetch_pages = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int pos = min(base + row0 + i * RSTEP, k1 - 1);
-      pg[i] = table[div_by(p.page, pos)];
-    }
+  auto fetch_page = [&](int base) {
+    pg = table[div_by(p.page, min(base + lane % KT, k1 - 1))];
   };
   // Every lane loads: one whose row may not be read loads block 0's first row instead and
   // stores zeros.
   auto fetch_tile = [&](int base) {
-    okbits = 0;
+    const int pos = base + lane % KT;
+    const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
+    bad_page |= !page_ok && pos < k1;
+    okrows = __ballot(ok);
+    const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
+    const int64_t off = ok ? pg * a.cache.page + in * a.cache.token : 0;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
-      const int pos = base + row0 + i * RSTEP;
-      const bool page_ok = pg[i] >= 0 && pg[i] < a.cache.P, ok = page_ok && pos < k1 && chunk_in;
-      bad_page |= !page_ok && pos < k1;
-      const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
-      const int64_t off = ok ? pg[i] * a.cache.page + in * a.cache.token : 0;
-      kr[i] = *reinterpret_cast<const uint4 *>(kbase + off);
-      vr[i] = *reinterpret_cast<const uint4 *>(vbase + off);
-      okbits |= (uint32_t)ok << i;
+      const int64_t at = __shfl((long long)off, row0 + i * RSTEP, kWave);
+      kr[i] = *reinterpret_cast<const uint4 *>(kbase + at);
+      vr[i] = *reinterpret_cast<const uint4 *>(vbase + at);
     }
   };
-  if (k0 < k1) fetch_pages(k0);
+  if (k0 < k1) fetch_page(k0);
 
   // this lane's query row
   const int r = tile * cut.tile_rows + wave * kRowsWave + col;
@@ -331,19 +329,18 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     return lo16 & hi16;
   };
   auto store_tile = [&](int buf, int base) {
-    if (__any(okbits != (1u << PAIRS) - 1)) {
+    if (okrows != ~0ull || DP != a.D) {
+      asm volatile("");
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i)
-        if (!((okbits >> i) & 1)) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+        if (!chunk_in || !((okrows >> (row0 + i * RSTEP)) & 1)) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i)
-      if (chunk == 0) sOk[buf][row0 + i * RSTEP] = (okbits >> i) & 1;
     if (!PREFIX && base + KT > ctx) {  // only new tokens can be hidden from some rows
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
         const uint32_t all = finite(vr[i].x) & finite(vr[i].y) & finite(vr[i].z) & finite(vr[i].w);
-        if (all != ~0u) atomicOr(&sOk[buf][row0 + i * RSTEP], 2);
+        const uint64_t odd = __ballot(all != ~0u);
+        if (chunk == 0) sOdd[buf][row0 + i * RSTEP] = (odd >> (lane / CH * CH)) & (CH == 64 ? ~0ull : (1ull << CH) - 1) ? 1 : 0;
       }
     }
 #pragma unroll
@@ -374,33 +371,46 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   typedef __attribute__((address_space(3))) char lds_char;
   lds_char *const lds = (lds_char *)sKV;
 
-  // 32 keys from position `base` on, group `u` of the tile; ok: which may be read, odd: whose
-  // values are not all finite.
-  auto step = [&](int u, int base, uint32_t ok, uint32_t odd) {
+  // The scores of group `u` of a tile's keys.
+  auto scores = [&](int u) {
     f32x16 z = f32x16{};
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
       const V8 kf = *(__attribute__((address_space(3))) const V8 *)(lds + ka[st % NKA] + (u * 32 * RB + (st / NKA) * 256));
       z = Mma<DT>::run(kf, q[st], z);
     }
-    auto sees = [&]() {  // the keys that this lane's row sees
-      const int nb = ctx - base;  // so many of them are context
+    return z;
+  };
+  // A tile's keys, from position `base` on; ok: which may be read, odd: whose values are not
+  // all finite.
+  auto step = [&](int base, uint64_t ok, uint64_t odd) {
+    auto sees = [&](int u) {  // the keys of group u that this lane's row sees
+      const int nb = ctx - (base + 32 * u);  // so many of them are context
       uint32_t see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
       if (nb < 32) see |= nb >= 0 ? (uint32_t)(bits << nb) : (nb > -64 ? (uint32_t)(bits >> -nb) : 0u);
-      return see & ok;
+      return see & (uint32_t)(ok >> (32 * u));
     };
-    if (ok != 0xFFFFFFFFu || (!PREFIX && base + 32 > ctx)) {
-      asm volatile("");  // a branch, taken by few steps: not to be computed by all
-      const uint32_t mine = sees() >> (4 * hw);
+    // all scores first: the matrix unit works on the next group's while this one's
+    // exponentials are formed
+    f32x16 z[SUBS];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[i] : kNegInf;
+    for (int u = 0; u < SUBS; ++u) z[u] = scores(u);
+    if (ok != ~0ull || (!PREFIX && base + KT > ctx)) {
+      asm volatile("");  // a branch, taken by few tiles: not to be computed by all
+#pragma unroll
+      for (int u = 0; u < SUBS; ++u) {
+        const uint32_t mine = sees(u) >> (4 * hw);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[u][i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[u][i] : kNegInf;
+      }
     }
-    float top = z[0];
+    float top = z[0][0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
+    for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, z[u][i]);
     top = max_halves(top) * p.c;
     if (__any(top > m + kLag)) {
-      asm volatile("");
       const float mn = fmaxf(m, top);
       const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn);
       m = mn;
@@ -412,30 +422,28 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     }
     const float ms = m == kNegInf ? 0.0f : m;
     typedef __attribute__((address_space(3))) s16x4 lds4;
-    V8 pr[2];
+    V8 pr[2 * SUBS];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * SUBS; ++h) {
       f32x8 e;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[8 * h + i], p.c, -ms));
+      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[h / 2][8 * (h % 2) + i], p.c, -ms));
       l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       pr[h] = __builtin_convertvector(e, V8);
-    }
-    // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
+      // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
 #pragma unroll
-    for (int t = 0; t < NA; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int t = 0; t < NA; ++t) {
         struct Two { s16x4 v[2]; } two;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           two.v[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds4 *)(lds + va[t % NVT][x] + ((32 * u + 16 * h) * RB + (t / 4) * 256)));
+              (lds4 *)(lds + va[t % NVT][x] + (16 * h * RB + (t / 4) * 256)));
         o[t] = Mma<DT>::run(__builtin_bit_cast(V8, two), pr[h], o[t]);
       }
+    }
     if (!PREFIX) {
       while (odd) {  // a key whose values are not all finite: for the rows that see it
-        const int key = __builtin_ctz(odd);
+        const int key = __builtin_ctzll(odd);
         odd &= odd - 1;
         const int pos = base + key;
         const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
@@ -443,10 +451,12 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
                              in * a.cache.token + (int64_t)hk * a.cache.head;
         float w = 0.0f;  // this row's probability of the key, from the half that holds it
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (8 * (i / 4) + 4 * hw + i % 4 == key) w = (float)pr[i / 8][i % 8];
+        for (int h = 0; h < 2 * SUBS; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (16 * h + 8 * (i / 4) + 4 * hw + i % 4 == key) w = (float)pr[h][i];
         w = sum_halves(w);
-        const bool seen = (sees() >> key) & 1;
+        const bool seen = (sees(key / 32) >> (key % 32)) & 1;
 #pragma unroll
         for (int t = 0; t < NA; ++t)
 #pragma unroll
@@ -466,20 +476,20 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
 
   if (k0 < k1) {
     fetch_tile(k0);
-    fetch_pages(k0 + KT);
+    fetch_page(k0 + KT);
     for (int base = k0, buf = 0; base < k1; base += KT, buf ^= NB - 1) {
       if (NB == 1) __syncthreads();
       store_tile(buf, base);
+      const uint64_t ok = okrows;
       if (base + KT < k1) {
         fetch_tile(base + KT);
-        fetch_pages(base + 2 * KT);
+        fetch_page(base + 2 * KT);
       }
+      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before, and nothing below moves up
       __syncthreads();
-      const uint32_t okw = sOk[buf][lane % KT];
-      const uint64_t ok = __ballot(okw & 1), odd = __ballot(okw & 2);
-#pragma unroll
-      for (int u = 0; u < SUBS; ++u)
-        step(u, base + 32 * u, (uint32_t)(ok >> (32 * u)), (uint32_t)(odd >> (32 * u)));
+      uint64_t odd = 0;
+      if (!PREFIX && base + KT > ctx) odd = __ballot(lane < KT && sOdd[buf][lane % KT]);
+      step(base, ok, odd);
       if (NB == 2) {  // the other buffer's offsets
         const int d = buf ? -TB : TB;
 #pragma unroll
@@ -492,7 +502,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
       }
     }
   }
-  if (bad_page && chunk == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+  if (bad_page) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
   l = sum_halves(l);
 
   // the row's part, or the row itself
