@@ -55,6 +55,31 @@ struct LpRow {
   }
 };
 
+// Whole numbers in the floats' order, the two zeros alike.
+__device__ __forceinline__ int ordered(float x) {
+  const int b = __float_as_int(x + 0.0f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
+constexpr int kKeyNegInf = (int)0x807FFFFFu;  // ordered(-inf)
+constexpr int kKeyLeast = INT32_MIN;
+
+// The maximum over the 64 lanes, in lane 63: DPP moves whose missing lanes read the least
+// value, which the compiler folds into the maxima.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_max(int v) {
+  return max(v, __builtin_amdgcn_update_dpp(kKeyLeast, v, CTRL, ROW_MASK, 0xf, false));
+}
+__device__ __forceinline__ int wave_max_key(int v) {
+  v = dpp_max<0x111, 0xf>(v);
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);
+  v = dpp_max<0x143, 0xc>(v);
+  return __builtin_amdgcn_readlane(v, kWave - 1);
+}
+
 struct LpState {
   float m, mc, s, u;
 };
@@ -80,28 +105,42 @@ __device__ __forceinline__ void lp_raise(LpState &st, float to, float c) {
 
 // The careful form: masked elements (-inf, or so low that x*c overflows) add nothing, where
 // the plain form's 0 * -inf would be NaN.
-template <int NV>
-__device__ __forceinline__ void lp_careful(LpState &st, const float (&x)[NV], float c) {
-  const bool wide = lp_wide(st.mc);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const float t = wide ? (x[i] - st.m) * c : fmaf(x[i], c, -st.mc);
-    const float e = fast_exp2(t);
-    st.s += e;
-    st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
-  }
+__device__ __forceinline__ void lp_careful(LpState &st, float x, float c) {
+  const float t = lp_wide(st.mc) ? (x - st.m) * c : fmaf(x, c, -st.mc);
+  const float e = fast_exp2(t);
+  st.s += e;
+  st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
+}
+__device__ __forceinline__ void lp_one(LpState &st, float x, float c) {
+  if (x > st.m) lp_raise(st, x, c);
+  lp_careful(st, x, c);
 }
 
-template <int NV>
-__device__ __forceinline__ void lp_update(LpState &st, const float (&x)[NV], float vmax, float c) {
+// The same words, which the compiler does not know to be the same: elements are widened again
+// where they are used rather than all kept in registers, which would leave two waves to a
+// SIMD instead of five.
+__device__ __forceinline__ uint4 again(uint4 w) {
+  asm("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+  return w;
+}
+
+// NU raw vectors whose largest element is vmax.
+template <int DT, int NU>
+__device__ __forceinline__ void lp_update(LpState &st, const uint4 (&raw)[NU], float vmax, float c) {
+  constexpr int EPV = Elt<DT>::kPerVec;
   if (vmax > st.m) lp_raise(st, vmax, c);
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const float t = fmaf(x[i], c, -st.mc);
-    const float e = fast_exp2(t);
-    s[i & 3] += e;
-    u[i & 3] = fmaf(e, t, u[i & 3]);
+  for (int v = 0; v < NU; ++v) {
+    float x[EPV];
+    Elt<DT>::unpack(raw[v], x);
+#pragma unroll
+    for (int i = 0; i < EPV; ++i) {
+      const float t = fmaf(x[i], c, -st.mc);
+      const float e = fast_exp2(t);
+      s[i & 3] += e;
+      u[i & 3] = fmaf(e, t, u[i & 3]);
+    }
   }
   // infinite or NaN sums, and maxima too large for the plain form, take the careful one
   const float us = (u[0] + u[1]) + (u[2] + u[3]);
@@ -109,15 +148,23 @@ __device__ __forceinline__ void lp_update(LpState &st, const float (&x)[NV], flo
     st.s += (s[0] + s[1]) + (s[2] + s[3]);
     st.u += us;
   } else {
-    lp_careful<NV>(st, x, c);
+#pragma unroll
+    for (int v = 0; v < NU; ++v) {
+      float x[EPV];
+      Elt<DT>::unpack(again(raw[v]), x);
+#pragma unroll
+      for (int i = 0; i < EPV; ++i) lp_careful(st, x[i], c);
+    }
   }
 }
 
-template <int NV>
-__device__ __forceinline__ float max_of(const float (&x)[NV]) {
+template <int DT>
+__device__ __forceinline__ float max_of(const uint4 &raw) {
+  float x[Elt<DT>::kPerVec];
+  Elt<DT>::unpack(raw, x);
   float v = x[0];
 #pragma unroll
-  for (int i = 1; i < NV; ++i) v = fmaxf(v, x[i]);
+  for (int i = 1; i < Elt<DT>::kPerVec; ++i) v = fmaxf(v, x[i]);
   return v;
 }
 
@@ -125,30 +172,29 @@ template <int DT, bool TOP>
 __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__ logits,
                                                         int64_t row_bytes, int V, float c, LpGeom g,
                                                         int64_t items, float4 *__restrict__ part,
-                                                        float *__restrict__ segmax) {
-  constexpr int EPV = Elt<DT>::kPerVec;
+                                                        int *__restrict__ segkey) {
   __shared__ float sm[kLpBlock / kWave], ssum[kLpBlock / kWave], su[kLpBlock / kWave];
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t r = it / g.tiles;
     const int ch = (int)(it - r * g.tiles);
     const LpRow<DT> row(logits + r * row_bytes, V);
-    float *const seg = TOP ? segmax + r * (g.segs + 2) : nullptr;
+    int *const seg = TOP ? segkey + r * (g.segs + 2) : nullptr;
     const int v0 = ch * g.tile_vecs, v1 = min(row.nvec, v0 + g.tile_vecs);
     LpState st{kNegInf, 0.0f, 0.0f, 0.0f};
     if (ch == 0) {
-      const float x[1] = {tid < row.head ? Elt<DT>::load(row.p, tid) : kNegInf};
-      if (tid < row.head) lp_update<1>(st, x, x[0], c);
+      const float x = tid < row.head ? Elt<DT>::load(row.p, tid) : kNegInf;
+      if (tid < row.head) lp_one(st, x, c);
       if (TOP && wave == 0) {
-        const float w = wave_max_f32(x[0]);
+        const int w = wave_max_key(ordered(fmaxf(x, kNegInf)));
         if (lane == 0) seg[0] = w;
       }
     }
     if (ch == g.tiles - 1) {
-      const float x[1] = {tid < V - row.a1 ? Elt<DT>::load(row.p, row.a1 + tid) : kNegInf};
-      if (tid < V - row.a1) lp_update<1>(st, x, x[0], c);
+      const float x = tid < V - row.a1 ? Elt<DT>::load(row.p, row.a1 + tid) : kNegInf;
+      if (tid < V - row.a1) lp_one(st, x, c);
       if (TOP && wave == 0) {
-        const float w = wave_max_f32(x[0]);
+        const int w = wave_max_key(ordered(fmaxf(x, kNegInf)));
         if (lane == 0) seg[g.segs + 1] = w;
       }
     }
@@ -159,24 +205,20 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
       uint4 buf[kLpUnroll];
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u) buf[u] = load_stream(rs, tid * 16, u * kLpBlock * 16);
-      float x[kLpUnroll * EPV], top = kNegInf, mine[kLpUnroll];
+      float top = kNegInf;
+      int keys = kKeyLeast;  // lane u: the largest of the wave's vectors u
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u) {
-        float y[EPV];
-        Elt<DT>::unpack(buf[u], y);
-        mine[u] = max_of<EPV>(y);
-        top = fmaxf(top, mine[u]);
-#pragma unroll
-        for (int i = 0; i < EPV; ++i) x[u * EPV + i] = y[i];
-      }
-      if (TOP) {
-#pragma unroll
-        for (int u = 0; u < kLpUnroll; ++u) {
-          const float w = wave_max_f32(mine[u]);
-          if (lane == 0) seg[1 + (v + u * kLpBlock) / kWave + wave] = w;
+        const float mine = max_of<DT>(buf[u]);
+        buf[u] = again(buf[u]);
+        top = fmaxf(top, mine);
+        if (TOP) {
+          const int w = wave_max_key(ordered(fmaxf(mine, kNegInf)));
+          keys = lane == u ? w : keys;
         }
       }
-      lp_update<kLpUnroll * EPV>(st, x, top, c);
+      if (TOP && lane < kLpUnroll) seg[1 + v / kWave + wave + lane * (kLpBlock / kWave)] = keys;
+      lp_update<DT, kLpUnroll>(st, buf, top, c);
     }
     // the tile's last steps: segments past the row's vectors get -inf
     const int vend = TOP ? min(g.segs * kWave, v0 + g.tile_vecs) : v1;
@@ -184,13 +226,12 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
       const int mv = v + tid;
       float top = kNegInf;
       if (mv < v1) {
-        float x[EPV];
-        Elt<DT>::unpack(load_stream(vp + mv), x);
-        top = max_of<EPV>(x);
-        lp_update<EPV>(st, x, top, c);
+        const uint4 raw[1] = {load_stream(vp + mv)};
+        top = max_of<DT>(raw[0]);
+        lp_update<DT, 1>(st, raw, top, c);
       }
       if (TOP) {
-        const float w = wave_max_f32(top);
+        const int w = wave_max_key(ordered(fmaxf(top, kNegInf)));
         if (lane == 0 && v / kWave + wave < g.segs) seg[1 + v / kWave + wave] = w;
       }
     }
@@ -220,16 +261,6 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
   }
 }
 
-// Whole numbers in the floats' order, the two zeros alike.
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // ordered(-inf)
-
 // First element of slot j of a row: the head, then the body's segments, then the tail.
 template <int DT>
 __device__ __forceinline__ int slot_start(const LpRow<DT> &row, int segs, int j, int V) {
@@ -238,34 +269,26 @@ __device__ __forceinline__ int slot_start(const LpRow<DT> &row, int segs, int j,
   return (int)min((int64_t)row.a1, row.head + (int64_t)(j - 1) * kWave * Elt<DT>::kPerVec);
 }
 
-template <int DT>
+constexpr int kLpSmall = 256;  // slots of a row that one wave ranks with 4 keys a lane
+
+// KREGS: keys of a lane of the wave that ranks the slots (4 or kLpSupers / 64).
+template <int DT, int KREGS>
 __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom g, int64_t rows,
                                                           const float4 *__restrict__ part,
-                                                          const float *__restrict__ segmax) {
+                                                          const int *__restrict__ segkey) {
   constexpr int EPV = Elt<DT>::kPerVec;
-  __shared__ float sup[kLpSupers];
-  __shared__ uint2 cand[kLpCands];
+  constexpr int W = kLpBlock / kWave;
+  __shared__ int2 cand[kLpCands];
   __shared__ int sel[kMaxTop];
-  __shared__ int s_nsel, s_ncand, s_count;
-  __shared__ uint32_t s_key;
+  __shared__ int s_nsel, s_ncand, s_count, s_key;
   __shared__ double s_max, s_ln;  // a row's largest logit, and ln of the sum relative to it
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int k = a.k;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const LpRow<DT> row(a.logits + r * a.row_bytes, a.V);
     const int slots = g.segs + 2;
-    const int run = (slots + kLpSupers - 1) / kLpSupers;  // slots ranked as one
+    const int run = (slots + KREGS * kWave - 1) / (KREGS * kWave);  // slots ranked as one
     const int nsup = (slots + run - 1) / run;
-    if (tid == 0) s_ncand = 0;
-    if (k > 0) {
-      const float *seg = segmax + r * slots;
-      for (int i = tid; i < nsup; i += kLpBlock) {
-        float v = seg[i * run];
-        for (int q = 1; q < run && i * run + q < slots; ++q) v = fmaxf(v, seg[i * run + q]);
-        sup[i] = v;
-      }
-    }
-    __syncthreads();
     if (wave == 0) {
       // the tiles joined in fp64: each is relative to m*c as rounded there
       const float4 *p = part + r * g.tiles;
@@ -291,41 +314,41 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       if (lane == 0) {
         const double ln = log(S);
         const bool nan = isnan(S) || M == __builtin_huge_valf(), empty = !nan && M == kNegInf;
-        const double lse = nan ? __builtin_nan("") : empty ? -__builtin_huge_val() : (double)M / a.T + ln;
         s_max = empty ? 0.0 : (double)M;
         s_ln = nan ? __builtin_nan("") : ln;
-        if (a.lse) a.lse[r] = (float)lse;
+        s_ncand = 0;
+        if (a.lse) a.lse[r] = nan ? __builtin_nanf("") : empty ? kNegInf : (float)((double)M / a.T + ln);
         if (a.entropy) a.entropy[r] = nan ? __builtin_nanf("") : empty ? 0.0f : (float)fmax(0.0, ln - kLn2 * U / S);
         if (nan || empty) atomicOr(a.status, nan ? SMCSD_ST_NAN_INPUT : SMCSD_ST_EMPTY_ROW);
       }
     } else if (wave == 1 && k > 0) {
-      // the k-th largest of the slots' maxima, bit by bit from the top
-      constexpr int kRegs = kLpSupers / kWave;
-      uint32_t key[kRegs];
+      const int *seg = segkey + r * slots;
+      int key[KREGS];
 #pragma unroll
-      for (int i = 0; i < kRegs; ++i) key[i] = i * kWave + lane < nsup ? ordered(sup[i * kWave + lane]) : 0;
-      const int regs = (nsup + kWave - 1) / kWave;
+      for (int i = 0; i < KREGS; ++i) {
+        const int sup = i * kWave + lane;
+        key[i] = kKeyLeast;
+        for (int q = 0; q < run && sup < nsup && sup * run + q < slots; ++q) key[i] = max(key[i], seg[sup * run + q]);
+      }
+      // the k-th largest of the slots' maxima, bit by bit from the top (as unsigned numbers)
       uint32_t T = 0;
       for (int b = 31; b >= (DT == SMCSD_DTYPE_BF16 ? 16 : 0); --b) {
-        const uint32_t t = T | (1u << b);
+        const int t = (int)((T | (1u << b)) ^ 0x80000000u);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i)
-          if (i < regs) n += __popcll(__ballot(key[i] >= t));
-        if (n >= k) T = t;
+        for (int i = 0; i < KREGS; ++i) n += __popcll(__ballot(key[i] >= t));
+        if (n >= k) T |= 1u << b;
       }
       // bf16 keys end in 16 equal bits: the bound stands for all of them
-      const uint32_t hi = DT == SMCSD_DTYPE_BF16 ? T | 0xFFFFu : T;
+      const int least = (int)(T ^ 0x80000000u), most = DT == SMCSD_DTYPE_BF16 ? least | 0xFFFF : least;
       int above = 0;
 #pragma unroll
-      for (int i = 0; i < kRegs; ++i)
-        if (i < regs) above += __popcll(__ballot(key[i] > hi));
+      for (int i = 0; i < KREGS; ++i) above += __popcll(__ballot(key[i] > most));
       int ties = k - above, at = 0;  // of those at the bound, the first by place
 #pragma unroll
-      for (int i = 0; i < kRegs; ++i) {
-        if (i >= regs) continue;
-        const bool live = key[i] > kKeyNegInf, gt = live && key[i] > hi;
-        const uint64_t eq = __ballot(live && !gt && key[i] >= T);
+      for (int i = 0; i < KREGS; ++i) {
+        const bool live = key[i] > kKeyNegInf, gt = live && key[i] > most;
+        const uint64_t eq = __ballot(live && !gt && key[i] >= least);
         const uint64_t before = lane == 0 ? 0 : ~0ull >> (64 - lane);
         const bool take = gt || (((eq >> lane) & 1) && __popcll(eq & before) < ties);
         const uint64_t tk = __ballot(take);
@@ -335,46 +358,101 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       }
       if (lane == 0) {
         s_nsel = at;
-        s_key = T;
+        s_key = max(least, kKeyNegInf + 1);
       }
     }
+    // the last two waves look up the given tokens' logits meanwhile, one to a thread
+    constexpr int kGather = kLpBlock / 2;
+    float zt = 0.0f;
+    bool ok = false;
+    auto gather = [&](int i) {
+      const int32_t x = a.tokens[r * a.C + i];
+      ok = x >= 0 && x < a.V;
+      if (ok) zt = Elt<DT>::load(row.p, x);
+    };
+    const int g0 = tid - kGather;
+    const bool gathers = a.logp && g0 >= 0;
+    if (gathers && g0 < a.C) gather(g0);
     __syncthreads();
     // log p = (x - max) / T - ln: the two never differ by more than the result holds
     const double rmax = s_max, ln = s_ln, invT = 1.0 / a.T;
     const bool none = isnan(ln), empty = ln == -__builtin_huge_val();
-    if (a.logp)
-      for (int i = tid; i < a.C; i += kLpBlock) {
-        const int32_t x = a.tokens[r * a.C + i];
-        const bool ok = x >= 0 && x < a.V;
+    if (gathers)
+      for (int i = g0; i < a.C; i += kGather) {
+        if (i != g0) gather(i);
         if (!ok) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-        const float z = ok ? Elt<DT>::load(row.p, x) : 0.0f;
-        float lp = (float)((z - rmax) * invT - ln);
-        if (!none && (z == kNegInf || empty)) lp = kNegInf;
+        float lp = (float)((zt - rmax) * invT - ln);
+        if (!none && (zt == kNegInf || empty)) lp = kNegInf;
         a.logp[r * a.C + i] = ok ? lp : __builtin_nanf("");
       }
     if (k > 0) {
-      const uint32_t T = max(s_key, kKeyNegInf + 1);
+      const int T = s_key;
       const int nsel = none ? 0 : s_nsel;  // a row with a NaN or +inf names no alternatives
-      auto offer = [&](float x, int id) {
-        const uint32_t key = ordered(x);
-        if (key >= T) {
-          const int at = atomicAdd(&s_ncand, 1);
-          if (at < kLpCands) cand[at] = make_uint2(key, (uint32_t)id);
+      // Candidates: a wave's lanes count theirs, one lane takes places for all.
+      auto offer = [&](uint32_t mine, auto value) {
+        if (!__any(mine)) return;
+        const int n = __popc(mine), upto = wave_inclusive_scan(n);
+        int at = 0;
+        if (lane == kWave - 1) at = atomicAdd(&s_ncand, upto);
+        at = __builtin_amdgcn_readlane(at, kWave - 1) + upto - n;
+        while (mine) {
+          const int b = __builtin_ctz(mine);
+          mine &= mine - 1;
+          if (at < kLpCands) cand[at] = value(b);
+          ++at;
         }
       };
-      for (int q = wave; q < nsel; q += kLpBlock / kWave) {
-        const int e0 = slot_start<DT>(row, g.segs, sel[q] * run, a.V);
-        const int e1 = slot_start<DT>(row, g.segs, sel[q] * run + run, a.V);
-        if (e0 + lane < min(e1, row.head)) offer(Elt<DT>::load(row.p, e0 + lane), e0 + lane);
-        const int b0 = max(e0, row.head), b1 = min(e1, row.a1);
-        for (int e = b0 + lane * EPV; e < b1; e += kWave * EPV) {
-          float x[EPV];
-          Elt<DT>::unpack(*reinterpret_cast<const uint4 *>(row.p + (int64_t)e * Elt<DT>::kBytes), x);
+      auto offer_one = [&](bool in, int id) {
+        const float x = in ? Elt<DT>::load(row.p, id) : kNegInf;
+        offer(in && ordered(x) >= T ? 1u : 0u, [&](int) { return make_int2(ordered(x), id); });
+      };
+      auto vec_bits = [&](const uint4 &w) {
+        float x[EPV];
+        Elt<DT>::unpack(w, x);
+        uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < EPV; ++i) offer(x[i], e + i);
+        for (int i = 0; i < EPV; ++i) m |= (ordered(x[i]) >= T ? 1u : 0u) << i;
+        return m;
+      };
+      auto load_vec = [&](int e) { return *reinterpret_cast<const uint4 *>(row.p + (int64_t)e * Elt<DT>::kBytes); };
+      // each wave reads its share of the slots, several at a time where a slot is one vector
+      // a lane; what is taken is read again, from the caches
+      constexpr int kBatch = 4;
+      for (int q0 = wave; q0 < nsel; q0 += W * kBatch) {
+        uint4 w[kBatch];
+        int at[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int i = q0 + q * W;
+          at[q] = -1;
+          if (i >= nsel) continue;
+          const int b0 = max(slot_start<DT>(row, g.segs, sel[i] * run, a.V), row.head) + lane * EPV;
+          const int b1 = min(slot_start<DT>(row, g.segs, sel[i] * run + run, a.V), row.a1);
+          if (b0 < b1) {
+            at[q] = b0;
+            w[q] = load_vec(b0);
+          }
         }
-        const int t0 = max(e0, row.a1);
-        if (t0 + lane < e1) offer(Elt<DT>::load(row.p, t0 + lane), t0 + lane);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+          if (at[q] >= 0) mine |= vec_bits(w[q]) << (EPV * q);
+        offer(mine, [&](int b) {
+          const int q = b / EPV;
+          const int id = (q == 0 ? at[0] : q == 1 ? at[1] : q == 2 ? at[2] : at[3]) + b % EPV;
+          return make_int2(ordered(Elt<DT>::load(row.p, id)), id);
+        });
+        for (int i = q0; i < min(nsel, q0 + W * kBatch); i += W) {
+          const int e0 = slot_start<DT>(row, g.segs, sel[i] * run, a.V);
+          const int e1 = slot_start<DT>(row, g.segs, sel[i] * run + run, a.V);
+          if (e0 < row.head) offer_one(e0 + lane < min(e1, row.head), e0 + lane);
+          if (e1 > row.a1) offer_one(max(e0, row.a1) + lane < e1, max(e0, row.a1) + lane);
+          for (int e = max(e0, row.head) + kWave * EPV; e < min(e1, row.a1); e += kWave * EPV) {
+            const int m0 = e + lane * EPV;
+            const uint32_t m = m0 < min(e1, row.a1) ? vec_bits(load_vec(m0)) : 0;
+            offer(m, [&](int b) { return make_int2(ordered(Elt<DT>::load(row.p, m0 + b)), m0 + b); });
+          }
+        }
       }
       __syncthreads();
       int nc = s_ncand;
@@ -389,22 +467,25 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
           for (int q = 0; q < nsel; ++q) {
             const int e1 = slot_start<DT>(row, g.segs, sel[q] * run + run, a.V);
             for (int e = slot_start<DT>(row, g.segs, sel[q] * run, a.V) + tid; e < e1; e += kLpBlock)
-              n += pred(ordered(Elt<DT>::load(row.p, e)), (uint32_t)e);
+              n += pred(ordered(Elt<DT>::load(row.p, e)), e);
           }
           if (n) atomicAdd(&s_count, n);
           __syncthreads();
           return s_count;
         };
         uint32_t K = 0;
+#pragma unroll 1
         for (int b = 31; b >= 0; --b) {
-          const uint32_t t = K | (1u << b);
-          if (count([&](uint32_t key, uint32_t) { return (int)(key >= t); }) >= k) K = t;
+          const int t = (int)((K | (1u << b)) ^ 0x80000000u);
+          if (count([&](int key, int) { return (int)(key >= t); }) >= k) K |= 1u << b;
         }
-        const int need = k - count([&](uint32_t key, uint32_t) { return (int)(key > K); });
-        uint32_t X = 0;  // the largest id bound that still holds fewer than `need` equals below it
+        const int bound = (int)(K ^ 0x80000000u);
+        const int need = k - count([&](int key, int) { return (int)(key > bound); });
+        int X = 0;  // the largest id bound that still holds fewer than `need` equals below it
+#pragma unroll 1
         for (int b = 24; b >= 0; --b) {
-          const uint32_t t = X | (1u << b);
-          if (count([&](uint32_t key, uint32_t id) { return (int)(key == K && id < t); }) < need) X = t;
+          const int t = X | (1 << b);
+          if (count([&](int key, int id) { return (int)(key == bound && id < t); }) < need) X = t;
         }
         __syncthreads();
         if (tid == 0) s_ncand = 0;
@@ -412,10 +493,10 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         for (int q = 0; q < nsel; ++q) {
           const int e1 = slot_start<DT>(row, g.segs, sel[q] * run + run, a.V);
           for (int e = slot_start<DT>(row, g.segs, sel[q] * run, a.V) + tid; e < e1; e += kLpBlock) {
-            const uint32_t key = ordered(Elt<DT>::load(row.p, e));
-            if (key > K || (key == K && (uint32_t)e <= X)) {
+            const int key = ordered(Elt<DT>::load(row.p, e));
+            if (key > bound || (key == bound && e <= X)) {
               const int at = atomicAdd(&s_ncand, 1);
-              if (at < kLpCands) cand[at] = make_uint2(key, (uint32_t)e);
+              if (at < kLpCands) cand[at] = make_int2(key, e);
             }
           }
         }
@@ -423,14 +504,14 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         nc = min(s_ncand, kLpCands);
       }
       for (int i = tid; i < nc; i += kLpBlock) {
-        const uint2 me = cand[i];
+        const int2 me = cand[i];
         int rank = 0;
         for (int j = 0; j < nc; ++j) {
-          const uint2 o = cand[j];
+          const int2 o = cand[j];
           rank += o.x > me.x || (o.x == me.x && o.y < me.y);
         }
         if (rank < k) {
-          if (a.top_ids) a.top_ids[r * k + rank] = (int32_t)me.y;
+          if (a.top_ids) a.top_ids[r * k + rank] = me.y;
           if (a.top_logp) a.top_logp[r * k + rank] = (float)((unordered(me.x) - rmax) * invT - ln);
         }
       }
@@ -438,8 +519,8 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         if (a.top_ids) a.top_ids[r * k + i] = -1;
         if (a.top_logp) a.top_logp[r * k + i] = none ? __builtin_nanf("") : kNegInf;
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
 }
 
@@ -448,7 +529,7 @@ void launch_dt(const LogprobsArgs &a, hipStream_t stream) {
   const LpGeom g = lp_geom(a.n, a.V, Elt<DT>::kPerVec);
   const int64_t items = (int64_t)a.n * g.tiles;
   float4 *part = reinterpret_cast<float4 *>(a.ws);
-  float *seg = reinterpret_cast<float *>(a.ws + align256(sizeof(float4) * (size_t)items));
+  int *seg = reinterpret_cast<int *>(a.ws + align256(sizeof(float4) * (size_t)items));
   const dim3 grid(grid_blocks(items, kLpBlock)), rows(grid_blocks(a.n, kLpBlock)), block(kLpBlock);
   if (a.k > 0)
     hipLaunchKernelGGL((k_lp_stream<DT, true>), grid, block, 0, stream, a.logits, a.row_bytes, a.V, a.c, g,
@@ -456,7 +537,10 @@ void launch_dt(const LogprobsArgs &a, hipStream_t stream) {
   else
     hipLaunchKernelGGL((k_lp_stream<DT, false>), grid, block, 0, stream, a.logits, a.row_bytes, a.V, a.c, g,
                        items, part, seg);
-  hipLaunchKernelGGL(k_lp_finalize<DT>, rows, block, 0, stream, a, g, (int64_t)a.n, part, seg);
+  if (g.segs + 2 <= kLpSmall)
+    hipLaunchKernelGGL((k_lp_finalize<DT, kLpSmall / kWave>), rows, block, 0, stream, a, g, (int64_t)a.n, part, seg);
+  else
+    hipLaunchKernelGGL((k_lp_finalize<DT, kLpSupers / kWave>), rows, block, 0, stream, a, g, (int64_t)a.n, part, seg);
 }
 
 }  // namespace
@@ -466,7 +550,7 @@ size_t logprobs_ws_bytes(int64_t n, int k, int V) {
   for (int per_vec : {Elt<SMCSD_DTYPE_BF16>::kPerVec, Elt<SMCSD_DTYPE_F32>::kPerVec}) {
     const LpGeom g = lp_geom(std::max<int64_t>(n, 1), V, per_vec);
     size_t b = align256(sizeof(float4) * (size_t)(n * g.tiles));
-    if (k > 0) b += align256(sizeof(float) * (size_t)(n * (g.segs + 2)));
+    if (k > 0) b += align256(sizeof(int) * (size_t)(n * (g.segs + 2)));
     most = std::max(most, b);
   }
   return std::max<size_t>(most, 256);
