@@ -592,7 +592,7 @@ int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int 
   a.n = n;
   a.V = V;
   a.c = (float)(1.4426950408889634073599246810018921 / (double)temperature);
-  a.T = temperature;
+  a.inv_T = 1.0 / (double)temperature;
   a.tokens = tokens;
   a.C = C;
   a.k = k;

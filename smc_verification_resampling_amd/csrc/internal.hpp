@@ -221,7 +221,7 @@ struct LogprobsArgs {
   int64_t row_bytes;
   int n, V;
   float c;     // log2(e) / T, rounded once on the host
-  double T;
+  double inv_T;
   const int32_t *tokens;
   int C, k;
   float *logp, *entropy, *lse;

@@ -103,17 +103,19 @@ __device__ __forceinline__ void lp_raise(LpState &st, float to, float c) {
   st.mc = mcn;
 }
 
-// The careful form: masked elements (-inf, or so low that x*c overflows) add nothing, where
-// the plain form's 0 * -inf would be NaN.
+// One element in the careful form: masked ones (-inf, or so low that x*c overflows) add
+// nothing, where the plain form's 0 * -inf would be NaN.
+template <bool WIDE>
 __device__ __forceinline__ void lp_careful(LpState &st, float x, float c) {
-  const float t = lp_wide(st.mc) ? (x - st.m) * c : fmaf(x, c, -st.mc);
+  const float t = WIDE ? (x - st.m) * c : fmaf(x, c, -st.mc);
   const float e = fast_exp2(t);
   st.s += e;
   st.u = fmaf(e, fmaxf(t, -1e4f), st.u);
 }
 __device__ __forceinline__ void lp_one(LpState &st, float x, float c) {
   if (x > st.m) lp_raise(st, x, c);
-  lp_careful(st, x, c);
+  if (lp_wide(st.mc)) lp_careful<true>(st, x, c);
+  else lp_careful<false>(st, x, c);
 }
 
 // The same words, which the compiler does not know to be the same: elements are widened again
@@ -124,44 +126,57 @@ __device__ __forceinline__ uint4 again(uint4 w) {
   return w;
 }
 
-// NU raw vectors whose largest element is vmax.
+// NU raw vectors whose largest element is vmax.  `masked` (the same in the whole wave):
+// earlier ones held elements that need the careful form, so it is taken at once.
 template <int DT, int NU>
-__device__ __forceinline__ void lp_update(LpState &st, const uint4 (&raw)[NU], float vmax, float c) {
+__device__ __forceinline__ void lp_update(LpState &st, const uint4 (&raw)[NU], float vmax, float c, bool &masked) {
   constexpr int EPV = Elt<DT>::kPerVec;
   if (vmax > st.m) lp_raise(st, vmax, c);
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int v = 0; v < NU; ++v) {
-    float x[EPV];
-    Elt<DT>::unpack(raw[v], x);
-#pragma unroll
-    for (int i = 0; i < EPV; ++i) {
-      const float t = fmaf(x[i], c, -st.mc);
-      const float e = fast_exp2(t);
-      s[i & 3] += e;
-      u[i & 3] = fmaf(e, t, u[i & 3]);
-    }
-  }
-  // infinite or NaN sums, and maxima too large for the plain form, take the careful one
-  const float us = (u[0] + u[1]) + (u[2] + u[3]);
-  if (fabsf(us) < __builtin_huge_valf() && !lp_wide(st.mc)) {
-    st.s += (s[0] + s[1]) + (s[2] + s[3]);
-    st.u += us;
-  } else {
+  const bool wide = __any(lp_wide(st.mc));
+  if (!masked && !wide) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < NU; ++v) {
       float x[EPV];
-      Elt<DT>::unpack(again(raw[v]), x);
+      Elt<DT>::unpack(raw[v], x);
 #pragma unroll
-      for (int i = 0; i < EPV; ++i) lp_careful(st, x[i], c);
+      for (int i = 0; i < EPV; ++i) {
+        const float t = fmaf(x[i], c, -st.mc);
+        const float e = fast_exp2(t);
+        s[i & 3] += e;
+        u[i & 3] = fmaf(e, t, u[i & 3]);
+      }
+    }
+    const float us = (u[0] + u[1]) + (u[2] + u[3]);
+    masked = __any(!(fabsf(us) < __builtin_huge_valf()));
+    if (!masked) {
+      st.s += (s[0] + s[1]) + (s[2] + s[3]);
+      st.u += us;
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < NU; ++v) {
+    float x[EPV];
+    Elt<DT>::unpack(again(raw[v]), x);
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < EPV; ++i) {
+        if (lp_wide(st.mc)) lp_careful<true>(st, x[i], c);
+        else lp_careful<false>(st, x[i], c);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPV; ++i) lp_careful<false>(st, x[i], c);
     }
   }
 }
 
+// The largest element of a raw vector.
 template <int DT>
-__device__ __forceinline__ float max_of(const uint4 &raw) {
+__device__ __forceinline__ float max_of(const uint4 &w) {
   float x[Elt<DT>::kPerVec];
-  Elt<DT>::unpack(raw, x);
+  Elt<DT>::unpack(w, x);
   float v = x[0];
 #pragma unroll
   for (int i = 1; i < Elt<DT>::kPerVec; ++i) v = fmaxf(v, x[i]);
@@ -186,7 +201,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
       const float x = tid < row.head ? Elt<DT>::load(row.p, tid) : kNegInf;
       if (tid < row.head) lp_one(st, x, c);
       if (TOP && wave == 0) {
-        const int w = wave_max_key(ordered(fmaxf(x, kNegInf)));
+        const int w = wave_max_key(ordered(x));
         if (lane == 0) seg[0] = w;
       }
     }
@@ -194,17 +209,29 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
       const float x = tid < V - row.a1 ? Elt<DT>::load(row.p, row.a1 + tid) : kNegInf;
       if (tid < V - row.a1) lp_one(st, x, c);
       if (TOP && wave == 0) {
-        const int w = wave_max_key(ordered(fmaxf(x, kNegInf)));
+        const int w = wave_max_key(ordered(x));
         if (lane == 0) seg[g.segs + 1] = w;
       }
     }
     const uint4 *vp = reinterpret_cast<const uint4 *>(row.p + row.head * Elt<DT>::kBytes);
     int v = v0;
-    for (; v + kLpBlock * kLpUnroll <= v1; v += kLpBlock * kLpUnroll) {
-      const __amdgpu_buffer_rsrc_t rs = stream_rsrc(vp + v, kLpBlock * kLpUnroll * 16);
+    bool masked = false;
+    // segments past the row's vectors get -inf
+    const int vend = TOP ? min(g.segs * kWave, v0 + g.tile_vecs) : v1;
+    for (; v + kLpBlock < vend; v += kLpBlock * kLpUnroll) {
       uint4 buf[kLpUnroll];
+      if (v + kLpBlock * kLpUnroll <= v1) {
+        const __amdgpu_buffer_rsrc_t rs = stream_rsrc(vp + v, kLpBlock * kLpUnroll * 16);
 #pragma unroll
-      for (int u = 0; u < kLpUnroll; ++u) buf[u] = load_stream(rs, tid * 16, u * kLpBlock * 16);
+        for (int u = 0; u < kLpUnroll; ++u) buf[u] = load_stream(rs, tid * 16, u * kLpBlock * 16);
+      } else {  // the row's end: -inf past it, which the careful form passes over
+        masked = true;
+#pragma unroll
+        for (int u = 0; u < kLpUnroll; ++u) {
+          const int at = v + u * kLpBlock + tid;
+          buf[u] = at < v1 ? load_stream(vp + at) : NegInfVec<DT>::get();
+        }
+      }
       float top = kNegInf;
       int keys = kKeyLeast;  // lane u: the largest of the wave's vectors u
 #pragma unroll
@@ -213,25 +240,26 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
         buf[u] = again(buf[u]);
         top = fmaxf(top, mine);
         if (TOP) {
-          const int w = wave_max_key(ordered(fmaxf(mine, kNegInf)));
+          const int w = wave_max_key(ordered(mine));
           keys = lane == u ? w : keys;
         }
       }
-      if (TOP && lane < kLpUnroll) seg[1 + v / kWave + wave + lane * (kLpBlock / kWave)] = keys;
-      lp_update<DT, kLpUnroll>(st, buf, top, c);
+      if (TOP) {
+        const int at = v / kWave + wave + lane * (kLpBlock / kWave);
+        if (lane < kLpUnroll && at < min(g.segs, (v0 + g.tile_vecs) / kWave)) seg[1 + at] = keys;
+      }
+      lp_update<DT, kLpUnroll>(st, buf, top, c, masked);
     }
-    // the tile's last steps: segments past the row's vectors get -inf
-    const int vend = TOP ? min(g.segs * kWave, v0 + g.tile_vecs) : v1;
-    for (; v < vend; v += kLpBlock) {
-      const int mv = v + tid;
+    if (v < vend) {  // one step, as in the smallest tiles
+      const int at = v + tid;
       float top = kNegInf;
-      if (mv < v1) {
-        const uint4 raw[1] = {load_stream(vp + mv)};
+      if (at < v1) {
+        const uint4 raw[1] = {load_stream(vp + at)};
         top = max_of<DT>(raw[0]);
-        lp_update<DT, 1>(st, raw, top, c);
+        lp_update<DT, 1>(st, raw, top, c, masked);
       }
       if (TOP) {
-        const int w = wave_max_key(ordered(fmaxf(top, kNegInf)));
+        const int w = wave_max_key(ordered(top));
         if (lane == 0 && v / kWave + wave < g.segs) seg[1 + v / kWave + wave] = w;
       }
     }
@@ -266,7 +294,7 @@ template <int DT>
 __device__ __forceinline__ int slot_start(const LpRow<DT> &row, int segs, int j, int V) {
   if (j <= 0) return 0;
   if (j > segs + 1) return V;
-  return (int)min((int64_t)row.a1, row.head + (int64_t)(j - 1) * kWave * Elt<DT>::kPerVec);
+  return min(row.a1, row.head + (j - 1) * kWave * Elt<DT>::kPerVec);
 }
 
 constexpr int kLpSmall = 256;  // slots of a row that one wave ranks with 4 keys a lane
@@ -313,11 +341,11 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       U = wave_sum(U);
       if (lane == 0) {
         const double ln = log(S);
-        const bool nan = isnan(S) || M == __builtin_huge_valf(), empty = !nan && M == kNegInf;
+        const bool nan = !(S < __builtin_huge_val()) || M == __builtin_huge_valf(), empty = !nan && M == kNegInf;
         s_max = empty ? 0.0 : (double)M;
         s_ln = nan ? __builtin_nan("") : ln;
         s_ncand = 0;
-        if (a.lse) a.lse[r] = nan ? __builtin_nanf("") : empty ? kNegInf : (float)((double)M / a.T + ln);
+        if (a.lse) a.lse[r] = nan ? __builtin_nanf("") : empty ? kNegInf : (float)((double)M * a.inv_T + ln);
         if (a.entropy) a.entropy[r] = nan ? __builtin_nanf("") : empty ? 0.0f : (float)fmax(0.0, ln - kLn2 * U / S);
         if (nan || empty) atomicOr(a.status, nan ? SMCSD_ST_NAN_INPUT : SMCSD_ST_EMPTY_ROW);
       }
@@ -375,7 +403,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
     if (gathers && g0 < a.C) gather(g0);
     __syncthreads();
     // log p = (x - max) / T - ln: the two never differ by more than the result holds
-    const double rmax = s_max, ln = s_ln, invT = 1.0 / a.T;
+    const double rmax = s_max, ln = s_ln, invT = a.inv_T;
     const bool none = isnan(ln), empty = ln == -__builtin_huge_val();
     if (gathers)
       for (int i = g0; i < a.C; i += kGather) {
@@ -387,6 +415,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       }
     if (k > 0) {
       const int T = s_key;
+      const float bound = unordered(T);
       const int nsel = none ? 0 : s_nsel;  // a row with a NaN or +inf names no alternatives
       // Candidates: a wave's lanes count theirs, one lane takes places for all.
       auto offer = [&](uint32_t mine, auto value) {
@@ -411,7 +440,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         Elt<DT>::unpack(w, x);
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < EPV; ++i) m |= (ordered(x[i]) >= T ? 1u : 0u) << i;
+        for (int i = 0; i < EPV; ++i) m |= (x[i] >= bound ? 1u : 0u) << i;
         return m;
       };
       auto load_vec = [&](int e) { return *reinterpret_cast<const uint4 *>(row.p + (int64_t)e * Elt<DT>::kBytes); };
