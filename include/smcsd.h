@@ -480,7 +480,7 @@ int smcsd_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int s
  * Limits: Hq, Hkv >= 1, 8 <= D <= 256 and D a multiple of 8; 0 <= rot_dim <= D, a multiple
  * of 16 (rot_dim = 0: no rotation, cos_sin may be NULL); eps >= 0 finite; 16-byte aligned
  * pointers and strides of a multiple of 8 elements; M_cap * block_size < 2^31;
- * S*R*(Hq + 2*Hkv) < 2^31.  One launch.
+ * S*R*(Hq + 2*Hkv), Hq*D and Hkv*D < 2^31.  One launch.
  */
 int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
                        int64_t k_stride, int64_t v_stride, int S, int R, int Hq, int Hkv, int D,

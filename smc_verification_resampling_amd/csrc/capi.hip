@@ -477,7 +477,8 @@ int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
       !(eps >= 0.0f) || !std::isfinite(eps))
     return SMCSD_EINVAL;
   if (S == 0) return SMCSD_OK;
-  if ((int64_t)S * R >= INT32_MAX || (int64_t)S * R * (Hq + 2 * Hkv) >= INT32_MAX ||
+  if ((int64_t)Hq * D >= INT32_MAX || (int64_t)Hkv * D >= INT32_MAX || (int64_t)S * R >= INT32_MAX ||
+      (int64_t)S * R * (Hq + 2 * Hkv) >= INT32_MAX ||
       (int64_t)S * M_cap >= INT32_MAX)
     return SMCSD_EINVAL;
   if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D ||

@@ -70,14 +70,28 @@ template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ int dpp_max(int v) {
   return max(v, __builtin_amdgcn_update_dpp(kKeyLeast, v, CTRL, ROW_MASK, 0xf, false));
 }
+// N of them, a step for all before the next: a DPP move has to wait for the lane before it.
+template <int N>
+__device__ __forceinline__ void wave_max_keys(int (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x111, 0xf>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x112, 0xf>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x114, 0xf>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x118, 0xf>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x142, 0xa>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x143, 0xc>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_readlane(v[i], kWave - 1);
+}
 __device__ __forceinline__ int wave_max_key(int v) {
-  v = dpp_max<0x111, 0xf>(v);
-  v = dpp_max<0x112, 0xf>(v);
-  v = dpp_max<0x114, 0xf>(v);
-  v = dpp_max<0x118, 0xf>(v);
-  v = dpp_max<0x142, 0xa>(v);
-  v = dpp_max<0x143, 0xc>(v);
-  return __builtin_amdgcn_readlane(v, kWave - 1);
+  int k[1] = {v};
+  wave_max_keys(k);
+  return k[0];
 }
 
 struct LpState {
@@ -233,18 +247,19 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_stream(const char *__restrict__
         }
       }
       float top = kNegInf;
-      int keys = kKeyLeast;  // lane u: the largest of the wave's vectors u
+      int key[kLpUnroll];
 #pragma unroll
       for (int u = 0; u < kLpUnroll; ++u) {
         const float mine = max_of<DT>(buf[u]);
         buf[u] = again(buf[u]);
         top = fmaxf(top, mine);
-        if (TOP) {
-          const int w = wave_max_key(ordered(mine));
-          keys = lane == u ? w : keys;
-        }
+        key[u] = ordered(mine);
       }
       if (TOP) {
+        wave_max_keys(key);
+        int keys = key[0];  // lane u: the largest of the wave's vectors u
+#pragma unroll
+        for (int u = 1; u < kLpUnroll; ++u) keys = lane == u ? key[u] : keys;
         const int at = v / kWave + wave + lane * (kLpBlock / kWave);
         if (lane < kLpUnroll && at < min(g.segs, (v0 + g.tile_vecs) / kWave)) seg[1 + at] = keys;
       }
@@ -317,9 +332,10 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
     const int slots = g.segs + 2;
     const int run = (slots + KREGS * kWave - 1) / (KREGS * kWave);  // slots ranked as one
     const int nsup = (slots + run - 1) / run;
+    if (tid == 0) s_ncand = 0;
     if (wave == 0) {
       // the tiles joined in fp64: each is relative to m*c as rounded there
-      const float4 *p = part + r * g.tiles;
+      const float4 *const p = part + r * g.tiles;
       float M = kNegInf;
       for (int i = lane; i < g.tiles; i += kWave) M = fmaxf(M, p[i].x);
       M = wave_max_f32(M);
@@ -332,19 +348,18 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         }
         const float mc = __fmul_rn(q.x, a.c);
         const double off = lp_wide(mc) ? 0.0 : (double)q.x * a.c - mc;
-        const double d = q.x == M ? 0.0 : ((double)q.x - M) * a.c;
-        const double f = exp2(d - off);
+        const double d = (q.x == M ? 0.0 : ((double)q.x - M) * a.c) - off;
+        const double f = (double)fast_exp2((float)d);  // d is small where f matters
         S += f * q.y;
-        if (f > 0.0) U += f * (q.z + (d - off) * q.y);
+        if (f > 0.0) U += f * (q.z + d * q.y);
       }
       S = wave_sum(S);
       U = wave_sum(U);
+      const double ln = log(S);
+      const bool nan = !(S < __builtin_huge_val()) || M == __builtin_huge_valf(), empty = !nan && M == kNegInf;
       if (lane == 0) {
-        const double ln = log(S);
-        const bool nan = !(S < __builtin_huge_val()) || M == __builtin_huge_valf(), empty = !nan && M == kNegInf;
         s_max = empty ? 0.0 : (double)M;
         s_ln = nan ? __builtin_nan("") : ln;
-        s_ncand = 0;
         if (a.lse) a.lse[r] = nan ? __builtin_nanf("") : empty ? kNegInf : (float)((double)M * a.inv_T + ln);
         if (a.entropy) a.entropy[r] = nan ? __builtin_nanf("") : empty ? 0.0f : (float)fmax(0.0, ln - kLn2 * U / S);
         if (nan || empty) atomicOr(a.status, nan ? SMCSD_ST_NAN_INPUT : SMCSD_ST_EMPTY_ROW);
@@ -402,21 +417,10 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
     const bool gathers = a.logp && g0 >= 0;
     if (gathers && g0 < a.C) gather(g0);
     __syncthreads();
-    // log p = (x - max) / T - ln: the two never differ by more than the result holds
-    const double rmax = s_max, ln = s_ln, invT = a.inv_T;
-    const bool none = isnan(ln), empty = ln == -__builtin_huge_val();
-    if (gathers)
-      for (int i = g0; i < a.C; i += kGather) {
-        if (i != g0) gather(i);
-        if (!ok) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-        float lp = (float)((zt - rmax) * invT - ln);
-        if (!none && (zt == kNegInf || empty)) lp = kNegInf;
-        a.logp[r * a.C + i] = ok ? lp : __builtin_nanf("");
-      }
     if (k > 0) {
       const int T = s_key;
       const float bound = unordered(T);
-      const int nsel = none ? 0 : s_nsel;  // a row with a NaN or +inf names no alternatives
+      const int nsel = s_nsel;
       // Candidates: a wave's lanes count theirs, one lane takes places for all.
       auto offer = [&](uint32_t mine, auto value) {
         if (!__any(mine)) return;
@@ -445,7 +449,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       };
       auto load_vec = [&](int e) { return *reinterpret_cast<const uint4 *>(row.p + (int64_t)e * Elt<DT>::kBytes); };
       // each wave reads its share of the slots, several at a time where a slot is one vector
-      // a lane; what is taken is read again, from the caches
+      // a lane
       constexpr int kBatch = 4;
       for (int q0 = wave; q0 < nsel; q0 += W * kBatch) {
         uint4 w[kBatch];
@@ -485,7 +489,7 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
       }
       __syncthreads();
       int nc = s_ncand;
-      if (nc > kLpCands) {
+      if (nc > kLpCands && !isnan(s_ln)) {
         // Too many elements at or above the bound (long runs of equal logits): the k-th
         // largest element itself, then the smallest ids among its equals, each bit by bit.
         auto count = [&](auto pred) {
@@ -532,21 +536,37 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         __syncthreads();
         nc = min(s_ncand, kLpCands);
       }
+      if (isnan(s_ln)) nc = 0;  // a row with a NaN or +inf names no alternatives
+      const double rmax = s_max, ln = s_ln;
       for (int i = tid; i < nc; i += kLpBlock) {
         const int2 me = cand[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < nc; ++j) {
           const int2 o = cand[j];
           rank += o.x > me.x || (o.x == me.x && o.y < me.y);
         }
         if (rank < k) {
           if (a.top_ids) a.top_ids[r * k + rank] = me.y;
-          if (a.top_logp) a.top_logp[r * k + rank] = (float)((unordered(me.x) - rmax) * invT - ln);
+          // log p = (x - max) / T - ln: the two never differ by more than the result holds
+          if (a.top_logp) a.top_logp[r * k + rank] = (float)((unordered(me.x) - rmax) * a.inv_T - ln);
         }
       }
       for (int i = nc + tid; i < k; i += kLpBlock) {
         if (a.top_ids) a.top_ids[r * k + i] = -1;
-        if (a.top_logp) a.top_logp[r * k + i] = none ? __builtin_nanf("") : kNegInf;
+        if (a.top_logp) a.top_logp[r * k + i] = isnan(ln) ? __builtin_nanf("") : kNegInf;
+      }
+    } else {
+      __syncthreads();
+    }
+    if (gathers) {
+      const double rmax = s_max, ln = s_ln;
+      for (int i = g0; i < a.C; i += kGather) {
+        if (i != g0) gather(i);
+        if (!ok) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+        float lp = (float)((zt - rmax) * a.inv_T - ln);
+        if (!isnan(ln) && (zt == kNegInf || ln == -__builtin_huge_val())) lp = kNegInf;
+        a.logp[r * a.C + i] = ok ? lp : __builtin_nanf("");
       }
     }
     __syncthreads();
