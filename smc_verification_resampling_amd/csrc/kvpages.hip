@@ -15,8 +15,34 @@ namespace smcsd {
 namespace {
 
 constexpr int kPgBlock = 256;
-constexpr int kGroup = 8192;  // blocks of one workgroup's part of the pool
-constexpr int kPerThread = kGroup / kPgBlock;
+// Blocks of a thread in the kernels over the pool, consecutive ones.  A workgroup adds up the
+// counts of the other workgroups' groups, so large pools take more blocks to a thread; with
+// 4, a pool of 24576 blocks is counted in 3.5 us instead of 9.7 us with 32 (three groups
+// keep only three workgroups busy).
+constexpr int kFewPerThread = 4, kManyPerThread = 32;
+constexpr int64_t kManyBlocks = 1 << 20;
+inline int per_thread(int64_t P) { return P <= kManyBlocks ? kFewPerThread : kManyPerThread; }
+
+// Bit i: `is` holds for the count of block b0 + i (b0 a multiple of PT).
+template <int PT, typename F>
+__device__ __forceinline__ uint32_t block_bits(const int32_t *rc, int64_t b0, int64_t P, F is) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < PT; i += 4) {
+    int32_t v[4] = {0, 0, 0, 0};
+    if (b0 + i + 4 <= P) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = rc[b0 + i + c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (b0 + i + c < P) v[c] = rc[b0 + i + c];
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m |= (b0 + i + c < P && is(v[c]) ? 1u : 0u) << (i + c);
+  }
+  return m;
+}
 
 // ---------------------------------------------------------------------------------
 // fork
@@ -34,22 +60,25 @@ __global__ __launch_bounds__(kPgBlock) void k_fork(const int32_t *__restrict__ f
     const int col = (int)(it % cols);
     const int64_t bp = it / cols;
     const int part = (int)(bp % parts), b = (int)(bp / parts);
-    const int s = col * kPgBlock + threadIdx.x;
-    if (forked[b] == 0 || s >= M) continue;
+    const int s = min(col * kPgBlock + (int)threadIdx.x, M - 1);
     int32_t *row0 = T + (int64_t)b * N * M + s;
-    const int32_t id = row0[0];
-    if (id == -1) continue;
+    const int32_t id = row0[0];  // on its way before the prompt's flag is looked at
+    if (forked[b] == 0 || col * kPgBlock + (int)threadIdx.x >= M || id == -1) continue;
     if (id < 0 || id >= P) {
       if (part == 0) atomicOr(status, SMCSD_ST_BAD_INPUT);
       continue;
     }
     const int n0 = 1 + part * kForkRows, n1 = min(N, n0 + kForkRows);
+    int32_t old[kForkRows];  // all read before any is written: one wait instead of one a row
+#pragma unroll
+    for (int i = 0; i < kForkRows; ++i) old[i] = row0[(int64_t)min(n0 + i, n1 - 1) * M];
     int took = 0;
     bool bad = false;
-    for (int n = n0; n < n1; ++n) {
-      int32_t *d = row0 + (int64_t)n * M;
-      if (*d == -1) {
-        *d = id;
+#pragma unroll
+    for (int i = 0; i < kForkRows; ++i) {
+      if (n0 + i >= n1) continue;
+      if (old[i] == -1) {
+        row0[(int64_t)(n0 + i) * M] = id;
         ++took;
       } else {
         bad = true;
@@ -95,19 +124,14 @@ __global__ __launch_bounds__(kPgBlock) void k_free_drop(const int32_t *__restric
 }
 
 // Workgroup g counts group g's freed blocks; workgroup 0 keeps the old top for the push.
+template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_free_count(const int32_t *__restrict__ rc, int64_t P,
                                                          const int32_t *__restrict__ free_top,
                                                          int32_t *__restrict__ gcount,
                                                          int32_t *__restrict__ old_top) {
   __shared__ int lds[kPgBlock / kWave];
-  const int64_t b0 = (int64_t)blockIdx.x * kGroup;
-  int n = 0;
-#pragma unroll 8
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t b = b0 + i * kPgBlock + threadIdx.x;
-    n += b < P && is_freed(rc[b]);
-  }
-  const int total = block_sum<int, kPgBlock>(n, lds);
+  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * PT;
+  const int total = block_sum<int, kPgBlock>(__popc(block_bits<PT>(rc, b0, P, is_freed)), lds);
   if (threadIdx.x == 0) {
     gcount[blockIdx.x] = total;
     if (blockIdx.x == 0) *old_top = *free_top;
@@ -116,6 +140,7 @@ __global__ __launch_bounds__(kPgBlock) void k_free_count(const int32_t *__restri
 
 // Workgroup g pushes group g's freed blocks: a block's place is the old top plus the number
 // of freed blocks with higher ids (those of later groups, then those above it here).
+template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc, int64_t P, int groups,
                                                         const int32_t *__restrict__ gcount,
                                                         const int32_t *__restrict__ old_top,
@@ -124,6 +149,8 @@ __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc
                                                         int32_t *__restrict__ status) {
   __shared__ int lds[kPgBlock / kWave];
   const int g = blockIdx.x;
+  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * PT;
+  uint32_t m = block_bits<PT>(rc, b0, P, is_freed);
   const int mine = gcount[g];
   if (mine == 0 && g != 0) return;
   int later = 0;
@@ -137,12 +164,6 @@ __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc
     *free_top = (int32_t)(to > P ? P : to);
   }
   if (mine == 0) return;
-  // thread t holds the consecutive blocks [t * kPerThread, ...): a mask of the freed ones
-  const int64_t b0 = (int64_t)g * kGroup + threadIdx.x * kPerThread;
-  uint32_t m = 0;
-  static_assert(kPerThread == 32, "one bit per block of a thread");
-  for (int i = 0; i < kPerThread; ++i)
-    if (b0 + i < P && is_freed(rc[b0 + i])) m |= 1u << i;
   const int n = __popc(m);
   int total;
   const int below = block_exclusive_scan<int, kPgBlock>(n, lds, &total);
@@ -164,17 +185,14 @@ __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc
 // once, while the number of movers is only known where id n lies); others are dead.
 constexpr int32_t kMapDead = -1, kMapStay = -2;
 
+__device__ __forceinline__ bool is_live(int32_t r) { return r > 0; }
+
+template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_compact_count(const int32_t *__restrict__ rc, int64_t P,
                                                             int32_t *__restrict__ gcount) {
   __shared__ int lds[kPgBlock / kWave];
-  const int64_t b0 = (int64_t)blockIdx.x * kGroup;
-  int n = 0;
-#pragma unroll 8
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t b = b0 + i * kPgBlock + threadIdx.x;
-    n += b < P && rc[b] > 0;
-  }
-  const int total = block_sum<int, kPgBlock>(n, lds);
+  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * PT;
+  const int total = block_sum<int, kPgBlock>(__popc(block_bits<PT>(rc, b0, P, is_live)), lds);
   if (threadIdx.x == 0) gcount[blockIdx.x] = total;
 }
 
@@ -182,11 +200,14 @@ struct CompactWs {
   int32_t *gcount, *meta, *map, *holes, *movers;  // meta: live blocks, moves
 };
 
+template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_compact_rank(int32_t *__restrict__ rc, int64_t P,
                                                            int groups, CompactWs w,
                                                            int32_t *__restrict__ move_count) {
   __shared__ int lds[kPgBlock / kWave];
   const int g = blockIdx.x;
+  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * PT;
+  const uint32_t m = block_bits<PT>(rc, b0, P, is_live);
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < groups; i += kPgBlock) {
     const int c = w.gcount[i];
@@ -195,25 +216,22 @@ __global__ __launch_bounds__(kPgBlock) void k_compact_rank(int32_t *__restrict__
   }
   before = block_sum<int, kPgBlock>(before, lds);
   const int n = block_sum<int, kPgBlock>(all, lds);
+  int total;
+  before += block_exclusive_scan<int, kPgBlock>(__popc(m), lds, &total);
   if (g == 0 && threadIdx.x == 0) {
     w.meta[0] = n;
     if (n == P) w.meta[1] = *move_count = 0;
   }
-  const int64_t g0 = (int64_t)g * kGroup;
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t b = g0 + i * kPgBlock + threadIdx.x;
-    const int32_t r = b < P ? rc[b] : 0;
-    const int live = r > 0;
-    int total;
-    const int rank = before + block_exclusive_scan<int, kPgBlock>(live, lds, &total);
-    before += total;
-    if (b >= P) continue;
+  for (int i = 0; i < PT; ++i) {
+    const int64_t b = b0 + i;
+    if (b >= P) break;
+    const int rank = before + __popc(m & ((1u << i) - 1));  // live blocks below b
     int32_t to = kMapDead;
-    if (live) {
+    if ((m >> i) & 1) {
       to = b < n ? kMapStay : n - 1 - rank;
       if (b >= n) w.movers[n - 1 - rank] = (int32_t)b;
     } else {
-      if (r < 0) rc[b] = 0;
+      if (rc[b] < 0) rc[b] = 0;
       if (b < n) w.holes[b - rank] = (int32_t)b;
     }
     w.map[b] = to;
@@ -266,6 +284,7 @@ struct CopyCaches {
 };
 
 constexpr int kCopyUnroll = 4;
+constexpr uint32_t kCopyWords = 1 << 20;
 
 // Workgroup = one (entry, cache) at a time, over all segments.  W: bytes moved at once.
 template <typename W>
@@ -292,25 +311,30 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, int n_cach
     const char *from = caches.p[c] + src * block_stride;
     char *to = caches.p[c] + dst * block_stride;
     const uint32_t per = (uint32_t)(tokens * token_bytes / (int)sizeof(W));  // words of a segment
-    const int64_t words = (int64_t)per * segments;
-    for (int64_t i0 = threadIdx.x; i0 < words; i0 += kPgBlock * kCopyUnroll) {
-      W v[kCopyUnroll];
-      int64_t off[kCopyUnroll];
+    if (per == 0) continue;
+    // some segments at a time, few enough for 32-bit word numbers
+    const int most = (int)max(1u, kCopyWords / per);
+    for (int h0 = 0; h0 < segments; h0 += most) {
+      const uint32_t words = per * (uint32_t)min(most, segments - h0);
+      for (uint32_t i0 = threadIdx.x; i0 < words; i0 += kPgBlock * kCopyUnroll) {
+        W v[kCopyUnroll];
+        int64_t off[kCopyUnroll];
 #pragma unroll
-      for (int u = 0; u < kCopyUnroll; ++u) {
-        const int64_t i = i0 + u * kPgBlock;
-        const int64_t h = i / per;
-        off[u] = h * segment_stride + (i - h * per) * (int64_t)sizeof(W);
-        if (i < words) v[u] = *reinterpret_cast<const W *>(from + off[u]);
+        for (int u = 0; u < kCopyUnroll; ++u) {
+          const uint32_t i = i0 + u * kPgBlock;
+          const uint32_t h = i / per;
+          off[u] = (h0 + (int64_t)h) * segment_stride + (int64_t)(i - h * per) * (int)sizeof(W);
+          if (i < words) v[u] = *reinterpret_cast<const W *>(from + off[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+          if (i0 + u * kPgBlock < words) *reinterpret_cast<W *>(to + off[u]) = v[u];
       }
-#pragma unroll
-      for (int u = 0; u < kCopyUnroll; ++u)
-        if (i0 + u * kPgBlock < words) *reinterpret_cast<W *>(to + off[u]) = v[u];
     }
   }
 }
 
-inline int64_t groups_of(int64_t P) { return ceil_div(P, kGroup); }
+inline int64_t groups_of(int64_t P) { return ceil_div(P, kPgBlock * per_thread(P)); }
 
 }  // namespace
 
@@ -336,9 +360,13 @@ hipError_t launch_kv_free(const int32_t *freed, int64_t S, int32_t *T, int M, in
   int32_t *gcount = reinterpret_cast<int32_t *>(ws), *old_top = gcount + groups;
   hipLaunchKernelGGL(k_free_drop, dim3(grid_blocks(S * cols, kPgBlock)), dim3(kPgBlock), 0, stream, freed, S,
                      T, M, rc, P, status, cols);
-  hipLaunchKernelGGL(k_free_count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, free_top, gcount, old_top);
-  hipLaunchKernelGGL(k_free_push, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, gcount, old_top, fl,
-                     free_top, status);
+  auto rest = [&](auto count, auto push) {
+    hipLaunchKernelGGL(count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, free_top, gcount, old_top);
+    hipLaunchKernelGGL(push, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, gcount, old_top, fl, free_top,
+                       status);
+  };
+  if (per_thread(P) == kFewPerThread) rest(k_free_count<kFewPerThread>, k_free_push<kFewPerThread>);
+  else rest(k_free_count<kManyPerThread>, k_free_push<kManyPerThread>);
   return hipGetLastError();
 }
 
@@ -354,8 +382,12 @@ hipError_t launch_kv_compact(int32_t *T, int64_t S, int M, int block_size, int32
   w.map = reinterpret_cast<int32_t *>(lists);
   w.holes = reinterpret_cast<int32_t *>(lists + list);
   w.movers = reinterpret_cast<int32_t *>(lists + 2 * list);
-  hipLaunchKernelGGL(k_compact_count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, w.gcount);
-  hipLaunchKernelGGL(k_compact_rank, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, w, move_count);
+  auto first = [&](auto count, auto rank) {
+    hipLaunchKernelGGL(count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, w.gcount);
+    hipLaunchKernelGGL(rank, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, w, move_count);
+  };
+  if (per_thread(P) == kFewPerThread) first(k_compact_count<kFewPerThread>, k_compact_rank<kFewPerThread>);
+  else first(k_compact_count<kManyPerThread>, k_compact_rank<kManyPerThread>);
   const int64_t most = std::max<int64_t>(S * M, P);
   hipLaunchKernelGGL(k_compact_apply, dim3(grid_blocks(ceil_div(most, kPgBlock), kPgBlock)), dim3(kPgBlock),
                      0, stream, T, S * M, block_size, rc, P, w, fl, free_top, moves, status);

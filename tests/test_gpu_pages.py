@@ -162,6 +162,16 @@ def test_compact(S, M, P, fill):
     p.same()
 
 
+def test_a_pool_of_millions_of_blocks():
+    P = (1 << 20) + 12345
+    p = Pool(4, 5000, P, seed=1, share=0.2)
+    p.free([1, 3])
+    p.same()
+    p.compact()
+    p.same()
+    p.consistent()
+
+
 def test_compact_full_and_empty_pools():
     p = Pool(2, 50, 100, share=0.0)
     for s in range(2):
