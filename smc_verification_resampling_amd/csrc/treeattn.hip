@@ -23,6 +23,12 @@
 #include "half.hpp"
 #include "internal.hpp"
 
+#ifndef B1
+#define B1 2
+#define B2 3
+#define B4 2
+#define K4 64
+#endif
 namespace smcsd {
 
 namespace {
@@ -207,11 +213,11 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   constexpr int NS = DP / 16;      // product steps of a score
   constexpr int NA = DP / 32;      // accumulator tiles of an output row
   constexpr int TB = KT * RB;      // bytes of a tile
-  constexpr int RSTEP = NW * kWave / CH;     // rows that the workgroup moves at once
-  constexpr int PAIRS = KT / RSTEP;          // chunks of keys (and as many of values) of a thread
+  constexpr int RW = kWave / CH;             // rows of a wave's load
+  constexpr int NLD = KT / (RW * NW);        // loads of keys (and as many of values) of a wave for a tile
   constexpr int SUBS = KT / 32;
   __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
-  __shared__ uint32_t sOdd[PREFIX ? 1 : NB][PREFIX ? 1 : KT];  // a new token whose values are not all finite
+  __shared__ uint32_t sOdd[PREFIX ? 1 : KT];  // a new token whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int hw = lane / 32, col = lane % 32;
   const Cut &cut = PREFIX ? p.prefix : p.suffix;
@@ -247,36 +253,41 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   const int64_t share = (int64_t)((per + KT - 1) / KT) * KT;
   const int k0 = (int)min((int64_t)hi, lo + split * share), k1 = (int)min((int64_t)hi, k0 + share);
 
-  // Staging: chunk `tid % CH` of rows `tid / CH + i * RSTEP`.  Every wave looks up a tile's
+  // Staging, by loads that go straight to LDS, 64 chunks of 16 bytes in a row for a wave's
+  // instruction: instruction i of a wave fills rows (i * NW + wave) * RW + lane / CH, place
+  // lane % CH, which asks for chunk (lane % CH) ^ place_of(row).  Every wave looks up a tile's
   // rows itself, one to a lane (row lane % KT), and its lanes take their rows' places from
   // there.
-  const int chunk = tid % CH, row0 = tid / CH;
-  const bool chunk_in = chunk * 8 < a.D;
   const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
-  const uint16_t *const kbase = a.k_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
-  const uint16_t *const vbase = a.v_cache + (int64_t)hk * a.cache.head + (chunk_in ? chunk * 8 : 0);
-  int32_t pg = 0;           // of the next tile, this lane's row: its block
-  uint64_t okrows = 0;      // of the tile in flight: which rows may be read
-  uint4 kr[PAIRS], vr[PAIRS];
+  const uint16_t *const kbase = a.k_cache + (int64_t)hk * a.cache.head;
+  const uint16_t *const vbase = a.v_cache + (int64_t)hk * a.cache.head;
+  typedef __attribute__((address_space(3))) char lds_char;
+  typedef __attribute__((address_space(3))) void lds_void;
+  typedef __attribute__((address_space(1))) const void glb_void;
+  lds_char *const lds = (lds_char *)sKV;
+  int32_t pg = 0;       // of the tile that is fetched next, this lane's row: its block
   bool bad_page = false;
   auto fetch_page = [&](int base) {
     pg = table[div_by(p.page, min(base + lane % KT, k1 - 1))];
   };
-  // Every lane loads: one whose row may not be read loads block 0's first row instead and
-  // stores zeros.
-  auto fetch_tile = [&](int base) {
+  // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Every lane loads:
+  // one whose row may not be read loads block 0's first row instead (mend() clears it).
+  auto fetch_tile = [&](int buf, int base) {
     const int pos = base + lane % KT;
     const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
     bad_page |= !page_ok && pos < k1;
-    okrows = __ballot(ok);
+    const uint64_t rows = __ballot(ok);
     const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
     const int64_t off = ok ? pg * a.cache.page + in * a.cache.token : 0;
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int64_t at = __shfl((long long)off, row0 + i * RSTEP, kWave);
-      kr[i] = *reinterpret_cast<const uint4 *>(kbase + at);
-      vr[i] = *reinterpret_cast<const uint4 *>(vbase + at);
+    for (int i = 0; i < NLD; ++i) {
+      const int first = (i * NW + wave) * RW, row = first + lane / CH;
+      const int chunk = (lane % CH) ^ place_of<CH>(row);
+      const int64_t at = __shfl((long long)off, row, kWave) + (chunk * 8 < a.D ? chunk * 8 : 0);
+      __builtin_amdgcn_global_load_lds((glb_void *)(kbase + at), (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((glb_void *)(vbase + at), (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
     }
+    return rows;
   };
   if (k0 < k1) fetch_page(k0);
 
@@ -319,8 +330,10 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   for (int t = 0; t < NA; ++t) o[t] = f32x16{};
   float m = kNegInf, l = 0.0f;
 
-  // Values of new tokens that are not finite are stored as 0: a probability of 0 then takes
-  // nothing from them, and the rows that do see them get them afterwards (below).
+  // What a tile in LDS needs where some rows may not be read, the head is padded or new
+  // tokens are among its rows: unread rows and padding become 0 (0 * NaN is no 0), and values
+  // of new tokens that are not finite become 0 too: a probability of 0 then takes nothing from
+  // them, and the rows that do see them get them afterwards (below).
   constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
   auto finite = [&](uint32_t &w) {
     const uint32_t lo16 = (w & kExp) == kExp ? 0xFFFF0000u : ~0u;
@@ -328,27 +341,21 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     w &= lo16 & hi16;
     return lo16 & hi16;
   };
-  auto store_tile = [&](int buf, int base) {
-    if (okrows != ~0ull || DP != a.D) {
-      asm volatile("");
-#pragma unroll
-      for (int i = 0; i < PAIRS; ++i)
-        if (!chunk_in || !((okrows >> (row0 + i * RSTEP)) & 1)) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-    }
-    if (!PREFIX && base + KT > ctx) {  // only new tokens can be hidden from some rows
-#pragma unroll
-      for (int i = 0; i < PAIRS; ++i) {
-        const uint32_t all = finite(vr[i].x) & finite(vr[i].y) & finite(vr[i].z) & finite(vr[i].w);
-        const uint64_t odd = __ballot(all != ~0u);
-        if (chunk == 0) sOdd[buf][row0 + i * RSTEP] = (odd >> (lane / CH * CH)) & (CH == 64 ? ~0ull : (1ull << CH) - 1) ? 1 : 0;
+  auto mend = [&](int buf, int base, uint64_t ok) {
+    const bool fresh = !PREFIX && base + KT > ctx;
+#pragma unroll 1
+    for (int i = 0; i < NLD; ++i) {
+      const int row = (i * NW + wave) * RW + lane / CH, chunk = (lane % CH) ^ place_of<CH>(row);
+      char *const k = sKV + buf * TB + row * RB + lane % CH * 16, *const v = k + NB * TB;
+      const bool in = (ok >> row) & 1;
+      if (!in || chunk * 8 >= a.D) *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
+      if (fresh) {
+        uint4 w = *reinterpret_cast<uint4 *>(v);
+        const bool odd = (finite(w.x) & finite(w.y) & finite(w.z) & finite(w.w)) != ~0u;
+        const uint64_t any = __ballot(odd);
+        if (odd) *reinterpret_cast<uint4 *>(v) = w;
+        if (lane % CH == 0) sOdd[row] = (any >> lane) & ((1ull << CH) - 1) ? 1 : 0;
       }
-    }
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int row = row0 + i * RSTEP;
-      const int at = row * RB + ((chunk ^ place_of<CH>(row)) * 16);
-      *reinterpret_cast<uint4 *>(&sKV[buf * TB + at]) = kr[i];
-      *reinterpret_cast<uint4 *>(&sKV[(NB + buf) * TB + at]) = vr[i];
     }
   };
 
@@ -368,8 +375,6 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
       const int row = 8 * x + 4 * hw + i16 / 4;
       va[t][x] = NB * TB + row * RB + ((4 * t + 2 * dh + (i16 % 4) / 2) ^ place_of<CH>(row)) * 16 + (i16 & 1) * 8;
     }
-  typedef __attribute__((address_space(3))) char lds_char;
-  lds_char *const lds = (lds_char *)sKV;
 
   // The scores of group `u` of a tile's keys.
   auto scores = [&](int u) {
@@ -474,31 +479,50 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     }
   };
 
+  // Tile n is computed from buffer n % NB while the next NB - 1 are on their way.  A wave
+  // waits for its own loads of tile n (those of later tiles may be outstanding), then for
+  // the other waves, which are then also done with the buffer that is filled next.
   if (k0 < k1) {
-    fetch_tile(k0);
-    fetch_page(k0 + KT);
-    for (int base = k0, buf = 0; base < k1; base += KT, buf ^= NB - 1) {
-      if (NB == 1) __syncthreads();
-      store_tile(buf, base);
-      const uint64_t ok = okrows;
-      if (base + KT < k1) {
-        fetch_tile(base + KT);
-        fetch_page(base + 2 * KT);
+    uint64_t oks[NB - 1];
+#pragma unroll
+    for (int i = 0; i < NB - 1; ++i) {
+      oks[i] = fetch_tile(i, k0 + i * KT);
+      fetch_page(k0 + (i + 1) * KT);
+    }
+    int buf = 0;
+    for (int base = k0; base < k1; base += KT) {
+      static_assert(2 * NLD * (NB - 2) < 64, "the wait counts at most 63 loads");
+      if (NB > 2 && base + (NB - 2) * KT < k1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * NLD * (NB - 2)) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const uint64_t ok = oks[0];
+#pragma unroll
+      for (int i = 0; i + 1 < NB - 1; ++i) oks[i] = oks[i + 1];
+      if (base + (NB - 1) * KT < k1) {
+        const int next = buf == 0 ? NB - 1 : buf - 1;
+        oks[NB - 2] = fetch_tile(next, base + (NB - 1) * KT);
+        fetch_page(base + NB * KT);
       }
-      __builtin_amdgcn_sched_barrier(0);  // the loads above go out before, and nothing below moves up
-      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);  // the loads go out before, and nothing below moves up
       uint64_t odd = 0;
-      if (!PREFIX && base + KT > ctx) odd = __ballot(lane < KT && sOdd[buf][lane % KT]);
+      if (ok != ~0ull || DP != a.D || (!PREFIX && base + KT > ctx)) {
+        mend(buf, base, ok);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (!PREFIX && base + KT > ctx) odd = __ballot(lane < KT && sOdd[lane % KT]);
+      }
       step(base, ok, odd);
-      if (NB == 2) {  // the other buffer's offsets
-        const int d = buf ? -TB : TB;
+      // the next buffer's offsets
+      const int d = buf == NB - 1 ? -(NB - 1) * TB : TB;
+      buf = buf == NB - 1 ? 0 : buf + 1;
 #pragma unroll
-        for (int st = 0; st < NKA; ++st) ka[st] += d;
+      for (int st = 0; st < NKA; ++st) ka[st] += d;
 #pragma unroll
-        for (int t = 0; t < NVT; ++t) {
-          va[t][0] += d;
-          va[t][1] += d;
-        }
+      for (int t = 0; t < NVT; ++t) {
+        va[t][0] += d;
+        va[t][1] += d;
       }
     }
   }
@@ -620,11 +644,11 @@ void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
   if (c.waves == 1)
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, 1, 1, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, DP == 256 ? 2 : B1, 1, PREFIX>), grid, block, 0, stream, a, p);
   else if (c.waves == 2)
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, 2, 2, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 32, DP == 256 ? 2 : B2, 2, PREFIX>), grid, block, 0, stream, a, p);
   else
-    hipLaunchKernelGGL((k_attn<DT, DP, DP == 256 ? 32 : 64, 2, 4, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, DP == 256 ? 32 : K4, DP == 256 ? 2 : B4, 4, PREFIX>), grid, block, 0, stream, a, p);
 }
 
 template <int DT, int DP>
