@@ -9,11 +9,10 @@
 // product's order of keys is free, so the first operand takes the same order, four keys at
 // a time, with the transposing LDS read.  Probabilities never leave the registers, and the
 // rescaling of O is one factor per lane.
-// Keys and values go through LDS in tiles of 32 or 64 tokens, shared by a workgroup's
-// waves: the next tile's loads are in flight, in registers, while the present one is
-// computed, and the block ids of the tile after it are fetched meanwhile.  Rows of a tile
-// are stored with their 16-byte chunks permuted by the row number, so that reads of one
-// chunk over many rows fall on different banks.
+// Keys and values go through LDS in tiles of 32 tokens, shared by a workgroup's waves, with
+// loads that write to LDS directly: the next tile is on its way while the present one is
+// computed.  Rows of a tile are stored with their 16-byte chunks permuted by the row number,
+// so that reads of one chunk over many rows fall on different banks.
 // Long contexts are split over workgroups (each a range of keys of equal length) and the
 // parts (m, l, O) joined in fp32.
 #include <cmath>
@@ -23,17 +22,38 @@
 #include "half.hpp"
 #include "internal.hpp"
 
-#ifndef B1
-#define B1 2
-#define B2 3
-#define B4 2
-#define K4 64
-#endif
 namespace smcsd {
 
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Reads of a tile.  In assembly, each with its wait: the compiler, which knows no buffers,
+// would let a read of one wait for all loads to LDS, those of the next tiles too.
+// four rows' 16 bytes each
+template <class V8>
+__device__ __forceinline__ void read_rows(V8 (&x)[4], uint32_t a, uint32_t b, uint32_t c, uint32_t d, int offset) {
+  asm volatile(
+      "ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+      "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+      : "v"(a), "v"(b), "v"(c), "v"(d), "i"(offset));
+}
+// two times 4 + 4 keys of one column
+template <class V8>
+__device__ __forceinline__ void read_columns(V8 (&x)[2], uint32_t a, uint32_t b, uint32_t c, uint32_t d, int offset) {
+  s16x4 y[4];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %4 offset:%8\n\tds_read_b64_tr_b16 %1, %5 offset:%8\n\t"
+      "ds_read_b64_tr_b16 %2, %6 offset:%8\n\tds_read_b64_tr_b16 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(y[0]), "=&v"(y[1]), "=&v"(y[2]), "=&v"(y[3])
+      : "v"(a), "v"(b), "v"(c), "v"(d), "i"(offset));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    struct { s16x4 v[2]; } two = {{y[2 * i], y[2 * i + 1]}};
+    x[i] = __builtin_bit_cast(V8, two);
+  }
+}
 
 template <int DT> struct Mma;
 template <> struct Mma<SMCSD_DTYPE_BF16> {
@@ -53,6 +73,12 @@ template <> struct Mma<SMCSD_DTYPE_F16> {
 // Launch plan
 // ---------------------------------------------------------------------------------
 constexpr int kRowsWave = 32;
+// Keys of a tile, and two buffers for them.  Heads of 128: 64 keys for four waves gave 110 us
+// against 118 for 64 rows of 16 heads over 131,071 keys, but 154 against 147 for 32 prompts'
+// 2048 shared keys and 320 x 8 rows each; three buffers 123 and 149 there, and for two waves
+// (256 sequences of 8 heads, 3.2 GB) 687 us against 661, four buffers 802: what the loads gain
+// in flight, the workgroups lose that no longer fit beside each other.
+constexpr int KT = 32, NB = 2;
 constexpr int kWavesMax = 4;      // two workgroups of four waves fill a compute unit's registers
 constexpr int kPartItems = 1024;  // workgroups that the splits of a launch aim at
 constexpr int kMinShared = 128;   // shorter shared prefixes are read per particle
@@ -203,8 +229,8 @@ __device__ __forceinline__ int place_of(int r) {
 // rescale nothing.
 constexpr float kLag = 8.0f;
 
-// DP: head size padded to 64, 128 or 256.  KT: keys of a tile.  NB: LDS buffers.  NW: waves.
-template <int DT, int DP, int KT, int NB, int NW, bool PREFIX>
+// DP: head size padded to 64, 128 or 256.  NW: waves.
+template <int DT, int DP, int NW, bool PREFIX>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
@@ -215,7 +241,6 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   constexpr int TB = KT * RB;      // bytes of a tile
   constexpr int RW = kWave / CH;             // rows of a wave's load
   constexpr int NLD = KT / (RW * NW);        // loads of keys (and as many of values) of a wave for a tile
-  constexpr int SUBS = KT / 32;
   __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
   __shared__ uint32_t sOdd[PREFIX ? 1 : KT];  // a new token whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -265,31 +290,39 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   typedef __attribute__((address_space(3))) void lds_void;
   typedef __attribute__((address_space(1))) const void glb_void;
   lds_char *const lds = (lds_char *)sKV;
-  int32_t pg = 0;       // of the tile that is fetched next, this lane's row: its block
+  // Block ids: lane i holds that of block id0 + i of the table, loaded again when a tile ends
+  // past them, once in 64 blocks.  A load for each tile would be waited for together with the
+  // tile that was asked for before it.
+  int32_t ids = 0;
+  int id0 = -kWave;
   bool bad_page = false;
-  auto fetch_page = [&](int base) {
-    pg = table[div_by(p.page, min(base + lane % KT, k1 - 1))];
-  };
   // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Every lane loads:
   // one whose row may not be read loads block 0's first row instead (mend() clears it).
   auto fetch_tile = [&](int buf, int base) {
-    const int pos = base + lane % KT;
+    if ((int)div_by(p.page, min(base + KT, k1) - 1) >= id0 + kWave) {
+      id0 = div_by(p.page, base);
+      ids = table[min(id0 + lane, (int)div_by(p.page, k1 - 1))];
+      asm volatile("" : "+v"(ids));  // waited for here, not by every tile
+    }
+    const int pos = base + lane % KT, block = div_by(p.page, pos);
+    const int32_t pg = __shfl(ids, min(block - id0, kWave - 1), kWave);
     const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
     bad_page |= !page_ok && pos < k1;
     const uint64_t rows = __ballot(ok);
-    const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
-    const int64_t off = ok ? pg * a.cache.page + in * a.cache.token : 0;
+    const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : 0;
+    int64_t at[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) at[i] = __shfl((long long)off, (i * NW + wave) * RW + lane / CH, kWave);
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
-      const int first = (i * NW + wave) * RW, row = first + lane / CH;
-      const int chunk = (lane % CH) ^ place_of<CH>(row);
-      const int64_t at = __shfl((long long)off, row, kWave) + (chunk * 8 < a.D ? chunk * 8 : 0);
-      __builtin_amdgcn_global_load_lds((glb_void *)(kbase + at), (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((glb_void *)(vbase + at), (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
+      const int first = (i * NW + wave) * RW;
+      const int chunk = (lane % CH) ^ place_of<CH>(first + lane / CH);
+      at[i] += chunk * 8 < a.D ? chunk * 8 : 0;
+      __builtin_amdgcn_global_load_lds((glb_void *)(kbase + at[i]), (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((glb_void *)(vbase + at[i]), (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
     }
     return rows;
   };
-  if (k0 < k1) fetch_page(k0);
 
   // this lane's query row
   const int r = tile * cut.tile_rows + wave * kRowsWave + col;
@@ -376,44 +409,39 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
       va[t][x] = NB * TB + row * RB + ((4 * t + 2 * dh + (i16 % 4) / 2) ^ place_of<CH>(row)) * 16 + (i16 & 1) * 8;
     }
 
-  // The scores of group `u` of a tile's keys.
-  auto scores = [&](int u) {
+  // The scores of a tile's keys.
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  auto scores = [&] {
     f32x16 z = f32x16{};
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
-      const V8 kf = *(__attribute__((address_space(3))) const V8 *)(lds + ka[st % NKA] + (u * 32 * RB + (st / NKA) * 256));
-      z = Mma<DT>::run(kf, q[st], z);
+    for (int st = 0; st < NS; st += 4) {
+      V8 kf[4];
+      read_rows(kf, lds0 + ka[st % NKA], lds0 + ka[st % NKA + 1], lds0 + ka[st % NKA + 2], lds0 + ka[st % NKA + 3],
+                (st / NKA) * 256);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z = Mma<DT>::run(kf[i], q[st + i], z);
     }
     return z;
   };
   // A tile's keys, from position `base` on; ok: which may be read, odd: whose values are not
   // all finite.
   auto step = [&](int base, uint64_t ok, uint64_t odd) {
-    auto sees = [&](int u) {  // the keys of group u that this lane's row sees
-      const int nb = ctx - (base + 32 * u);  // so many of them are context
+    auto sees = [&] {  // the tile's keys that this lane's row sees
+      const int nb = ctx - base;  // so many of them are context
       uint32_t see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
       if (nb < 32) see |= nb >= 0 ? (uint32_t)(bits << nb) : (nb > -64 ? (uint32_t)(bits >> -nb) : 0u);
-      return see & (uint32_t)(ok >> (32 * u));
+      return see & (uint32_t)ok;
     };
-    // all scores first: the matrix unit works on the next group's while this one's
-    // exponentials are formed
-    f32x16 z[SUBS];
-#pragma unroll
-    for (int u = 0; u < SUBS; ++u) z[u] = scores(u);
+    f32x16 z = scores();
     if (ok != ~0ull || (!PREFIX && base + KT > ctx)) {
       asm volatile("");  // a branch, taken by few tiles: not to be computed by all
+      const uint32_t mine = sees() >> (4 * hw);
 #pragma unroll
-      for (int u = 0; u < SUBS; ++u) {
-        const uint32_t mine = sees(u) >> (4 * hw);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[u][i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[u][i] : kNegInf;
-      }
+      for (int i = 0; i < 16; ++i) z[i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[i] : kNegInf;
     }
-    float top = z[0][0];
+    float top = z[0];
 #pragma unroll
-    for (int u = 0; u < SUBS; ++u)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, z[u][i]);
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
     top = max_halves(top) * p.c;
     if (__any(top > m + kLag)) {
       const float mn = fmaxf(m, top);
@@ -426,24 +454,22 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
         for (int i = 0; i < 16; ++i) o[t][i] *= f;
     }
     const float ms = m == kNegInf ? 0.0f : m;
-    typedef __attribute__((address_space(3))) s16x4 lds4;
-    V8 pr[2 * SUBS];
+    V8 pr[2];
 #pragma unroll
-    for (int h = 0; h < 2 * SUBS; ++h) {
+    for (int h = 0; h < 2; ++h) {
       f32x8 e;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[h / 2][8 * (h % 2) + i], p.c, -ms));
+      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[8 * h + i], p.c, -ms));
       l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       pr[h] = __builtin_convertvector(e, V8);
       // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
 #pragma unroll
-      for (int t = 0; t < NA; ++t) {
-        struct Two { s16x4 v[2]; } two;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          two.v[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds4 *)(lds + va[t % NVT][x] + (16 * h * RB + (t / 4) * 256)));
-        o[t] = Mma<DT>::run(__builtin_bit_cast(V8, two), pr[h], o[t]);
+      for (int t = 0; t < NA; t += 2) {
+        V8 vf[2];
+        read_columns(vf, lds0 + va[t % NVT][0], lds0 + va[t % NVT][1], lds0 + va[t % NVT + 1][0], lds0 + va[t % NVT + 1][1],
+                     16 * h * RB + (t / 4) * 256);
+        o[t] = Mma<DT>::run(vf[0], pr[h], o[t]);
+        o[t + 1] = Mma<DT>::run(vf[1], pr[h], o[t + 1]);
       }
     }
     if (!PREFIX) {
@@ -456,12 +482,12 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
                              in * a.cache.token + (int64_t)hk * a.cache.head;
         float w = 0.0f;  // this row's probability of the key, from the half that holds it
 #pragma unroll
-        for (int h = 0; h < 2 * SUBS; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (16 * h + 8 * (i / 4) + 4 * hw + i % 4 == key) w = (float)pr[h][i];
         w = sum_halves(w);
-        const bool seen = (sees(key / 32) >> (key % 32)) & 1;
+        const bool seen = (sees() >> key) & 1;
 #pragma unroll
         for (int t = 0; t < NA; ++t)
 #pragma unroll
@@ -479,31 +505,18 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     }
   };
 
-  // Tile n is computed from buffer n % NB while the next NB - 1 are on their way.  A wave
-  // waits for its own loads of tile n (those of later tiles may be outstanding), then for
-  // the other waves, which are then also done with the buffer that is filled next.
+  // Tile n is computed from buffer n % 2 while the next one is on its way.  A wave waits for
+  // its own loads of tile n, then for the other waves, which are then also done with the buffer
+  // that is filled next.
   if (k0 < k1) {
-    uint64_t oks[NB - 1];
-#pragma unroll
-    for (int i = 0; i < NB - 1; ++i) {
-      oks[i] = fetch_tile(i, k0 + i * KT);
-      fetch_page(k0 + (i + 1) * KT);
-    }
+    uint64_t next_ok = fetch_tile(0, k0);
     int buf = 0;
     for (int base = k0; base < k1; base += KT) {
-      static_assert(2 * NLD * (NB - 2) < 64, "the wait counts at most 63 loads");
-      if (NB > 2 && base + (NB - 2) * KT < k1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * NLD * (NB - 2)) : "memory");
-      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      const uint64_t ok = oks[0];
-#pragma unroll
-      for (int i = 0; i + 1 < NB - 1; ++i) oks[i] = oks[i + 1];
-      if (base + (NB - 1) * KT < k1) {
-        const int next = buf == 0 ? NB - 1 : buf - 1;
-        oks[NB - 2] = fetch_tile(next, base + (NB - 1) * KT);
-        fetch_page(base + NB * KT);
-      }
+      const uint64_t ok = next_ok;
+      if (base + KT < k1) next_ok = fetch_tile(buf ^ 1, base + KT);
       __builtin_amdgcn_sched_barrier(0);  // the loads go out before, and nothing below moves up
       uint64_t odd = 0;
       if (ok != ~0ull || DP != a.D || (!PREFIX && base + KT > ctx)) {
@@ -515,8 +528,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
       }
       step(base, ok, odd);
       // the next buffer's offsets
-      const int d = buf == NB - 1 ? -(NB - 1) * TB : TB;
-      buf = buf == NB - 1 ? 0 : buf + 1;
+      const int d = buf ? -TB : TB;
+      buf ^= 1;
 #pragma unroll
       for (int st = 0; st < NKA; ++st) ka[st] += d;
 #pragma unroll
@@ -593,7 +606,10 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
 }
 
 // ---------------------------------------------------------------------------------
-// The parts of a row joined: one wave per row of out.
+// The parts of a row joined: a workgroup per row of out.  Groups of D/4 lanes (rounded up to
+// a power of two) take every so many parts, four loads at a time, and their sums meet in LDS, in a
+// fixed order.  Bound by reading the parts: 1024 rows x 64 parts of 128 (34 MB) 12 us; a
+// wave per row, part after part, took 49.
 // ---------------------------------------------------------------------------------
 constexpr int kJoinBlock = 256;
 
@@ -601,9 +617,12 @@ template <int DT>
 __global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p, int64_t rows) {
   typedef typename Half<DT>::V4 V4;
   typedef float f32x4 __attribute__((ext_vector_type(4)));
-  const int lane = threadIdx.x % kWave;
-  for (int64_t r = (int64_t)blockIdx.x * (kJoinBlock / kWave) + threadIdx.x / kWave; r < rows;
-       r += (int64_t)gridDim.x * (kJoinBlock / kWave)) {
+  __shared__ f32x4 sums[kJoinBlock];
+  const int tid = threadIdx.x, lane = tid % kWave;
+  int width = 1;  // lanes of a group
+  while (4 * width < a.D) width *= 2;
+  const int groups = kJoinBlock / width, group = tid / width, d = 4 * (tid % width);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const int64_t t = r / a.Hq;
     const int s = (int)(t / a.R), j = (int)(t - (int64_t)s * a.R);
     const Seq sq = seq_of(a, s);
@@ -612,29 +631,37 @@ __global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p
     const int parts = p.prefix.splits + p.suffix.splits;
     float m = kNegInf;
     for (int i = first + lane; i < parts; i += kWave) {
-      const float *ml = p.ml + 2 * (i * rows + r);
-      if (ml[1] != 0.0f) m = fmaxf(m, ml[0]);
+      const float2 ml = *reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r));
+      m = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
     }
     m = wave_max_f32(m);
+    auto factor = [&](float2 ml) { return ml.y == 0.0f || ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - m); };
     float l = 0.0f;
-    f32x4 acc = {};
-    const int d = 4 * lane;
-    for (int i = first; i < parts; ++i) {
-      const float *ml = p.ml + 2 * (i * rows + r);
-      if (ml[1] == 0.0f) continue;
-      const float f = ml[0] == kNegInf ? 0.0f : fast_exp2(ml[0] - m);
-      l = fmaf(ml[1], f, l);
-      if (d < a.D) {
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(p.acc + (i * rows + r) * a.D + d);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c] = fmaf(x[c], f, acc[c]);
-      }
+    for (int i = first + lane; i < parts; i += kWave) {
+      const float2 ml = *reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r));
+      l = fmaf(ml.y, factor(ml), l);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    l = wave_sum_f32(l);
+    f32x4 acc = {};
+#pragma unroll 4
+    for (int i = first + group; i < parts; i += groups) {
+      const float f = factor(*reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r)));
+      // an empty part is not written: what lies there is not used
+      const f32x4 x = *reinterpret_cast<const f32x4 *>(p.acc + (i * rows + r) * a.D + (d < a.D ? d : 0));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] *= inv;
-    if (d < a.D) *reinterpret_cast<uint2 *>(a.out + r * a.D + d) = __builtin_bit_cast(uint2, __builtin_convertvector(acc, V4));
-    if (a.lse && lane == 0) a.lse[r] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
+      for (int c = 0; c < 4; ++c) acc[c] = f != 0.0f ? fmaf(x[c], f, acc[c]) : acc[c];
+    }
+    sums[tid] = acc;
+    __syncthreads();
+    if (group == 0) {
+      for (int g = 1; g < groups; ++g) acc += sums[g * width + tid];
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      acc *= inv;
+      if (d < a.D)
+        *reinterpret_cast<uint2 *>(a.out + r * a.D + d) = __builtin_bit_cast(uint2, __builtin_convertvector(acc, V4));
+    }
+    if (a.lse && tid == 0) a.lse[r] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
+    __syncthreads();
   }
 }
 
@@ -644,11 +671,11 @@ void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
   if (c.waves == 1)
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, DP == 256 ? 2 : B1, 1, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 1, PREFIX>), grid, block, 0, stream, a, p);
   else if (c.waves == 2)
-    hipLaunchKernelGGL((k_attn<DT, DP, 32, DP == 256 ? 2 : B2, 2, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX>), grid, block, 0, stream, a, p);
   else
-    hipLaunchKernelGGL((k_attn<DT, DP, DP == 256 ? 32 : K4, DP == 256 ? 2 : B4, 4, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX>), grid, block, 0, stream, a, p);
 }
 
 template <int DT, int DP>
@@ -660,8 +687,7 @@ void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStr
   }
   launch_part<DT, DP, false>(a, p, stream);
   if (p.suffix.splits > 1)
-    hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(ceil_div(rows, kJoinBlock / kWave), kJoinBlock)),
-                       dim3(kJoinBlock), 0, stream, a, p, rows);
+    hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(rows, kJoinBlock)), dim3(kJoinBlock), 0, stream, a, p, rows);
 }
 
 }  // namespace
