@@ -155,9 +155,12 @@ __device__ __forceinline__ Seq seq_of(const TreeAttnArgs &a, int s) {
 
 // ---------------------------------------------------------------------------------
 // Shared prefix: per prompt, the length in whole blocks that all N tables name alike and
-// that every particle has as context.
+// that every particle has as context.  A thread per block of the table, 16 particles' entries
+// in flight: bound by the latency of those loads (32 prompts of 16 x 133 entries 5.1 us, 4 of
+// 31 x 4665 entries 15 us).
 // ---------------------------------------------------------------------------------
-constexpr int kShareBlock = 512;
+constexpr int kShareBlock = 1024;
+constexpr int kShareLoads = 16;
 
 __global__ __launch_bounds__(kShareBlock) void k_shared_len(TreeAttnArgs a, int32_t *__restrict__ out) {
   __shared__ int s_first, s_ctx;
@@ -181,8 +184,10 @@ __global__ __launch_bounds__(kShareBlock) void k_shared_len(TreeAttnArgs a, int3
       if (c < slots) {
         const int32_t id = T[c];
         bool same = id >= 0 && id < a.cache.P;
-#pragma unroll 8
-        for (int n = 1; n < a.N; ++n) same &= T[(int64_t)n * a.cache.M_cap + c] == id;
+        for (int n = 1; n < a.N && same; n += kShareLoads) {
+#pragma unroll
+          for (int u = 0; u < kShareLoads; ++u) same &= T[(int64_t)min(n + u, a.N - 1) * a.cache.M_cap + c] == id;
+        }
         if (!same) atomicMin(&s_first, c);
       }
       __syncthreads();
@@ -228,6 +233,8 @@ __device__ __forceinline__ int place_of(int r) {
 // rescaled: probabilities up to 256 lose nothing in either type, and most steps then
 // rescale nothing.
 constexpr float kLag = 8.0f;
+
+__device__ const uint32_t kNothing[4] = {0, 0, 0, 0};  // loaded where there is nothing to load
 
 // DP: head size padded to 64, 128 or 256.  NW: waves.
 template <int DT, int DP, int NW, bool PREFIX>
@@ -296,8 +303,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   int32_t ids = 0;
   int id0 = -kWave;
   bool bad_page = false;
-  // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Every lane loads:
-  // one whose row may not be read loads block 0's first row instead (mend() clears it).
+  // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Rows that may not
+  // be, and the padding of a head, become 0, as what such a lane loads is (0 * NaN is no 0).
   auto fetch_tile = [&](int buf, int base) {
     if ((int)div_by(p.page, min(base + KT, k1) - 1) >= id0 + kWave) {
       id0 = div_by(p.page, base);
@@ -309,17 +316,23 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
     bad_page |= !page_ok && pos < k1;
     const uint64_t rows = __ballot(ok);
-    const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : 0;
-    int64_t at[NLD];
+    const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
+    constexpr int NAT = NLD < 4 ? NLD : 4;  // looked up together
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) at[i] = __shfl((long long)off, (i * NW + wave) * RW + lane / CH, kWave);
+    for (int i0 = 0; i0 < NLD; i0 += NAT) {
+      int64_t at[NAT];
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-      const int first = (i * NW + wave) * RW;
-      const int chunk = (lane % CH) ^ place_of<CH>(first + lane / CH);
-      at[i] += chunk * 8 < a.D ? chunk * 8 : 0;
-      __builtin_amdgcn_global_load_lds((glb_void *)(kbase + at[i]), (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((glb_void *)(vbase + at[i]), (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
+      for (int i = 0; i < NAT; ++i) at[i] = __shfl((long long)off, ((i0 + i) * NW + wave) * RW + lane / CH, kWave);
+#pragma unroll
+      for (int i = 0; i < NAT; ++i) {
+        const int first = ((i0 + i) * NW + wave) * RW;
+        const int chunk = (lane % CH) ^ place_of<CH>(first + lane / CH);
+        const bool in = at[i] >= 0 && chunk * 8 < a.D;
+        const uint16_t *const k = in ? kbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
+        const uint16_t *const v = in ? vbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
+        __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
+      }
     }
     return rows;
   };
@@ -363,10 +376,9 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   for (int t = 0; t < NA; ++t) o[t] = f32x16{};
   float m = kNegInf, l = 0.0f;
 
-  // What a tile in LDS needs where some rows may not be read, the head is padded or new
-  // tokens are among its rows: unread rows and padding become 0 (0 * NaN is no 0), and values
-  // of new tokens that are not finite become 0 too: a probability of 0 then takes nothing from
-  // them, and the rows that do see them get them afterwards (below).
+  // What a tile in LDS needs where new tokens are among its rows: their values that are not
+  // finite become 0: a probability of 0 then takes nothing from them, and the rows that do see
+  // them get them after the last tile.
   constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
   auto finite = [&](uint32_t &w) {
     const uint32_t lo16 = (w & kExp) == kExp ? 0xFFFF0000u : ~0u;
@@ -374,21 +386,16 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     w &= lo16 & hi16;
     return lo16 & hi16;
   };
-  auto mend = [&](int buf, int base, uint64_t ok) {
-    const bool fresh = !PREFIX && base + KT > ctx;
+  auto mend = [&](int buf, int base) {
 #pragma unroll 1
     for (int i = 0; i < NLD; ++i) {
-      const int row = (i * NW + wave) * RW + lane / CH, chunk = (lane % CH) ^ place_of<CH>(row);
-      char *const k = sKV + buf * TB + row * RB + lane % CH * 16, *const v = k + NB * TB;
-      const bool in = (ok >> row) & 1;
-      if (!in || chunk * 8 >= a.D) *reinterpret_cast<uint4 *>(k) = *reinterpret_cast<uint4 *>(v) = make_uint4(0, 0, 0, 0);
-      if (fresh) {
-        uint4 w = *reinterpret_cast<uint4 *>(v);
-        const bool odd = (finite(w.x) & finite(w.y) & finite(w.z) & finite(w.w)) != ~0u;
-        const uint64_t any = __ballot(odd);
-        if (odd) *reinterpret_cast<uint4 *>(v) = w;
-        if (lane % CH == 0) sOdd[row] = (any >> lane) & ((1ull << CH) - 1) ? 1 : 0;
-      }
+      const int row = (i * NW + wave) * RW + lane / CH;
+      char *const v = sKV + (NB + buf) * TB + row * RB + lane % CH * 16;
+      uint4 w = *reinterpret_cast<uint4 *>(v);
+      const bool odd = (finite(w.x) & finite(w.y) & finite(w.z) & finite(w.w)) != ~0u && base + row >= ctx;
+      const uint64_t any = __ballot(odd);
+      if (odd) *reinterpret_cast<uint4 *>(v) = w;
+      if (lane % CH == 0) sOdd[row] = (any >> lane) & ((1ull << CH) - 1) ? 1 : 0;
     }
   };
 
@@ -423,9 +430,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     }
     return z;
   };
-  // A tile's keys, from position `base` on; ok: which may be read, odd: whose values are not
-  // all finite.
-  auto step = [&](int base, uint64_t ok, uint64_t odd) {
+  // A tile's keys, from position `base` on; ok: which may be read.
+  auto step = [&](int base, uint64_t ok) {
     auto sees = [&] {  // the tile's keys that this lane's row sees
       const int nb = ctx - base;  // so many of them are context
       uint32_t see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
@@ -472,42 +478,12 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
         o[t + 1] = Mma<DT>::run(vf[1], pr[h], o[t + 1]);
       }
     }
-    if (!PREFIX) {
-      while (odd) {  // a key whose values are not all finite: for the rows that see it
-        const int key = __builtin_ctzll(odd);
-        odd &= odd - 1;
-        const int pos = base + key;
-        const int in = pos - (int)(div_by(p.page, pos) * p.page.d);
-        const uint16_t *vp = a.v_cache + table[div_by(p.page, pos)] * a.cache.page +
-                             in * a.cache.token + (int64_t)hk * a.cache.head;
-        float w = 0.0f;  // this row's probability of the key, from the half that holds it
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (16 * h + 8 * (i / 4) + 4 * hw + i % 4 == key) w = (float)pr[h][i];
-        w = sum_halves(w);
-        const bool seen = (sees() >> key) & 1;
-#pragma unroll
-        for (int t = 0; t < NA; ++t)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int d = 32 * t + 8 * b + 4 * hw;
-            uint16_t x[4] = {0, 0, 0, 0};
-            if (d < a.D) *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(vp + d);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float y = w * (float)__builtin_bit_cast(typename Half<DT>::T, x[c]);
-              o[t][4 * b + c] += seen && (x[c] & kExp) == kExp ? y : 0.0f;
-            }
-          }
-      }
-    }
   };
 
   // Tile n is computed from buffer n % 2 while the next one is on its way.  A wave waits for
   // its own loads of tile n, then for the other waves, which are then also done with the buffer
   // that is filled next.
+  uint64_t odd = 0;  // new tokens, by node, whose values are not all finite
   if (k0 < k1) {
     uint64_t next_ok = fetch_tile(0, k0);
     int buf = 0;
@@ -518,15 +494,15 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
       const uint64_t ok = next_ok;
       if (base + KT < k1) next_ok = fetch_tile(buf ^ 1, base + KT);
       __builtin_amdgcn_sched_barrier(0);  // the loads go out before, and nothing below moves up
-      uint64_t odd = 0;
-      if (ok != ~0ull || DP != a.D || (!PREFIX && base + KT > ctx)) {
-        mend(buf, base, ok);
+      if (!PREFIX && base + KT > ctx) {
+        mend(buf, base);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (!PREFIX && base + KT > ctx) odd = __ballot(lane < KT && sOdd[lane % KT]);
+        const uint64_t rows = __ballot(lane < KT && sOdd[lane % KT]);
+        odd |= base >= ctx ? rows << (base - ctx) : rows >> (ctx - base);
       }
-      step(base, ok, odd);
+      step(base, ok);
       // the next buffer's offsets
       const int d = buf ? -TB : TB;
       buf ^= 1;
@@ -538,6 +514,25 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
         va[t][1] += d;
       }
     }
+  }
+  while (!PREFIX && odd) {
+    // of a value that is not finite any share is not finite either
+    const int node = __builtin_ctzll(odd), pos = ctx + node;
+    odd &= odd - 1;
+    const int block = div_by(p.page, pos);
+    const uint16_t *vp = vbase + table[block] * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token;
+    const bool seen = (bits >> node) & 1;
+#pragma unroll
+    for (int t = 0; t < NA; ++t)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int d = 32 * t + 8 * b + 4 * hw;
+        uint16_t x[4] = {0, 0, 0, 0};
+        if (d < a.D) *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(vp + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          o[t][4 * b + c] += seen && (x[c] & kExp) == kExp ? (float)__builtin_bit_cast(typename Half<DT>::T, x[c]) : 0.0f;
+      }
   }
   if (bad_page) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
   l = sum_halves(l);
@@ -606,62 +601,65 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
 }
 
 // ---------------------------------------------------------------------------------
-// The parts of a row joined: a workgroup per row of out.  Groups of D/4 lanes (rounded up to
-// a power of two) take every so many parts, four loads at a time, and their sums meet in LDS, in a
-// fixed order.  Bound by reading the parts: 1024 rows x 64 parts of 128 (34 MB) 12 us; a
-// wave per row, part after part, took 49.
+// The parts of a row joined.  Groups of D/4 lanes (rounded up to a power of two) take a row's
+// parts, `per` groups to a row, each every per-th of them, four loads in flight; their sums
+// meet in LDS, in a fixed order.  Bound by reading the parts: 1024 rows x 64 parts of 128
+// (34 MB) 12 us with 8 groups to a row; a wave per row, part after part, took 49.
+// 21,168 rows x 4 parts of 96 took 13 us with one group to a row, 42 with 8.
 // ---------------------------------------------------------------------------------
 constexpr int kJoinBlock = 256;
+inline int join_width(int D) { return D <= 64 ? 16 : D <= 128 ? 32 : 64; }
 
 template <int DT>
-__global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p, int64_t rows) {
+__global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p, int64_t rows, int width, int per) {
   typedef typename Half<DT>::V4 V4;
   typedef float f32x4 __attribute__((ext_vector_type(4)));
   __shared__ f32x4 sums[kJoinBlock];
-  const int tid = threadIdx.x, lane = tid % kWave;
-  int width = 1;  // lanes of a group
-  while (4 * width < a.D) width *= 2;
-  const int groups = kJoinBlock / width, group = tid / width, d = 4 * (tid % width);
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  const int tid = threadIdx.x, group = tid / width, wl = tid % width, d = 4 * wl;
+  const int sub = group % per, some = kJoinBlock / width / per;  // this group's place, rows of a workgroup
+  for (int64_t r0 = (int64_t)blockIdx.x * some; r0 < rows; r0 += (int64_t)gridDim.x * some) {
+    const int64_t r = min(r0 + group / per, rows - 1);
     const int64_t t = r / a.Hq;
     const int s = (int)(t / a.R), j = (int)(t - (int64_t)s * a.R);
-    const Seq sq = seq_of(a, s);
-    if (j >= sq.nodes) continue;
+    const bool live = r0 + group / per < rows && j < seq_of(a, s).nodes;
     const int first = p.prefix.splits > 0 && p.shared_len[s / a.N] > 0 ? 0 : p.prefix.splits;
-    const int parts = p.prefix.splits + p.suffix.splits;
+    const int parts = live ? p.prefix.splits + p.suffix.splits : 0;
+    auto stat = [&](int i) { return *reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r)); };
     float m = kNegInf;
-    for (int i = first + lane; i < parts; i += kWave) {
-      const float2 ml = *reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r));
+    for (int i = first + wl; i < parts; i += width) {
+      const float2 ml = stat(i);
       m = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
     }
-    m = wave_max_f32(m);
+    for (int o = width / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor(m, o, kWave));
     auto factor = [&](float2 ml) { return ml.y == 0.0f || ml.x == kNegInf ? 0.0f : fast_exp2(ml.x - m); };
     float l = 0.0f;
-    for (int i = first + lane; i < parts; i += kWave) {
-      const float2 ml = *reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r));
+    for (int i = first + wl; i < parts; i += width) {
+      const float2 ml = stat(i);
       l = fmaf(ml.y, factor(ml), l);
     }
-    l = wave_sum_f32(l);
+    for (int o = width / 2; o > 0; o /= 2) l += __shfl_xor(l, o, kWave);
     f32x4 acc = {};
 #pragma unroll 4
-    for (int i = first + group; i < parts; i += groups) {
-      const float f = factor(*reinterpret_cast<const float2 *>(p.ml + 2 * (i * rows + r)));
+    for (int i = first + sub; i < parts; i += per) {
+      const float2 ml = stat(i);
+      const float f = factor(ml);
       // an empty part is not written: what lies there is not used
       const f32x4 x = *reinterpret_cast<const f32x4 *>(p.acc + (i * rows + r) * a.D + (d < a.D ? d : 0));
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[c] = f != 0.0f ? fmaf(x[c], f, acc[c]) : acc[c];
+      for (int c = 0; c < 4; ++c) acc[c] = ml.y != 0.0f ? fmaf(x[c], f, acc[c]) : acc[c];
     }
-    sums[tid] = acc;
-    __syncthreads();
-    if (group == 0) {
-      for (int g = 1; g < groups; ++g) acc += sums[g * width + tid];
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      acc *= inv;
-      if (d < a.D)
-        *reinterpret_cast<uint2 *>(a.out + r * a.D + d) = __builtin_bit_cast(uint2, __builtin_convertvector(acc, V4));
+    if (per > 1) {
+      sums[tid] = acc;
+      __syncthreads();
+      if (sub == 0)
+        for (int g = 1; g < per; ++g) acc += sums[g * width + tid];
+      __syncthreads();
     }
-    if (a.lse && tid == 0) a.lse[r] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
-    __syncthreads();
+    if (sub > 0 || !live) continue;
+    acc *= l == 0.0f ? 0.0f : 1.0f / l;
+    if (d < a.D)
+      *reinterpret_cast<uint2 *>(a.out + r * a.D + d) = __builtin_bit_cast(uint2, __builtin_convertvector(acc, V4));
+    if (a.lse && wl == 0) a.lse[r] = l == 0.0f ? kNegInf : (float)(((double)m + (double)log2f(l)) * kLn2);
   }
 }
 
@@ -686,8 +684,14 @@ void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStr
     launch_part<DT, DP, true>(a, p, stream);
   }
   launch_part<DT, DP, false>(a, p, stream);
-  if (p.suffix.splits > 1)
-    hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(rows, kJoinBlock)), dim3(kJoinBlock), 0, stream, a, p, rows);
+  if (p.suffix.splits > 1) {
+    // four parts or more to a group
+    const int width = join_width(a.D), parts = p.prefix.splits + p.suffix.splits;
+    int per = 1;
+    while (per < kJoinBlock / width && 8 * per <= parts) per *= 2;
+    hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(ceil_div(rows * per * width, kJoinBlock), kJoinBlock)),
+                       dim3(kJoinBlock), 0, stream, a, p, rows, width, per);
+  }
 }
 
 }  // namespace

@@ -259,6 +259,42 @@ def test_a_node_that_a_row_does_not_see_cannot_reach_it(poison, R):
         assert torch.equal(got[1][s, others[s]], c.lse[s, others[s]]), s
 
 
+@pytest.mark.parametrize("bs", [1, 2])
+@pytest.mark.parametrize("N,shared", [(1, 0), (3, 700)])
+def test_a_context_of_many_small_pages(bs, N, shared):
+    Case(N=N, R=5, D=128, lens=(1000, 777, 2077), bs=bs, shared=shared).call().check()
+
+
+@pytest.mark.parametrize("D", [136, 256])
+@pytest.mark.parametrize("R", [1, 9, 40])
+@pytest.mark.parametrize("N,shared", [(1, 0), (4, 512)])
+def test_wide_heads_over_split_contexts(D, R, N, shared):
+    Case(N=N, R=R, Hq=8, Hkv=2, D=D, lens=(3000, 513), shared=shared, tree=R > 1, layout="head").call().check()
+
+
+@pytest.mark.parametrize("D", [24, 64, 96, 200])
+@pytest.mark.parametrize("L", [600, 1500, 9000])
+def test_parts_of_several_numbers(D, L):
+    Case(B=2, N=3, R=2, D=D, lens=(L, L - 99), shared=L // 2, nodes=(2, 1, 0)).call().check()
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("L", [5, 30, 3000])
+def test_a_value_that_is_not_finite_is_seen_by_its_rows(poison, L):
+    """Node 1's value holds one element that is not finite: node 0 does not see it, nodes 1 and
+    2 do, at every head of that key/value head."""
+    c = Case(R=3, Hq=4, Hkv=2, D=64, lens=(L,))
+    at = c.tables[0, (L + 1) // c.bs].long()
+    c.v[at, (L + 1) % c.bs, 1, 37] = poison
+    c.call()
+    out = c.out[0].float()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[:, :2]).all()
+    hit = out[1:, 2:, 37]
+    assert (torch.isnan(hit) if math.isnan(poison) else hit == poison).all()
+    rest = torch.cat([out[1:, 2:, :37], out[1:, 2:, 38:]], -1)
+    assert torch.isfinite(rest).all()
+
+
 def test_infinite_scores():
     # A key that scores +inf against a positive query makes its rows NaN; -inf leaves them out.
     c = Case(B=1, N=1, R=1, Hq=1, Hkv=1, D=64, lens=(40,))
