@@ -24,6 +24,10 @@ constexpr int kLpTileVecsMax = kLpBlock * kLpUnroll * 2;  // 64 KiB of logits
 constexpr int kLpTilesWanted = 2048;                  // 8 workgroups for each of 256 CUs
 constexpr int kLpSupers = 1024;                       // segments (or runs of them) ranked per row
 constexpr int kLpCands = 1024;
+// More than half of that at or above the bound that the slots' maxima give (as where a row has
+// hardly more slots than k): the bound is formed again from the maxima of vectors, kept where
+// the candidates go.  One row of 11,788 bf16, k = 32: 31 us, and 429 by the count over all bits.
+constexpr int kLpUnits = 2 * kLpCands;
 
 struct LpGeom {
   int tiles, tile_vecs, segs;  // segs: body segments of a row; with the head and the tail, segs + 2
@@ -314,16 +318,18 @@ __device__ __forceinline__ int slot_start(const LpRow<DT> &row, int segs, int j,
 
 constexpr int kLpSmall = 256;  // slots of a row that one wave ranks with 4 keys a lane
 
-// KREGS: keys of a lane of the wave that ranks the slots (4 or kLpSupers / 64).
+// KREGS: keys of a lane of the wave that ranks the slots (4 or kLpSupers / 64).  Registers for five
+// workgroups of a unit: 32 us for 2560 rows of 128,256, k = 20, against 39 with four, 36 with six
+// (which spill).
 template <int DT, int KREGS>
-__global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom g, int64_t rows,
+__global__ __launch_bounds__(kLpBlock, KREGS == 4 ? 5 : 3) void k_lp_finalize(LogprobsArgs a, LpGeom g, int64_t rows,
                                                           const float4 *__restrict__ part,
                                                           const int *__restrict__ segkey) {
   constexpr int EPV = Elt<DT>::kPerVec;
   constexpr int W = kLpBlock / kWave;
   __shared__ int2 cand[kLpCands];
   __shared__ int sel[kMaxTop];
-  __shared__ int s_nsel, s_ncand, s_count, s_key;
+  __shared__ int s_nsel, s_ncand, s_count, s_key, s_bits[32];
   __shared__ double s_max, s_ln;  // a row's largest logit, and ln of the sum relative to it
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int k = a.k;
@@ -418,10 +424,10 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
     if (gathers && g0 < a.C) gather(g0);
     __syncthreads();
     if (k > 0) {
-      const int T = s_key;
-      const float bound = unordered(T);
+      int T = s_key;
+      float bound = unordered(T);
       const int nsel = s_nsel;
-      // Candidates: a wave's lanes count theirs, one lane takes places for all.
+      // Candidates' ids: a wave's lanes count theirs, one lane takes places for all.
       auto offer = [&](uint32_t mine, auto value) {
         if (!__any(mine)) return;
         const int n = __popc(mine), upto = wave_inclusive_scan(n);
@@ -431,13 +437,13 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         while (mine) {
           const int b = __builtin_ctz(mine);
           mine &= mine - 1;
-          if (at < kLpCands) cand[at] = value(b);
+          if (at < kLpCands) cand[at].y = value(b);
           ++at;
         }
       };
       auto offer_one = [&](bool in, int id) {
         const float x = in ? Elt<DT>::load(row.p, id) : kNegInf;
-        offer(in && ordered(x) >= T ? 1u : 0u, [&](int) { return make_int2(ordered(x), id); });
+        offer(in && ordered(x) >= T ? 1u : 0u, [&](int) { return id; });
       };
       auto vec_bits = [&](const uint4 &w) {
         float x[EPV];
@@ -448,47 +454,97 @@ __global__ __launch_bounds__(kLpBlock) void k_lp_finalize(LogprobsArgs a, LpGeom
         return m;
       };
       auto load_vec = [&](int e) { return *reinterpret_cast<const uint4 *>(row.p + (int64_t)e * Elt<DT>::kBytes); };
-      // each wave reads its share of the slots, several at a time where a slot is one vector
-      // a lane
-      constexpr int kBatch = 4;
-      for (int q0 = wave; q0 < nsel; q0 += W * kBatch) {
-        uint4 w[kBatch];
-        int at[kBatch];
+      // The k-th largest of the maxima of the selected slots' vectors (or of runs of them), as of
+      // the slots above: at least k elements reach it, and without ties at most k vectors' can.
+      auto refine = [&] {
+        int *const key = reinterpret_cast<int *>(cand);
+        const int each = run * kWave, vecs = nsel * each;
+        const int per = (vecs + kLpUnits - 1) / kLpUnits, units = (vecs + per - 1) / per;
+#pragma unroll 1
+        for (int u = tid; u < units; u += kLpBlock) {
+          int most = kKeyNegInf;
+#pragma unroll 1
+          for (int v = u * per; v < min(u * per + per, vecs); ++v) {
+            const int slot = sel[v / each] * run;
+            const int e = max(slot_start<DT>(row, g.segs, slot, a.V), row.head) + v % each * EPV;
+            if (e >= min(slot_start<DT>(row, g.segs, slot + run, a.V), row.a1)) continue;
+            float x[EPV];
+            Elt<DT>::unpack(load_vec(e), x);
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const int i = q0 + q * W;
-          at[q] = -1;
-          if (i >= nsel) continue;
-          const int b0 = max(slot_start<DT>(row, g.segs, sel[i] * run, a.V), row.head) + lane * EPV;
-          const int b1 = min(slot_start<DT>(row, g.segs, sel[i] * run + run, a.V), row.a1);
-          if (b0 < b1) {
-            at[q] = b0;
-            w[q] = load_vec(b0);
+            for (int i = 0; i < EPV; ++i) most = max(most, ordered(x[i]));
+          }
+          key[u] = most;
+        }
+        if (tid < 32) s_bits[tid] = 0;
+        __syncthreads();
+        uint32_t K = 0;
+        for (int b = 31; b >= (DT == SMCSD_DTYPE_BF16 ? 16 : 0); --b) {
+          const int t = (int)((K | (1u << b)) ^ 0x80000000u);
+          int n = 0;
+          for (int u = tid; u < units; u += kLpBlock) n += key[u] >= t;
+          n = wave_inclusive_scan(n);
+          if (lane == kWave - 1) atomicAdd(&s_bits[b], n);
+          __syncthreads();
+          if (s_bits[b] >= k) K |= 1u << b;
+        }
+        T = max((int)(K ^ 0x80000000u), kKeyNegInf + 1);
+        bound = unordered(T);
+        if (tid == 0) s_ncand = 0;
+        __syncthreads();
+      };
+      int nc;
+      // a bound that nothing is below, as where the row has fewer slots than k, is formed again at once
+      const bool fine = T > kKeyNegInf + 1 || nsel * run * kWave * EPV <= kLpCands / 2;
+      for (bool again = false;; again = true) {
+        if (again || !fine) {
+          refine();
+          again = true;
+        }
+        // each wave reads its share of the slots, several at a time where a slot is one vector
+        // a lane
+        constexpr int kBatch = 4;
+        for (int q0 = wave; q0 < nsel; q0 += W * kBatch) {
+          uint4 w[kBatch];
+          int at[kBatch];
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const int i = q0 + q * W;
+            at[q] = -1;
+            if (i >= nsel) continue;
+            const int b0 = max(slot_start<DT>(row, g.segs, sel[i] * run, a.V), row.head) + lane * EPV;
+            const int b1 = min(slot_start<DT>(row, g.segs, sel[i] * run + run, a.V), row.a1);
+            if (b0 < b1) {
+              at[q] = b0;
+              w[q] = load_vec(b0);
+            }
+          }
+          uint32_t mine = 0;
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)
+            if (at[q] >= 0) mine |= vec_bits(w[q]) << (EPV * q);
+          offer(mine, [&](int b) {
+            const int q = b / EPV;
+            return (q == 0 ? at[0] : q == 1 ? at[1] : q == 2 ? at[2] : at[3]) + b % EPV;
+          });
+          for (int i = q0; i < min(nsel, q0 + W * kBatch); i += W) {
+            const int e0 = slot_start<DT>(row, g.segs, sel[i] * run, a.V);
+            const int e1 = slot_start<DT>(row, g.segs, sel[i] * run + run, a.V);
+            if (e0 < row.head) offer_one(e0 + lane < min(e1, row.head), e0 + lane);
+            if (e1 > row.a1) offer_one(max(e0, row.a1) + lane < e1, max(e0, row.a1) + lane);
+            for (int e = max(e0, row.head) + kWave * EPV; e < min(e1, row.a1); e += kWave * EPV) {
+              const int m0 = e + lane * EPV;
+              const uint32_t m = m0 < min(e1, row.a1) ? vec_bits(load_vec(m0)) : 0;
+              offer(m, [&](int b) { return m0 + b; });
+            }
           }
         }
-        uint32_t mine = 0;
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-          if (at[q] >= 0) mine |= vec_bits(w[q]) << (EPV * q);
-        offer(mine, [&](int b) {
-          const int q = b / EPV;
-          const int id = (q == 0 ? at[0] : q == 1 ? at[1] : q == 2 ? at[2] : at[3]) + b % EPV;
-          return make_int2(ordered(Elt<DT>::load(row.p, id)), id);
-        });
-        for (int i = q0; i < min(nsel, q0 + W * kBatch); i += W) {
-          const int e0 = slot_start<DT>(row, g.segs, sel[i] * run, a.V);
-          const int e1 = slot_start<DT>(row, g.segs, sel[i] * run + run, a.V);
-          if (e0 < row.head) offer_one(e0 + lane < min(e1, row.head), e0 + lane);
-          if (e1 > row.a1) offer_one(max(e0, row.a1) + lane < e1, max(e0, row.a1) + lane);
-          for (int e = max(e0, row.head) + kWave * EPV; e < min(e1, row.a1); e += kWave * EPV) {
-            const int m0 = e + lane * EPV;
-            const uint32_t m = m0 < min(e1, row.a1) ? vec_bits(load_vec(m0)) : 0;
-            offer(m, [&](int b) { return make_int2(ordered(Elt<DT>::load(row.p, m0 + b)), m0 + b); });
-          }
-        }
+        __syncthreads();
+        nc = s_ncand;
+        if (again || nc <= kLpCands / 2 || isnan(s_ln)) break;
+        __syncthreads();
       }
+      for (int i = tid; i < min(nc, kLpCands); i += kLpBlock) cand[i].x = ordered(Elt<DT>::load(row.p, cand[i].y));
       __syncthreads();
-      int nc = s_ncand;
       if (nc > kLpCands && !isnan(s_ln)) {
         // Too many elements at or above the bound (long runs of equal logits): the k-th
         // largest element itself, then the smallest ids among its equals, each bit by bit.

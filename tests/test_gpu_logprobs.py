@@ -96,6 +96,17 @@ def test_alternatives(k, n):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,k", [(1, 11789, 32), (3, 1502, 64), (2, 6807, 33), (9, 409, 32), (2, 16900, 64), (1, 40001, 64)])
+@pytest.mark.parametrize("steps", [0, 40])
+def test_more_alternatives_than_segments(dt, n, V, k, steps):
+    """Rows of fewer segments than alternatives, or hardly more; with `steps`, of few distinct values."""
+    x = logits(n, V, dt, 1)
+    if steps:
+        x[:, :V] = (x[:, :V].float() * (steps / 8)).round().clamp(-steps / 2, steps / 2).to(x.dtype)
+    check(call(x, V, 0.8, k=k), x, V, 0.8)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_many_rows(dt):
     n, V = 700, 33000
     x, t = logits(n, V, dt, 5, sigma=1.0), some(n, V, 3)
