@@ -4,8 +4,9 @@
 //
 // All but the copy are integer work on the refcounted block-table state (SMC explainers,
 // "system optimisation design": shared blocks, released by reference count) and are bound
-// by the latency of a few launches; the order of every list they leave is fixed by block
-// ids alone, so the state does not depend on the order of the atomics.
+// by the latency of a few launches (512 tables of 133 blocks, a pool of 24,576: fork 3.7 us,
+// free 3.7 + 2.2 + 2.9 us, compact 4.5 + 4.6 + 4.7 us); the order of every list they leave is
+// fixed by block ids alone, so the state does not depend on the order of the atomics.
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "internal.hpp"
@@ -15,20 +16,18 @@ namespace smcsd {
 namespace {
 
 constexpr int kPgBlock = 256;
-// Blocks of a thread in the kernels over the pool, consecutive ones.  A workgroup adds up the
-// counts of the other workgroups' groups, so large pools take more blocks to a thread; with
-// 4, a pool of 24576 blocks is counted in 3.5 us instead of 9.7 us with 32 (three groups
-// keep only three workgroups busy).
-constexpr int kFewPerThread = 4, kManyPerThread = 32;
-constexpr int64_t kManyBlocks = 1 << 20;
-inline int per_thread(int64_t P) { return P <= kManyBlocks ? kFewPerThread : kManyPerThread; }
+// Consecutive blocks of a thread in the kernels over the pool.  A workgroup adds up the counts of
+// all other workgroups' groups, which larger groups would make fewer, but 32 to a thread lose
+// at every size measured: count and rank of 24,576 blocks 19 us against 7, of 8 million 226
+// against 45 (a thread's neighbours are then 128 bytes away).
+constexpr int kPerThread = 4;
 
-// Bit i: `is` holds for the count of block b0 + i (b0 a multiple of PT).
-template <int PT, typename F>
+// Bit i: `is` holds for the count of block b0 + i (b0 a multiple of kPerThread).
+template <typename F>
 __device__ __forceinline__ uint32_t block_bits(const int32_t *rc, int64_t b0, int64_t P, F is) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < PT; i += 4) {
+  for (int i = 0; i < kPerThread; i += 4) {
     int32_t v[4] = {0, 0, 0, 0};
     if (b0 + i + 4 <= P) {
 #pragma unroll
@@ -124,14 +123,13 @@ __global__ __launch_bounds__(kPgBlock) void k_free_drop(const int32_t *__restric
 }
 
 // Workgroup g counts group g's freed blocks; workgroup 0 keeps the old top for the push.
-template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_free_count(const int32_t *__restrict__ rc, int64_t P,
                                                          const int32_t *__restrict__ free_top,
                                                          int32_t *__restrict__ gcount,
                                                          int32_t *__restrict__ old_top) {
   __shared__ int lds[kPgBlock / kWave];
-  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * PT;
-  const int total = block_sum<int, kPgBlock>(__popc(block_bits<PT>(rc, b0, P, is_freed)), lds);
+  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * kPerThread;
+  const int total = block_sum<int, kPgBlock>(__popc(block_bits(rc, b0, P, is_freed)), lds);
   if (threadIdx.x == 0) {
     gcount[blockIdx.x] = total;
     if (blockIdx.x == 0) *old_top = *free_top;
@@ -140,7 +138,6 @@ __global__ __launch_bounds__(kPgBlock) void k_free_count(const int32_t *__restri
 
 // Workgroup g pushes group g's freed blocks: a block's place is the old top plus the number
 // of freed blocks with higher ids (those of later groups, then those above it here).
-template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc, int64_t P, int groups,
                                                         const int32_t *__restrict__ gcount,
                                                         const int32_t *__restrict__ old_top,
@@ -149,8 +146,8 @@ __global__ __launch_bounds__(kPgBlock) void k_free_push(int32_t *__restrict__ rc
                                                         int32_t *__restrict__ status) {
   __shared__ int lds[kPgBlock / kWave];
   const int g = blockIdx.x;
-  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * PT;
-  uint32_t m = block_bits<PT>(rc, b0, P, is_freed);
+  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * kPerThread;
+  uint32_t m = block_bits(rc, b0, P, is_freed);
   const int mine = gcount[g];
   if (mine == 0 && g != 0) return;
   int later = 0;
@@ -187,12 +184,11 @@ constexpr int32_t kMapDead = -1, kMapStay = -2;
 
 __device__ __forceinline__ bool is_live(int32_t r) { return r > 0; }
 
-template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_compact_count(const int32_t *__restrict__ rc, int64_t P,
                                                             int32_t *__restrict__ gcount) {
   __shared__ int lds[kPgBlock / kWave];
-  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * PT;
-  const int total = block_sum<int, kPgBlock>(__popc(block_bits<PT>(rc, b0, P, is_live)), lds);
+  const int64_t b0 = ((int64_t)blockIdx.x * kPgBlock + threadIdx.x) * kPerThread;
+  const int total = block_sum<int, kPgBlock>(__popc(block_bits(rc, b0, P, is_live)), lds);
   if (threadIdx.x == 0) gcount[blockIdx.x] = total;
 }
 
@@ -200,14 +196,13 @@ struct CompactWs {
   int32_t *gcount, *meta, *map, *holes, *movers;  // meta: live blocks, moves
 };
 
-template <int PT>
 __global__ __launch_bounds__(kPgBlock) void k_compact_rank(int32_t *__restrict__ rc, int64_t P,
                                                            int groups, CompactWs w,
                                                            int32_t *__restrict__ move_count) {
   __shared__ int lds[kPgBlock / kWave];
   const int g = blockIdx.x;
-  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * PT;
-  const uint32_t m = block_bits<PT>(rc, b0, P, is_live);
+  const int64_t b0 = ((int64_t)g * kPgBlock + threadIdx.x) * kPerThread;
+  const uint32_t m = block_bits(rc, b0, P, is_live);
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < groups; i += kPgBlock) {
     const int c = w.gcount[i];
@@ -222,7 +217,7 @@ __global__ __launch_bounds__(kPgBlock) void k_compact_rank(int32_t *__restrict__
     w.meta[0] = n;
     if (n == P) w.meta[1] = *move_count = 0;
   }
-  for (int i = 0; i < PT; ++i) {
+  for (int i = 0; i < kPerThread; ++i) {
     const int64_t b = b0 + i;
     if (b >= P) break;
     const int rank = before + __popc(m & ((1u << i) - 1));  // live blocks below b
@@ -286,7 +281,10 @@ struct CopyCaches {
 constexpr int kCopyUnroll = 4;
 constexpr uint32_t kCopyWords = 1 << 20;
 
-// Workgroup = one (entry, cache) at a time, over all segments.  W: bytes moved at once.
+// Workgroup = one (entry, cache) at a time, over all segments, four words of a thread in flight.
+// W: bytes moved at once.  Bound by memory: 1.6 GB of a compaction's moves take 320 us (5.0 TB/s
+// read and written, the rate of a large copy); 67 MB of copy-on-write tails 26 us (2.6 TB/s, their
+// pages lie scattered and each is a few KB).
 template <typename W>
 __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, int n_caches, int64_t block_stride,
                                                    int segments, int64_t segment_stride,
@@ -334,7 +332,7 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, int n_cach
   }
 }
 
-inline int64_t groups_of(int64_t P) { return ceil_div(P, kPgBlock * per_thread(P)); }
+inline int64_t groups_of(int64_t P) { return ceil_div(P, kPgBlock * kPerThread); }
 
 }  // namespace
 
@@ -360,13 +358,9 @@ hipError_t launch_kv_free(const int32_t *freed, int64_t S, int32_t *T, int M, in
   int32_t *gcount = reinterpret_cast<int32_t *>(ws), *old_top = gcount + groups;
   hipLaunchKernelGGL(k_free_drop, dim3(grid_blocks(S * cols, kPgBlock)), dim3(kPgBlock), 0, stream, freed, S,
                      T, M, rc, P, status, cols);
-  auto rest = [&](auto count, auto push) {
-    hipLaunchKernelGGL(count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, free_top, gcount, old_top);
-    hipLaunchKernelGGL(push, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, gcount, old_top, fl, free_top,
-                       status);
-  };
-  if (per_thread(P) == kFewPerThread) rest(k_free_count<kFewPerThread>, k_free_push<kFewPerThread>);
-  else rest(k_free_count<kManyPerThread>, k_free_push<kManyPerThread>);
+  hipLaunchKernelGGL(k_free_count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, free_top, gcount, old_top);
+  hipLaunchKernelGGL(k_free_push, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, gcount, old_top, fl, free_top,
+                     status);
   return hipGetLastError();
 }
 
@@ -382,12 +376,8 @@ hipError_t launch_kv_compact(int32_t *T, int64_t S, int M, int block_size, int32
   w.map = reinterpret_cast<int32_t *>(lists);
   w.holes = reinterpret_cast<int32_t *>(lists + list);
   w.movers = reinterpret_cast<int32_t *>(lists + 2 * list);
-  auto first = [&](auto count, auto rank) {
-    hipLaunchKernelGGL(count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, w.gcount);
-    hipLaunchKernelGGL(rank, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, w, move_count);
-  };
-  if (per_thread(P) == kFewPerThread) first(k_compact_count<kFewPerThread>, k_compact_rank<kFewPerThread>);
-  else first(k_compact_count<kManyPerThread>, k_compact_rank<kManyPerThread>);
+  hipLaunchKernelGGL(k_compact_count, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, w.gcount);
+  hipLaunchKernelGGL(k_compact_rank, dim3(groups), dim3(kPgBlock), 0, stream, rc, P, groups, w, move_count);
   const int64_t most = std::max<int64_t>(S * M, P);
   hipLaunchKernelGGL(k_compact_apply, dim3(grid_blocks(ceil_div(most, kPgBlock), kPgBlock)), dim3(kPgBlock),
                      0, stream, T, S * M, block_size, rc, P, w, fl, free_top, moves, status);

@@ -9,7 +9,10 @@
 // they lie in the k segments with the largest maxima (ordered like the elements: by value,
 // then by place), because each of those k segments holds an element that precedes all
 // elements of any other segment; only they are read again.
-// Bound by memory: V logits in, one float per 1 KiB of them out.
+// Bound by memory: V logits in, one float per 1 KiB of them out.  2560 rows of 128,256 bf16, k = 20:
+// 114 us for the stream (5.8 TB/s) and 31 us for the rest, which is latency: a row's steps follow
+// one another, and five workgroups of a unit hide little of it.  576 rows of 152,063 fp32 with
+// masked logits: 62 us (5.6 TB/s) and 19 us.
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "internal.hpp"

@@ -5,7 +5,9 @@
 // head of D elements belongs to a group of lanes of 8 elements (16 bytes) each: the sum of
 // squares is a butterfly over the group, and the rotation's partner elements lie in the same
 // lane (interleaved pairs) or in the lane rot_dim/16 away (pairs i, i + rot_dim/2), so
-// nothing goes through LDS.  Bound by memory: each head is read once and written once.
+// nothing goes through LDS.  Bound by memory: each head is read once and written once; 2560
+// tokens of 32 + 2 x 8 heads of 128 (63 MB) take 20.5 us (3.1 TB/s, launch and first loads included),
+// 12 tokens of 8 + 2 x 2 heads of 64 take 3.8 us.
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "half.hpp"

@@ -80,8 +80,13 @@ constexpr int kRowsWave = 32;
 // in flight, the workgroups lose that no longer fit beside each other.
 constexpr int KT = 32, NB = 2;
 constexpr int kWavesMax = 4;      // two workgroups of four waves fill a compute unit's registers
-constexpr int kPartItems = 1024;  // workgroups that the splits of a launch aim at
-constexpr int kMinShared = 128;   // shorter shared prefixes are read per particle
+// Workgroups that the splits of a launch aim at: 64 rows x 16 heads over 131,071 keys take 120 us
+// and 12 to join the parts with 1024, 161 + 8 with 512, 136 + 22 with 2048.
+constexpr int kPartItems = 1024;
+// Shorter shared prefixes are read by every particle (the caches hold them): 512 sequences of 5 x
+// 32 heads with 128 shared keys take 67 us so and 85 to 89 with a pass of their own, with 256 keys
+// 94 against 93 to 107, and from there on the pass wins (2048 keys: 240 us against 482).
+constexpr int kMinShared = 256;
 
 // How the rows of one key/value head and the keys are cut: `tiles` workgroups of `waves`
 // waves over the rows, `splits` over the keys.
@@ -237,6 +242,13 @@ constexpr float kLag = 8.0f;
 __device__ const uint32_t kNothing[4] = {0, 0, 0, 0};  // loaded where there is nothing to load
 
 // DP: head size padded to 64, 128 or 256.  NW: waves.
+// Measured, bf16, heads of 128: 32 prompts of 16 x 5 rows x 32 heads over 2048 shared keys, the
+// shared pass 150 us (570 TFLOP/s: bound by a wave's chain of product, exponentials and product;
+// its arithmetic alone takes 112 us, its loads alone 71) and the particles' own keys 76 us;
+// 64 rows x 16 heads over 131,071 keys 120 us (570 TFLOP/s); 256 sequences of 9 x 32 heads over up
+// to 4093 keys, 3.2 GB of pages, 660 us (4.9 TB/s: bound by the loads, which without any
+// arithmetic take 640 us, whatever the pages' order and the bytes in flight); f16, heads of 64,
+// one token of 4 sequences of 16 keys 6 us, all of it latency.
 template <int DT, int DP, int NW, bool PREFIX>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
