@@ -246,8 +246,8 @@ __device__ const uint32_t kNothing[4] = {0, 0, 0, 0};  // loaded where there is 
 // shared pass 150 us (570 TFLOP/s: bound by a wave's chain of product, exponentials and product;
 // its arithmetic alone takes 112 us, its loads alone 71) and the particles' own keys 76 us;
 // 64 rows x 16 heads over 131,071 keys 120 us (570 TFLOP/s); 256 sequences of 9 x 32 heads over up
-// to 4093 keys, 3.2 GB of pages, 660 us (4.9 TB/s: bound by the loads, which without any
-// arithmetic take 640 us, whatever the pages' order and the bytes in flight); f16, heads of 64,
+// to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
+// any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 6 us, all of it latency.
 template <int DT, int DP, int NW, bool PREFIX>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttnArgs a, Plan p) {
@@ -330,6 +330,12 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
     const uint64_t rows = __ballot(ok);
     const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
     constexpr int NAT = NLD < 4 ? NLD : 4;  // looked up together
+    // Up to 64 rows are one workgroup's, and it alone reads its keys: past the caches (nt).  256
+    // sequences of 9 x 32 heads, 3.2 GB, 608 us against 660, of one x 32 heads 577 against 628, 16
+    // of 30,000 keys 264 against 297; where particles share fewer than kMinShared keys it costs
+    // (128 keys, 512 sequences: 70 against 67).  More rows are several workgroups', of the same keys:
+    // 64 x 16 heads over 131,071 keys took 134 us with it, 130 without.
+    constexpr int kPolicy = NW < 4 ? 2 : 0;
 #pragma unroll
     for (int i0 = 0; i0 < NLD; i0 += NAT) {
       int64_t at[NAT];
@@ -342,8 +348,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
         const bool in = at[i] >= 0 && chunk * 8 < a.D;
         const uint16_t *const k = in ? kbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
         const uint16_t *const v = in ? vbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
-        __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * RB), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * RB), 16, 0, kPolicy);
+        __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, kPolicy);
       }
     }
     return rows;
