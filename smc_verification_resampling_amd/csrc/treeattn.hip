@@ -100,7 +100,7 @@ inline Cut cut_of(int rows, int64_t heads, int64_t max_len) {
   c.rows = rows;
   const int most = kWavesMax * kRowsWave;
   c.tiles = (int)ceil_div(rows, most);
-  c.tile_rows = (int)ceil_div(rows, c.tiles);
+  c.tile_rows = (int)ceil_div(ceil_div(rows, c.tiles), kRowsWave) * kRowsWave;  // whole waves
   c.waves = c.tile_rows <= kRowsWave ? 1 : c.tile_rows <= 2 * kRowsWave ? 2 : kWavesMax;
   // enough workgroups to fill the chip, but a split's keys outweigh the part it leaves
   const int64_t most_splits = ceil_div(max_len, std::max(256, 4 * std::min(rows, most)));
@@ -250,7 +250,7 @@ __device__ const uint32_t kNothing[4] = {0, 0, 0, 0};  // loaded where there is 
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 6 us, all of it latency.
 template <int DT, int DP, int NW, bool PREFIX>
-__global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttnArgs a, Plan p) {
+__global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
   constexpr int CH = DP / 8;       // 16-byte chunks of a row
@@ -502,6 +502,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
   // its own loads of tile n, then for the other waves, which are then also done with the buffer
   // that is filled next.
   uint64_t odd = 0;  // new tokens, by node, whose values are not all finite
+  const bool busy = tile * cut.tile_rows + wave * kRowsWave < cut.rows;  // a wave without rows only loads
   if (k0 < k1) {
     uint64_t next_ok = fetch_tile(0, k0);
     int buf = 0;
@@ -520,7 +521,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : 2) void k_attn(TreeAttn
         const uint64_t rows = __ballot(lane < KT && sOdd[lane % KT]);
         odd |= base >= ctx ? rows << (base - ctx) : rows >> (ctx - base);
       }
-      step(base, ok);
+      if (busy) step(base, ok);
       // the next buffer's offsets
       const int d = buf ? -TB : TB;
       buf ^= 1;
