@@ -14,6 +14,10 @@
  * Tecnico" section 2).  The speculative-sampling notes ("Accelerating-Large-Language-
  * Model-Decoding-with-Speculative-Sampling", section 1 and section 4.2) define the
  * secondary SpS mode: modified rejection sampling on the same logits.
+ * Beside that path stand the operators that a target's pass and a server need around it:
+ * the new tokens' way into the paged cache, attention over it, log-probabilities with
+ * alternatives, and the pages' admission, retirement, compaction and copies (the only
+ * entry that copies KV data is smcsd_kv_copy, which runs the lists that others write).
  *
  * Conventions for every entry point
  *   - Array arguments are DEVICE pointers owned by the caller; the library allocates
