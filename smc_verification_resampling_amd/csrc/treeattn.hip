@@ -239,13 +239,13 @@ __device__ __forceinline__ int place_of(int r) {
 // rescale nothing.
 constexpr float kLag = 8.0f;
 
-__device__ const uint32_t kNothing[4] = {0, 0, 0, 0};  // loaded where there is nothing to load
+__device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothing to load
 
 // DP: head size padded to 64, 128 or 256.  NW: waves.
 // Measured, bf16, heads of 128: 32 prompts of 16 x 5 rows x 32 heads over 2048 shared keys, the
-// shared pass 150 us (570 TFLOP/s: bound by a wave's chain of product, exponentials and product;
-// its arithmetic alone takes 112 us, its loads alone 71) and the particles' own keys 76 us;
-// 64 rows x 16 heads over 131,071 keys 120 us (570 TFLOP/s); 256 sequences of 9 x 32 heads over up
+// shared pass 143 us (600 TFLOP/s: bound by a wave's chain of product, exponentials and product;
+// with idle waves in it, 150 us, its arithmetic alone took 112 and its loads alone 71) and the
+// particles' own keys 72 us; 64 rows x 16 heads over 131,071 keys 111 us (620 TFLOP/s); 256 sequences of 9 x 32 heads over up
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 6 us, all of it latency.
@@ -346,8 +346,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
         const int first = ((i0 + i) * NW + wave) * RW;
         const int chunk = (lane % CH) ^ place_of<CH>(first + lane / CH);
         const bool in = at[i] >= 0 && chunk * 8 < a.D;
-        const uint16_t *const k = in ? kbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
-        const uint16_t *const v = in ? vbase + at[i] + chunk * 8 : (const uint16_t *)kNothing;
+        const uint16_t *const k = in ? kbase + at[i] + chunk * 8 : (const uint16_t *)&kNothing;
+        const uint16_t *const v = in ? vbase + at[i] + chunk * 8 : (const uint16_t *)&kNothing;
         __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * RB), 16, 0, kPolicy);
         __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, kPolicy);
       }
