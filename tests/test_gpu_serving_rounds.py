@@ -201,3 +201,92 @@ def test_rounds_of_a_server(dt, layout, side, tau):
         # particles were exchanged, with tau > 1 in every round of every prompt
         assert resampled == 7 * B if tau > 1 else resampled > 0
     stream.synchronize()
+
+
+class Pass:
+    """One round's pass over fixed buffers: write, attend, score."""
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        blocks = -(-(300 + R) // BS)
+        self.tables = torch.randperm(S * blocks, generator=g).int().view(S, blocks).cuda()
+        self.tables[:, :10] = self.tables[::N, :10].repeat_interleave(N, 0)  # prompts share 160 tokens,
+        if seed % 2:
+            self.tables[:, :18] = self.tables[::N, :18].repeat_interleave(N, 0)  # or 288
+        self.k, self.v = (torch.randn(S * blocks, BS, HKV, D, generator=g).bfloat16().cuda() for _ in range(2))
+        self.lens = torch.randint(290, 301, (S,), generator=g, dtype=torch.int32).cuda()
+        self.x = torch.randn(S, R, HQ + 2 * HKV, D, generator=g).bfloat16().cuda()
+        a = torch.arange(blocks * BS).double()[:, None] * 10000.0 ** (-torch.arange(D // 2).double() / (D // 2))
+        self.cos_sin = torch.cat([a.cos(), a.sin()], 1).float().cuda()
+        self.head = (torch.randn(HQ * D, V, generator=g) / 8).bfloat16().cuda()
+        self.q, self.out = (torch.empty(S, R, HQ, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.lse, self.logits = torch.empty(S, R, HQ, device="cuda"), torch.empty(S * R, V, dtype=torch.bfloat16, device="cuda")
+        self.ids, self.top = torch.empty(S * R, 5, **I32), torch.empty(S * R, 5, device="cuda")
+        self.entropy, self.st = torch.empty(S * R, device="cuda"), torch.zeros(1, **I32)
+        self.ws = sm.alloc_workspace(sm.OP_TREE_ATTN, B, N, K=R, V=HQ * D, P=HKV)
+        self.ws_lp = sm.alloc_workspace(sm.OP_LOGPROBS, S * R, 1, K=5, V=V)
+
+    def run(self):
+        x = self.x
+        sm.qk_norm_rope(x[:, :, :HQ], x[:, :, HQ:HQ + HKV], x[:, :, HQ + HKV:], self.lens, self.tables, self.k, self.v, self.q,
+                        self.st, cos_sin=self.cos_sin)
+        sm.tree_attention(self.q, self.k, self.v, self.tables, self.lens, B, N, D ** -0.5, self.out, self.st, self.ws, lse=self.lse)
+        torch.mm(self.out.view(S * R, HQ * D), self.head, out=self.logits)
+        sm.token_logprobs(self.logits, S * R, V, 1.0, self.st, self.ws_lp, out_entropy=self.entropy, top_ids=self.ids, top_logp=self.top)
+
+    def results(self):
+        assert int(self.st) == 0
+        return [t.clone() for t in (self.q, self.out, self.lse, self.logits, self.ids, self.top, self.entropy)]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_passes_at_once():
+    one, two = Pass(1), Pass(2)
+    alone = []
+    for p in (one, two):
+        p.run()
+        torch.cuda.synchronize()
+        alone.append(p.results())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for p in (one, two):
+            p.out.fill_(3.0)
+            p.ids.fill_(-2)
+        torch.cuda.synchronize()
+        for p, s in zip((one, two), streams):
+            with torch.cuda.stream(s):
+                p.run()
+                p.run()
+        torch.cuda.synchronize()
+        assert same(one.results(), alone[0]) and same(two.results(), alone[1])
+
+
+def test_a_captured_pass():
+    p = Pass(1)
+    p.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        p.run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.run()
+    inputs = [Pass(seed) for seed in (1, 2, 3, 1)]
+    for other in inputs:  # other inputs in the same buffers, eager work between the replays
+        for name in ("tables", "k", "v", "lens", "x", "head"):
+            getattr(p, name).copy_(getattr(other, name))
+        p.out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = p.results()
+        other.run()
+        torch.cuda.synchronize()
+        assert same(got, other.results())
+        graph.replay()
+        p.run()
+        torch.cuda.synchronize()
+        assert same(p.results(), got)
