@@ -30,6 +30,8 @@ constexpr int kLpCands = 1024;
 // More than half of that at or above the bound that the slots' maxima give (as where a row has
 // hardly more slots than k): the bound is formed again from the maxima of vectors, kept where
 // the candidates go.  One row of 11,788 bf16, k = 32: 31 us, and 429 by the count over all bits.
+// If more still reach it they are its equals, and the first of those by id are taken: 2560 rows of
+// 128,256 bf16, all but 3 at the lowest value, k = 20: 295 us, and 1716 by that count.
 constexpr int kLpUnits = 2 * kLpCands;
 
 struct LpGeom {
@@ -495,14 +497,12 @@ __global__ __launch_bounds__(kLpBlock, KREGS == 4 ? 5 : 3) void k_lp_finalize(Lo
         if (tid == 0) s_ncand = 0;
         __syncthreads();
       };
-      int nc;
-      // a bound that nothing is below, as where the row has fewer slots than k, is formed again at once
-      const bool fine = T > kKeyNegInf + 1 || nsel * run * kWave * EPV <= kLpCands / 2;
-      for (bool again = false;; again = true) {
-        if (again || !fine) {
-          refine();
-          again = true;
-        }
+      // Pass 0: what reaches the slots' bound; 1: what reaches the finer one (at once where nothing
+      // is below the first, as in rows of fewer slots than k); 2, where many equal the finer one
+      // (rows masked with a lowest value): what is above it.
+      int nc, pass = T > kKeyNegInf + 1 || nsel * run * kWave * EPV <= kLpCands / 2 ? 0 : 1;
+      for (;; ++pass) {
+        if (pass == 1) refine();
         // each wave reads its share of the slots, several at a time where a slot is one vector
         // a lane
         constexpr int kBatch = 4;
@@ -543,13 +543,40 @@ __global__ __launch_bounds__(kLpBlock, KREGS == 4 ? 5 : 3) void k_lp_finalize(Lo
         }
         __syncthreads();
         nc = s_ncand;
-        if (again || nc <= kLpCands / 2 || isnan(s_ln)) break;
+        if (pass == 2 || nc <= (pass == 0 ? kLpCands / 2 : kLpCands) || isnan(s_ln)) break;
         __syncthreads();
+        if (pass == 1) {
+          T = (DT == SMCSD_DTYPE_BF16 ? T | 0xFFFF : T) + 1;
+          bound = unordered(T);
+          if (tid == 0) s_ncand = 0;
+          __syncthreads();
+        }
       }
       for (int i = tid; i < min(nc, kLpCands); i += kLpBlock) cand[i].x = ordered(Elt<DT>::load(row.p, cand[i].y));
       __syncthreads();
+      if (pass == 2 && !isnan(s_ln)) {
+        // the equals of the smallest ids: the slots, and the elements in them, stand by id
+        for (int q = 0; q < nsel && nc < k; ++q) {
+          const int e1 = slot_start<DT>(row, g.segs, sel[q] * run + run, a.V);
+          for (int e0 = slot_start<DT>(row, g.segs, sel[q] * run, a.V); e0 < e1 && nc < k; e0 += kLpBlock) {
+            const int e = e0 + tid;
+            const int key = e < e1 ? ordered(Elt<DT>::load(row.p, e)) : 0;
+            const uint64_t eq = __ballot(e < e1 && key < T && key >= T - (DT == SMCSD_DTYPE_BF16 ? 0x10000 : 1));
+            if (lane == 0) s_bits[wave] = (int)__popcll(eq);
+            __syncthreads();
+            int at = nc + (int)__popcll(eq & (lane == 0 ? 0 : ~0ull >> (64 - lane)));
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              at += w < wave ? s_bits[w] : 0;
+              nc += s_bits[w];
+            }
+            if (((eq >> lane) & 1) && at < kLpCands) cand[at] = make_int2(key, e);
+            __syncthreads();
+          }
+        }
+      }
       if (nc > kLpCands && !isnan(s_ln)) {
-        // Too many elements at or above the bound (long runs of equal logits): the k-th
+        // Too many elements above the finer bound, as in sorted rows of millions: the k-th
         // largest element itself, then the smallest ids among its equals, each bit by bit.
         auto count = [&](auto pred) {
           __syncthreads();

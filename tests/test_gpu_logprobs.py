@@ -107,6 +107,29 @@ def test_more_alternatives_than_segments(dt, n, V, k, steps):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V,k", [(1500, 20), (32000, 64), (128256, 20), (50001, 5)])
+def test_masked_with_the_lowest_value(dt, V, k):
+    """0, 1, 3, k - 1, k and 700 allowed tokens of a row, the others at the type's lowest value:
+    the alternatives past the allowed ones are the smallest ids."""
+    x = logits(6, V, dt, 1)
+    g = torch.Generator().manual_seed(3)
+    for r, n in enumerate([0, 1, 3, k - 1, k, 700]):
+        keep = torch.randperm(V, generator=g)[:n].cuda()
+        kept = x[r, keep].clone()
+        x[r, :V] = torch.finfo(DT[dt]).min
+        x[r, keep] = kept
+    check(call(x, V, 1.0, k=k), x, V)
+
+
+@pytest.mark.parametrize("down", [False, True])
+def test_a_sorted_row_of_millions(down):
+    V = (1 << 21) + 5
+    x = torch.linspace(-8, 8, V)
+    x = torch.stack([x.flip(0) if down else x, (x * 16).round() / 16]).cuda()
+    check(call(x, V, 1.0, k=64), x, V)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_many_rows(dt):
     n, V = 700, 33000
     x, t = logits(n, V, dt, 5, sigma=1.0), some(n, V, 3)
