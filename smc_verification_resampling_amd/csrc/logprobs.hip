@@ -321,7 +321,9 @@ __device__ __forceinline__ int slot_start(const LpRow<DT> &row, int segs, int j,
   return min(row.a1, row.head + (j - 1) * kWave * Elt<DT>::kPerVec);
 }
 
-constexpr int kLpSmall = 256;  // slots of a row that one wave ranks with 4 keys a lane
+// Slots of a row that one wave ranks with 4 keys a lane; more take 16 keys a lane (as 252 slots
+// would, in 63 us for 2560 rows instead of 32).
+constexpr int kLpSmall = 256;
 
 // KREGS: keys of a lane of the wave that ranks the slots (4 or kLpSupers / 64).  Registers for five
 // workgroups of a unit: 32 us for 2560 rows of 128,256, k = 20, against 39 with four, 36 with six

@@ -79,7 +79,7 @@ constexpr int kRowsWave = 32;
 // (256 sequences of 8 heads, 3.2 GB) 687 us against 661, four buffers 802: what the loads gain
 // in flight, the workgroups lose that no longer fit beside each other.
 constexpr int KT = 32, NB = 2;
-constexpr int kWavesMax = 4;      // two workgroups of four waves fill a compute unit's registers
+constexpr int kWavesMax = 4;
 // Workgroups that the splits of a launch aim at: 64 rows x 16 heads over 131,071 keys take 120 us
 // and 12 to join the parts with 1024, 161 + 8 with 512, 136 + 22 with 2048.
 constexpr int kPartItems = 1024;
@@ -101,11 +101,16 @@ inline Cut cut_of(int rows, int64_t heads, int64_t max_len) {
   const int most = kWavesMax * kRowsWave;
   c.tiles = (int)ceil_div(rows, most);
   c.tile_rows = (int)ceil_div(ceil_div(rows, c.tiles), kRowsWave) * kRowsWave;  // whole waves
-  c.waves = c.tile_rows <= kRowsWave ? 1 : c.tile_rows <= 2 * kRowsWave ? 2 : kWavesMax;
+  // Two waves for up to 32 rows too, where the second one only loads: 66 us against 75 with one (512
+  // sequences of 20 rows x 8 heads, 80 keys each), 250 against 261 (16 of 30,000 keys), 359 against
+  // 396 (heads of 192), 5.6 against 6.1 (one token); four took 92, 469, 699 and 5.5.  36 rows of 256
+  // sequences: 606 us with two, 684 with four; 107 to 128 rows: 150 with four, 208 with twice as
+  // many tiles of two.
+  c.waves = c.tile_rows <= 2 * kRowsWave ? 2 : kWavesMax;
   // enough workgroups to fill the chip, but a split's keys outweigh the part it leaves
   const int64_t most_splits = ceil_div(max_len, std::max(256, 4 * std::min(rows, most)));
   c.splits = (int)std::max<int64_t>(
-      1, std::min<int64_t>(max_splits(heads) / std::min(c.waves * c.tiles, 4), most_splits));
+      1, std::min<int64_t>(max_splits(heads) / std::min(c.tile_rows / kRowsWave * c.tiles, 4), most_splits));
   return c;
 }
 
@@ -245,10 +250,10 @@ __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothin
 // Measured, bf16, heads of 128: 32 prompts of 16 x 5 rows x 32 heads over 2048 shared keys, the
 // shared pass 143 us (600 TFLOP/s: bound by a wave's chain of product, exponentials and product;
 // with idle waves in it, 150 us, its arithmetic alone took 112 and its loads alone 71) and the
-// particles' own keys 72 us; 64 rows x 16 heads over 131,071 keys 111 us (620 TFLOP/s); 256 sequences of 9 x 32 heads over up
+// particles' own keys 66 us; 64 rows x 16 heads over 131,071 keys 111 us (620 TFLOP/s); 256 sequences of 9 x 32 heads over up
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
-// one token of 4 sequences of 16 keys 6 us, all of it latency.
+// one token of 4 sequences of 16 keys 5.6 us, all of it latency.
 template <int DT, int DP, int NW, bool PREFIX>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
@@ -331,8 +336,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
     constexpr int NAT = NLD < 4 ? NLD : 4;  // looked up together
     // Up to 64 rows are one workgroup's, and it alone reads its keys: past the caches (nt).  256
-    // sequences of 9 x 32 heads, 3.2 GB, 608 us against 660, of one x 32 heads 577 against 628, 16
-    // of 30,000 keys 264 against 297; where particles share fewer than kMinShared keys it costs
+    // sequences of 9 x 32 heads, 3.2 GB, 608 us against 660, of one x 32 heads 577 against 628 (both
+    // then with a wave to 32 rows), 16 of 30,000 keys 264 against 297; where particles share fewer than kMinShared keys it costs
     // (128 keys, 512 sequences: 70 against 67).  More rows are several workgroups', of the same keys:
     // 64 x 16 heads over 131,071 keys took 134 us with it, 130 without.
     constexpr int kPolicy = NW < 4 ? 2 : 0;
@@ -687,9 +692,7 @@ void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const Cut &c = PREFIX ? p.prefix : p.suffix;
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
-  if (c.waves == 1)
-    hipLaunchKernelGGL((k_attn<DT, DP, 1, PREFIX>), grid, block, 0, stream, a, p);
-  else if (c.waves == 2)
+  if (c.waves == 2)
     hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX>), grid, block, 0, stream, a, p);
   else
     hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX>), grid, block, 0, stream, a, p);
