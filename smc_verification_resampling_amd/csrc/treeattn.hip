@@ -201,8 +201,10 @@ __global__ __launch_bounds__(kShareBlock) void k_shared_len(TreeAttnArgs a, int3
         if (!same) atomicMin(&s_first, c);
       }
       __syncthreads();
-      if (s_first != INT32_MAX) {
-        done = s_first;
+      const int first = s_first;
+      __syncthreads();  // read by every wave before the next blocks' mismatches are noted
+      if (first != INT32_MAX) {
+        done = first;
         break;
       }
     }

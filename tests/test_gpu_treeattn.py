@@ -420,3 +420,19 @@ def test_pages_past_32_bits():
 def test_largest_batch_of_short_sequences():
     c = Case(B=64, N=16, R=2, Hq=4, Hkv=1, D=64, lens=(3, 17, 0, 9), bs=4)
     c.call().check(rows=range(0, 1024, 37))
+
+
+@pytest.mark.parametrize("shared", [1023, 1024, 1025, 2047, 2048, 2049, 2300])
+def test_more_shared_blocks_than_are_compared_at_once(shared):
+    Case(N=5, R=2, lens=(2310, 2400, 2333), bs=1, shared=shared).call().check()
+
+
+@pytest.mark.parametrize("differ", [
+    ((2, 1024),), ((1, 2047), (3, 1024)), ((3, 1500), (1, 1900), (2, 1026), (4, 2047)), ((4, 2048), (1, 2049), (2, 2299)),
+    ((1, 1023), (2, 1024)), ((4, 2299),), ((1, 1100), (1, 2100), (3, 2200))])
+def test_several_particles_leave_the_shared_blocks(differ):
+    """Tables alike past 2048 blocks but for single entries: (particle, slot) that names another block."""
+    c = Case(N=5, R=2, lens=(2310, 2400, 2333), bs=1, shared=2300, seed=len(differ))
+    for n, slot in differ:
+        c.tables[n, slot] = c.tables[n, 2305].item()
+    c.call().check()
