@@ -91,9 +91,10 @@ __global__ __launch_bounds__(kPgBlock) void k_fork(const int32_t *__restrict__ f
 // ---------------------------------------------------------------------------------
 // free
 // ---------------------------------------------------------------------------------
-// A block whose last reference went is marked in its own refcount until it is pushed: the
-// mark is far from any count, and what a corrupt state takes from or adds to it keeps it so.
-constexpr int32_t kFreedMark = INT32_MIN;
+// A block whose last reference went is marked in its own refcount until it is pushed.  In a
+// corrupt state others take from the mark and give back (at most one each of the threads in
+// flight, some 2^19): it lies 2^29 from the least number and 2^29 below what counts as marked.
+constexpr int32_t kFreedMark = -(3 << 29);
 __device__ __forceinline__ bool is_freed(int32_t r) { return r < INT32_MIN / 2; }
 
 __global__ __launch_bounds__(kPgBlock) void k_free_drop(const int32_t *__restrict__ freed, int64_t S,

@@ -223,6 +223,23 @@ def test_corrupt_states_are_flagged_and_stay_in_bounds():
     p.same(B)
 
 
+@pytest.mark.parametrize("count", [1, 2, 7])
+@pytest.mark.parametrize("times", [2, 3, 64])
+def test_a_block_that_loses_far_more_references_than_it_has(count, times):
+    """Every block has `count` references; row 0 names it once, the others `times` times in a run."""
+    n, rows = 256, 10 * times
+    p = Pool(rows, n, n + 30, share=0.0, fill=0.0)
+    p.T[0] = list(range(n))
+    for s in range(1, rows):
+        p.T[s] = [(s * (n // times) + i // times) % n for i in range(n)]
+    p.rc = [count] * n + [0] * 30
+    p.stack = list(range(n, n + 30))
+    p.up()
+    p.free(list(range(rows)))
+    p.same(sm.ST_BAD_INPUT)
+    p.consistent()
+
+
 def caches(n, P, bs, H, D, dtype, layout, seed=0):
     g = torch.Generator("cuda").manual_seed(seed)
     shape = (P, bs, H, D) if layout == "token" else (P, H, bs, D)
