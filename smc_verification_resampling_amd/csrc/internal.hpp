@@ -195,7 +195,7 @@ hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a, int dtype, hipStream_t s
 // Attention over the pages (treeattn.hip).
 constexpr int kMaxNodes = 64;
 constexpr int kMaxHeadDim = 256;
-constexpr int64_t kMaxAttnRows = 1 << 25;  // a wave takes at least one row: 2^31 threads
+constexpr int64_t kMaxAttnRows = (1 << 25) - 1;  // 128 threads take at least one row: fewer than 2^32 of them
 struct TreeAttnArgs {
   const uint16_t *q, *k_cache, *v_cache;
   int64_t q_stride;

@@ -135,6 +135,17 @@ def test_tree_attention(lib):
     assert f(B=0) == 0 and f(N=0) == 0
 
 
+def test_tree_attention_rows(lib):
+    """128 threads a query row at least, and a launch has fewer than 2^32: 2^25 rows are refused, one
+    less is not (what it is refused for here is the missing workspace)."""
+    f = caller(lib.smcsd_tree_attention, " ".join(ATTN), dict(ATTN, M=1, ws=None))
+    one = dict(R=1, Hq=1, Hkv=1, N=1, D=8, qs=8)
+    assert f(**dict(one, B=1 << 25)) == -1 and f(**dict(one, B=(1 << 25) - 1)) == -4
+    assert f(**dict(one, B=1 << 15, N=1 << 10)) == -1 and f(**dict(one, B=(1 << 15) - 1, N=1 << 10)) == -4
+    many = dict(R=64, Hq=16, Hkv=16, N=1, D=8, qs=128)
+    assert f(**dict(many, B=1 << 15)) == -1 and f(**dict(many, B=(1 << 15) - 1)) == -4
+
+
 def test_token_logprobs(lib):
     f = caller(lib.smcsd_token_logprobs, "x dt rs n V T tok C k lp en lse ti tl st ws wsb s",
                dict(x=P0, dt=1, rs=64, n=4, V=64, T=1.0, tok=P0, C=1, k=5, lp=P0, en=P0, lse=P0, ti=P0, tl=P0, st=P0,
