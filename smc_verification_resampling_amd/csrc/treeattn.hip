@@ -80,8 +80,9 @@ constexpr int kRowsWave = 32;
 // in flight, the workgroups lose that no longer fit beside each other.
 constexpr int KT = 32, NB = 2;
 constexpr int kWavesMax = 4;
-// Workgroups that the splits of a launch aim at: 64 rows x 16 heads over 131,071 keys take 120 us
-// and 12 to join the parts with 1024, 161 + 8 with 512, 136 + 22 with 2048.
+// Workgroups of one wave of rows that the splits of a launch aim at (half as many where two row tiles
+// of four waves share a head's keys): 64 rows x 16 heads over 131,071 keys take 120 us and 12 to join
+// the parts with 1024, 161 + 8 with 512, 136 + 22 with 2048.
 constexpr int kPartItems = 1024;
 // Shorter shared prefixes are read by every particle (the caches hold them): 512 sequences of 5 x
 // 32 heads with 128 shared keys take 67 us so and 85 to 89 with a pass of their own, with 256 keys
@@ -94,7 +95,14 @@ struct Cut {
   int rows, tiles, tile_rows, waves, splits;
 };
 inline int pad_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-inline int max_splits(int64_t heads) { return (int)ceil_div(kPartItems, std::max<int64_t>(heads, 1)); }
+// The most splits for `heads` heads of `rows` rows each: a head's share of kPartItems, divided by the
+// waves of its rows or, beyond four tiles, by its tiles.  Fewer for more rows.  Divided by four for
+// any number of tiles, 64 particles x 9 nodes x 32 / 8 heads over 8192 shared keys (18 tiles) took 190 us
+// and 1.5 GB of workspace for 160 us and 0.3 GB, over 32,768 keys 586 us for 439.
+inline int max_splits(int64_t heads, int64_t rows) {
+  const int64_t tiles = ceil_div(rows, kWavesMax * kRowsWave), waves = std::min<int64_t>(ceil_div(rows, kRowsWave), kWavesMax);
+  return (int)std::max<int64_t>(1, ceil_div(kPartItems, std::max<int64_t>(heads, 1)) / std::max<int64_t>({waves, tiles, 1}));
+}
 inline Cut cut_of(int rows, int64_t heads, int64_t max_len) {
   Cut c;
   c.rows = rows;
@@ -109,8 +117,7 @@ inline Cut cut_of(int rows, int64_t heads, int64_t max_len) {
   c.waves = c.tile_rows <= 2 * kRowsWave ? 2 : kWavesMax;
   // enough workgroups to fill the chip, but a split's keys outweigh the part it leaves
   const int64_t most_splits = ceil_div(max_len, std::max(256, 4 * std::min(rows, most)));
-  c.splits = (int)std::max<int64_t>(
-      1, std::min<int64_t>(max_splits(heads) / std::min(c.tile_rows / kRowsWave * c.tiles, 4), most_splits));
+  c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(max_splits(heads, rows), most_splits));
   return c;
 }
 
@@ -721,10 +728,11 @@ void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStr
 }  // namespace
 
 // Workspace: [shared lengths int32 x B][(max, sum) x parts x rows][O fp32 x parts x rows x D], with
-// parts bounded by the splits that S*Hkv (B*Hkv) heads can ask for.  rows*2 <= rows*D / 4.
+// parts bounded by the splits that S*Hkv heads of R rows or more (B*Hkv heads of N*R or more) can ask
+// for; N > 1 particles may share a prefix, which only the tables tell.  rows*2 <= rows*D / 4.
 size_t tree_attn_ws_bytes(int64_t B, int64_t N, int R, int64_t HqD, int64_t Hkv) {
   const int64_t S = B * N;
-  const int ss = max_splits(S * Hkv), sp = N > 1 ? max_splits(B * Hkv) : 0;
+  const int ss = max_splits(S * Hkv, R), sp = N > 1 ? max_splits(B * Hkv, N * R) : 0;
   const size_t floats = (size_t)((ss > 1 ? ss : 0) + sp) * (size_t)(S * R) * (size_t)HqD;
   return align256(sizeof(int32_t) * (size_t)std::max<int64_t>(B, 1)) + align256(sizeof(float) * (floats / 4)) +
          align256(sizeof(float) * floats);

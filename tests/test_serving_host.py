@@ -43,6 +43,14 @@ def test_workspace_sizes(lib):
     assert w(sm.OP_KV_COMPACT, 0, 0, P=100000) >= 3 * 4 * 100000
 
 
+@pytest.mark.parametrize("B,N,R,Hkv,G,most", [(4, 64, 9, 8, 4, 0.5e9), (1, 256, 9, 8, 4, 0.5e9), (1, 1024, 5, 8, 4, 0.5e9),
+                                            (1, 64, 64, 8, 4, 0.5e9), (1, 1024, 64, 1, 8, 1e9), (1, 1, 64, 1, 32, 1.1e9)])
+def test_attention_workspace_follows_the_rows_that_exist(lib, B, N, R, Hkv, G, most):
+    """Heads of 128.  Splits fall as row tiles grow: the parts stay near those of 1024 tiles of 128 rows
+    (67 MB, G times that where the heads of a group are not known), or one a row."""
+    assert 0 < sm.workspace_bytes(sm.OP_TREE_ATTN, B, N, R, Hkv * G * 128, Hkv) < most
+
+
 def test_kv_fork(lib):
     f = caller(lib.smcsd_kv_fork, "m B N T M rc P st s",
                dict(m=P0, B=2, N=4, T=P0, M=8, rc=P0, P=64, st=P0, s=None))
