@@ -516,7 +516,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   // its own loads of tile n, then for the other waves, which are then also done with the buffer
   // that is filled next.
   uint64_t odd = 0;  // new tokens, by node, whose values are not all finite
-  const bool busy = tile * cut.tile_rows + wave * kRowsWave < cut.rows;  // a wave without rows only loads
+  // a wave without rows only loads (of four, the last one of a tile of 96 rows among them)
+  const bool busy = wave * kRowsWave < cut.tile_rows && tile * cut.tile_rows + wave * kRowsWave < cut.rows;
   if (k0 < k1) {
     uint64_t next_ok = fetch_tile(0, k0);
     int buf = 0;

@@ -436,3 +436,10 @@ def test_several_particles_leave_the_shared_blocks(differ):
     for n, slot in differ:
         c.tables[n, slot] = c.tables[n, 2305].item()
     c.call().check()
+
+
+@pytest.mark.parametrize("N,R,Hq", [(8, 5, 8), (14, 5, 8), (1, 33, 8), (1, 48, 6), (2, 64, 9)])
+def test_row_tiles_of_three_waves(N, R, Hq):
+    """129 to 192 rows of a head in two tiles, 257 to 288 in three: their fourth wave has no rows."""
+    c = Case(B=2, N=N, R=R, Hq=Hq, Hkv=2 if Hq % 2 == 0 else 3, D=128, lens=(300, 311), shared=288 if N > 1 else 0, tree=True)
+    c.call().check()
