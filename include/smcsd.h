@@ -552,7 +552,7 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
  * SMCSD_ST_EMPTY_ROW; a row with a NaN or +inf logit gets NaN and ids -1, and sets
  * SMCSD_ST_NAN_INPUT.  Every output is nullable (C = 0 needs no tokens, k = 0 no top).
  * Limits: n >= 0, 1 <= V <= 2^24, 0 <= C <= 1024, 0 <= k <= 64, k <= V, row_stride >= V,
- * temperature finite > 0.  workspace: smcsd_workspace_bytes(SMCSD_OP_LOGPROBS, n, 1, k, V, 0).
+ * temperature finite, at least 2^-127.  workspace: smcsd_workspace_bytes(SMCSD_OP_LOGPROBS, n, 1, k, V, 0).
  */
 int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n, int V,
                          float temperature, const int32_t *tokens, int C, int k,

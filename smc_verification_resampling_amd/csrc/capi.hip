@@ -581,6 +581,8 @@ int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int 
       k > kMaxTop || k > V)
     return SMCSD_EINVAL;
   if (!(temperature > 0.0f) || !std::isfinite(temperature)) return SMCSD_EINVAL;
+  const float c = (float)(1.4426950408889634073599246810018921 / (double)temperature);
+  if (!std::isfinite(c)) return SMCSD_EINVAL;  // differences of logits are multiplied by it
   if (n == 0) return SMCSD_OK;
   const size_t esz = dtype == SMCSD_DTYPE_BF16 ? 2 : 4;
   if (!logits || !aligned(logits, esz) || !status || (C > 0 && out_logp && !tokens))
@@ -592,7 +594,7 @@ int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int 
   a.row_bytes = row_stride * (int64_t)esz;
   a.n = n;
   a.V = V;
-  a.c = (float)(1.4426950408889634073599246810018921 / (double)temperature);
+  a.c = c;
   a.inv_T = 1.0 / (double)temperature;
   a.tokens = tokens;
   a.C = C;

@@ -167,6 +167,16 @@ def test_token_logprobs(lib):
     assert f(n=0) == 0
 
 
+def test_token_logprobs_temperatures_whose_inverse_is_no_number(lib):
+    f = caller(lib.smcsd_token_logprobs, "x dt rs n V T tok C k lp en lse ti tl st ws wsb s",
+               dict(x=P0, dt=1, rs=64, n=4, V=64, T=1.0, tok=P0, C=1, k=5, lp=P0, en=P0, lse=P0, ti=P0, tl=P0, st=P0,
+                    ws=None, wsb=0, s=None))
+    for T in (2.0 ** -149, 1e-40, 4e-39):  # log2(e) / T is past the largest float
+        assert f(T=T) == -1 and f(T=T, n=0) == -1, T
+    for T in (2.0 ** -127, 2.0 ** -126, 3e38):  # no refusal but the missing workspace's
+        assert f(T=T) == -4, T
+
+
 def test_binding_refuses_host_tensors(lib):
     i = torch.zeros(8, dtype=torch.int32)
     t = torch.zeros(2, 4, dtype=torch.int32)
