@@ -523,7 +523,7 @@ int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
  * max_len: the largest ctx_lens[s] + R, as far as the caller knows it (0: M_cap *
  * block_size); it steers how the keys are split over workgroups, and is no bound.
  * Limits: B, N >= 0, 1 <= R <= 64, Hq a multiple of Hkv, 8 <= D <= 256 and D a multiple of
- * 8; scale finite; 16-byte aligned pointers and strides of a multiple of 8 elements;
+ * 8; |scale| <= 2^127; 16-byte aligned pointers and strides of a multiple of 8 elements;
  * M_cap * block_size < 2^31 - 4096, B*N*R*Hq < 2^25, B*N*M_cap < 2^31.
  * out overlaps neither q nor the caches.
  * workspace: smcsd_workspace_bytes(SMCSD_OP_TREE_ATTN, B, N, R, Hq * D, Hkv).

@@ -531,8 +531,8 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
                          void *stream) {
   if (dtype != SMCSD_DTYPE_BF16 && dtype != SMCSD_DTYPE_F16) return SMCSD_EDTYPE;
   if (B < 0 || N < 0 || R < 1 || R > kMaxNodes || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 8 ||
-      D > kMaxHeadDim || D % 8 || !std::isfinite(scale) || max_len < 0)
-    return SMCSD_EINVAL;
+      D > kMaxHeadDim || D % 8 || !(std::fabs(scale) <= 0x1p127f) || max_len < 0)
+    return SMCSD_EINVAL;  // (times log2(e), a scale past 2^127 could be infinite)
   const int64_t S = (int64_t)B * N;
   if (S == 0) return SMCSD_OK;
   if (S >= INT32_MAX || S * R >= INT32_MAX || S * R * Hq > kMaxAttnRows || (int64_t)Hq * D >= INT32_MAX ||

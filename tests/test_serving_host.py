@@ -154,6 +154,14 @@ def test_tree_attention_rows(lib):
     assert f(**dict(many, B=1 << 15)) == -1 and f(**dict(many, B=(1 << 15) - 1)) == -4
 
 
+def test_tree_attention_scales_past_a_float(lib):
+    f = caller(lib.smcsd_tree_attention, " ".join(ATTN), dict(ATTN, ws=None))
+    for scale in (3e38, -3e38, float("-inf")):  # scale * log2(e) is infinite
+        assert f(scale=scale) == -1, scale
+    for scale in (2.0 ** 127, -2.0 ** 127, 0.0, 1e-45):
+        assert f(scale=scale) == -4, scale
+
+
 def test_token_logprobs(lib):
     f = caller(lib.smcsd_token_logprobs, "x dt rs n V T tok C k lp en lse ti tl st ws wsb s",
                dict(x=P0, dt=1, rs=64, n=4, V=64, T=1.0, tok=P0, C=1, k=5, lp=P0, en=P0, lse=P0, ti=P0, tl=P0, st=P0,
