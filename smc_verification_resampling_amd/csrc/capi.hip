@@ -398,7 +398,7 @@ int smcsd_kv_fork(const int32_t *forked, int B, int N, int32_t *block_tables, in
                   int32_t *refcounts, int64_t P, int32_t *status, void *stream) {
   if (B < 0 || N < 1 || N > kMaxN || M_cap < 1 || P < 1 || P > INT32_MAX) return SMCSD_EINVAL;
   if (B == 0) return SMCSD_OK;
-  if ((int64_t)B * N * M_cap >= INT32_MAX) return SMCSD_EINVAL;
+  if ((int64_t)B * N >= INT32_MAX || (int64_t)B * N * M_cap >= INT32_MAX) return SMCSD_EINVAL;
   if (!forked || !block_tables || !refcounts || !status) return SMCSD_EINVAL;
   return hip_rc(launch_kv_fork(forked, B, N, block_tables, M_cap, refcounts, P, status,
                                as_stream(stream)));

@@ -62,6 +62,13 @@ def test_kv_fork(lib):
     assert f(N=1, M=1) == 0  # one particle: nothing to share, nothing enqueued
 
 
+def test_kv_fork_sizes_whose_product_passes_64_bits(lib):
+    f = caller(lib.smcsd_kv_fork, "m B N T M rc P st s",
+               dict(m=P0, B=2, N=1024, T=P0, M=8, rc=P0, P=64, st=P0, s=None))
+    assert f(B=1 << 30, M=1 << 24) == -1 and f(B=1 << 29, M=1 << 25) == -1 and f(B=(1 << 31) - 1, N=1, M=1) == -1
+    assert f(B=(1 << 31) - 2, N=1, M=1) == 0  # one particle each: nothing is enqueued
+
+
 def test_kv_free(lib):
     f = caller(lib.smcsd_kv_free, "m S T M rc fl top P st ws wsb s",
                dict(m=P0, S=4, T=P0, M=8, rc=P0, fl=P0, top=P0, P=64, st=P0, ws=P0, wsb=1 << 20, s=None))
