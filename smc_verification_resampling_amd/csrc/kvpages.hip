@@ -19,7 +19,9 @@ constexpr int kPgBlock = 256;
 // Consecutive blocks of a thread in the kernels over the pool.  A workgroup adds up the counts of
 // all other workgroups' groups, which larger groups would make fewer, but 32 to a thread lose
 // at every size measured: count and rank of 24,576 blocks 19 us against 7, of 8 million 226
-// against 45 (a thread's neighbours are then 128 bytes away).
+// against 45 (a thread's neighbours are then 128 bytes away).  That sum grows with the square of
+// the pool: 64 tables of 2000 blocks freed (half of them) and compacted take 20 and 25 us in a pool of
+// 2^20 blocks, 39 and 71 of 2^23, 183 and 403 of 2^25, 431 and 1276 of 2^26, the largest.
 constexpr int kPerThread = 4;
 
 // Bit i: `is` holds for the count of block b0 + i (b0 a multiple of kPerThread).

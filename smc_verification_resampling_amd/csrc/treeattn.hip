@@ -346,9 +346,11 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     constexpr int NAT = NLD < 4 ? NLD : 4;  // looked up together
     // Up to 64 rows are one workgroup's, and it alone reads its keys: past the caches (nt).  256
     // sequences of 9 x 32 heads, 3.2 GB, 608 us against 660, of one x 32 heads 577 against 628 (both
-    // then with a wave to 32 rows), 16 of 30,000 keys 264 against 297; where particles share fewer than kMinShared keys it costs
-    // (128 keys, 512 sequences: 70 against 67).  More rows are several workgroups', of the same keys:
-    // 64 x 16 heads over 131,071 keys took 134 us with it, 130 without.
+    // then with a wave to 32 rows), 16 of 30,000 keys 264 against 297; where particles share fewer than
+    // kMinShared keys it costs (128 keys, 512 sequences: 70 against 67).  Four waves' rows may be
+    // several workgroups', of the same keys: 64 x 16 heads over 131,071 keys took 134 us with it, 130
+    // without.  From 65 to 128 rows four waves are one workgroup too, and lose 1 to 3 % by that (256
+    // sequences of 17 x 32 heads 711 us, 690 past the caches).
     constexpr int kPolicy = NW < 4 ? 2 : 0;
 #pragma unroll
     for (int i0 = 0; i0 < NLD; i0 += NAT) {
@@ -499,6 +501,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[8 * h + i], p.c, -ms));
       l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      // rounded for the product, as the matrix instruction takes them; l sums them unrounded.  Against 64
+      // bits that makes 0.0023 of relative error in bf16 where fp32 probabilities leave 0.0017
       pr[h] = __builtin_convertvector(e, V8);
       // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
 #pragma unroll
