@@ -403,9 +403,10 @@ int smcsd_kv_fork(const int32_t *forked, int B, int N, int32_t *block_tables, in
  * freed [S] int32; block_tables [S, M_cap], refcounts [P], free_list [P], free_top [1]
  * int32 in/out, as in smcsd_kv_reassign.  An id outside [0, P) other than -1, a block
  * that loses more references than it has (its count ends at 0, and it is pushed once if
- * it had any; one below 0, which no call leaves, stays), and a free_top outside [0, P] (then clamped) or pushed past P (the entries
- * that do not fit are dropped) set SMCSD_ST_BAD_INPUT.  Limits: 0 <= S, S*M_cap < 2^31,
- * 1 <= P <= SMCSD_POOL_OPS_MAX_BLOCKS, refcounts >= -2^30 (marks of the call lie below).
+ * it had any; one below 0, which no call leaves, stays), and a free_top outside [0, P] (then
+ * clamped) or pushed past P (the entries that do not fit are dropped) set
+ * SMCSD_ST_BAD_INPUT.  Limits: 0 <= S, S*M_cap < 2^31, 1 <= P <= SMCSD_POOL_OPS_MAX_BLOCKS,
+ * refcounts >= -2^30 (marks of the call lie below).
  * workspace: smcsd_workspace_bytes(SMCSD_OP_KV_FREE, 0, 0, 0, 0, P).
  */
 #define SMCSD_POOL_OPS_MAX_BLOCKS (1LL << 26)
