@@ -345,7 +345,7 @@ def _own(s):
     if s["op"] == "prompt":
         T, Hq, D = s["q"].shape
         if "ws" not in s:
-            s["ws"] = sm.alloc_workspace(sm.OP_PROMPT_ATTN, len(s["lens"]), T, V=Hq * D, P=s["k"].shape[2])
+            s["ws"] = sm.alloc_workspace(sm.OP_PROMPT_ATTN, len(s["lens"]), T, K=D, V=Hq * D, P=s["k"].shape[2])
         sm.prompt_attention(s["q"], s["k"], s["v"], s["tables"], s["lens"], s["cu"], s["scale"], s["out"], s["status"], s["ws"], k_scales=s["k_scales"], v_scales=s["v_scales"],
                             lse=s["lse"], max_len=s["longest"])
         return s["out"], s["lse"]
