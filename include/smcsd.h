@@ -63,6 +63,9 @@ extern "C" {
 #define SMCSD_DTYPE_BF16 1
 /* element type of queries, keys and values beside bf16 (smcsd_qk_norm_rope, smcsd_tree_attention) */
 #define SMCSD_DTYPE_F16 2
+/* element type of 8-bit pages: e4m3 (OCP; no infinities), with a scale for each block and head:
+ * a code x (E8M0) that stands for 2^(x - 127), 255 for NaN (smcsd_kv_append) */
+#define SMCSD_DTYPE_E4M3 3
 
 /* verify mode */
 #define SMCSD_MODE_SMC 0
@@ -95,6 +98,7 @@ extern "C" {
 #define SMCSD_OP_LOGPROBS 6
 #define SMCSD_OP_KV_FREE 7
 #define SMCSD_OP_KV_COMPACT 8
+#define SMCSD_OP_PROMPT_ATTN 9
 
 /* kinds of violation counted by smcsd_kv_check */
 #define SMCSD_KV_CHECK_KINDS 5
@@ -113,6 +117,8 @@ const char *smcsd_status_string(int code);
  *   SMCSD_OP_KV_CHECK: the pool size P (B, N, K, V ignored); no initial contents needed.
  *   SMCSD_OP_TREE_ATTN: B, N as passed to smcsd_tree_attention, K = R, V = Hq * D and
  *   P = Hkv; no initial contents needed.
+ *   SMCSD_OP_PROMPT_ATTN: B = S and N = T as passed to smcsd_prompt_attention, K = D,
+ *   V = Hq * D and P = Hkv; it serves calls of fewer tokens too; no initial contents needed.
  *   SMCSD_OP_LOGPROBS: B = number of rows, N = 1, K = k (the number of alternatives), V;
  *   no initial contents needed.
  *   SMCSD_OP_KV_FREE, SMCSD_OP_KV_COMPACT: the pool size P (B, N, K, V ignored); no initial
@@ -462,6 +468,22 @@ int smcsd_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int s
                   int32_t *status, void *stream);
 
 /*
+ * smcsd_kv_copy_scaled - smcsd_kv_copy for 8-bit pages: the blocks' scales follow their data.
+ * scales: a HOST array of n_caches device pointers, read during the call; scales[c] [P, Hkv]
+ * holds the codes of the cache caches[c].  An entry that copies tokens (one or more) copies
+ * its source block's Hkv codes too: the tokens that a copy-on-write leaves behind share their
+ * scale.  Everything else as in smcsd_kv_copy, with token_bytes the bytes of 8-bit elements.
+ * Limits: those of smcsd_kv_copy, n_caches <= SMCSD_KV_COPY_SCALED_MAX_CACHES, Hkv >= 1,
+ * P*Hkv < 2^40.  One launch.
+ */
+#define SMCSD_KV_COPY_SCALED_MAX_CACHES 128
+int smcsd_kv_copy_scaled(void *const *caches, uint8_t *const *scales, int n_caches, int Hkv,
+                         int64_t block_stride, int segments, int64_t segment_stride,
+                         int64_t token_bytes, int block_size, const int32_t *list,
+                         const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
+                         void *stream);
+
+/*
  * smcsd_qk_norm_rope - the new tokens' way into the cache: RMS norms of queries and keys
  * for each head, the position rotation, and the write of keys and values into the pages
  * that the round reserved, in one pass (the Score step's batched pass over K+1 positions:
@@ -496,6 +518,45 @@ int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
                        int block_size, int64_t P, void *k_cache, void *v_cache,
                        int64_t page_stride, int64_t token_stride, int64_t head_stride,
                        void *q_out, int32_t *status, void *stream);
+
+/*
+ * smcsd_kv_append - packed tokens' way into the cache: whole prompts, chunks of them or a
+ * round's new tokens, any number for each sequence, into pages of 16 or of 8 bits.  Norms,
+ * rotation and the write are those of smcsd_qk_norm_rope.
+ * Sequence s < S has the tokens t = cu_tokens[s] .. cu_tokens[s + 1] - 1 of T (cu_tokens
+ * [S + 1] int32, not decreasing, within [0, T]; tokens outside [cu_tokens[0], cu_tokens[S])
+ * are left alone).  Its i-th token goes to page position ctx_lens[s] + i (ctx_lens NULL: 0)
+ * and has the position positions[t], or ctx_lens[s] + i where positions is NULL.
+ * q [T, q_stride] and q_out [T, Hq, D] may both be NULL: keys and values alone.
+ * cache_dtype is dtype or SMCSD_DTYPE_E4M3.  8-bit pages hold e4m3 elements whose value is
+ *   element * 2^(x - 127),   x = k_scales[b, h] (v_scales[b, h]) of block b and head h,
+ * k_scales, v_scales [P, Hkv] uint8 (NULL for 16-bit pages).  For each block, head and call,
+ * with A the largest finite magnitude that the call writes there,
+ *   x_new = the least x in [1, 247] with A <= 448 * 2^(x - 127)   (1 where A = 0),
+ * and where the block holds older tokens of the sequence (its first page position of the call
+ * is not the block's first) no less than x: scales only grow, and older tokens are rounded
+ * again to the grown scale, which a power of two changes only below e4m3's normal range.
+ * Values are rounded once, from fp32, to nearest even; what is not finite becomes NaN.
+ * Page positions behind a sequence's last token are left as they are, but what they hold is
+ * scaled by x_new.
+ * SMCSD_ST_BAD_INPUT: a token whose position is outside [0, max_pos) (when rot_dim > 0), or of
+ * a sequence whose ctx_lens is negative, is left alone; one whose page position is outside [0,
+ * M_cap * block_size), or block id outside [0, P), has its query written and nothing else;
+ * where cu_tokens is not as above, which tokens are written is not defined.  Two sequences
+ * that name the same block for their tokens race.
+ * q_out may be q itself if q_stride = Hq * D.
+ * Limits: those of smcsd_qk_norm_rope with T for S*R and S, T >= 0; for 8-bit pages D and the
+ * three strides multiples of 16.  One launch.
+ */
+int smcsd_kv_append(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                    int64_t k_stride, int64_t v_stride, int S, int T, const int32_t *cu_tokens,
+                    int Hq, int Hkv, int D, const void *q_weight, const void *k_weight, float eps,
+                    const float *cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                    const int32_t *positions, const int32_t *ctx_lens,
+                    const int32_t *block_tables, int M_cap, int block_size, int64_t P,
+                    int cache_dtype, void *k_cache, void *v_cache, int64_t page_stride,
+                    int64_t token_stride, int64_t head_stride, uint8_t *k_scales,
+                    uint8_t *v_scales, void *q_out, int32_t *status, void *stream);
 
 /*
  * smcsd_tree_attention - attention of the drafted tokens over the paged cache: the Score
@@ -537,6 +598,61 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
                          int Hq, int Hkv, int D, float scale, int64_t max_len, void *out,
                          float *lse, int32_t *status, void *workspace, size_t workspace_bytes,
                          void *stream);
+
+/*
+ * smcsd_tree_attention_e4m3 - smcsd_tree_attention over 8-bit pages: caches of e4m3 elements
+ * with k_scales, v_scales [P, Hkv] uint8 as smcsd_kv_append writes them (any codes; 0 stands
+ * for 2^-127 and 255 for NaN).  Keys and values are widened to dtype: exactly in bf16, rounded
+ * to nearest where they are subnormal in f16 and held within its largest number.  dtype is
+ * that of q and out; everything else, the workspace among it, as in smcsd_tree_attention.
+ * Limits: those of smcsd_tree_attention, with D and the three strides multiples of 16.
+ */
+int smcsd_tree_attention_e4m3(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                              const void *v_cache, int64_t page_stride, int64_t token_stride,
+                              int64_t head_stride, const uint8_t *k_scales,
+                              const uint8_t *v_scales, const int32_t *block_tables, int M_cap,
+                              int block_size, int64_t P, const int32_t *ctx_lens,
+                              const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N,
+                              int R, int Hq, int Hkv, int D, float scale, int64_t max_len,
+                              void *out, float *lse, int32_t *status, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * smcsd_prompt_attention - causal attention of whole prompts, or of chunks of them, over the
+ * paged cache: the prefill that precedes a prompt's rounds.  Sequences of different lengths
+ * are packed as in smcsd_kv_append: sequence s has the queries cu_tokens[s] ..
+ * cu_tokens[s + 1] - 1 behind ctx_lens[s] tokens (NULL: 0) that the cache holds already, and
+ * query i of it sees the page positions 0 .. ctx_lens[s] + i (the new tokens' keys and values
+ * are in the pages: smcsd_kv_append).  With c = scale:
+ *   z_t = c * <q_i, k_t>,  out_i = sum_t softmax(z)_t v_t,  lse_i = ln sum_t exp(z_t);
+ * query head h reads key/value head h / (Hq/Hkv).  Scores, the running maximum and sum and the
+ * output are held in fp32; the probabilities are rounded to dtype for the product with v.
+ * q [T, q_stride] holds Hq heads of D elements per token; out [T, Hq, D]; lse [T, Hq] fp32
+ * (nullable); dtype bf16 or f16 for q and out; cache_dtype is dtype, or SMCSD_DTYPE_E4M3 with
+ * k_scales and v_scales (NULL for 16-bit pages) as in smcsd_tree_attention_e4m3.
+ * Rows of out and lse outside [cu_tokens[0], cu_tokens[S]) are left as they were.  What
+ * stands at a page position that a query does not see is never used for it, nor is a block id
+ * outside [0, P): the tokens of such a block are not seen and set SMCSD_ST_BAD_INPUT.  So does
+ * a ctx_lens[s] that is negative or leaves no room for the sequence's tokens in M_cap *
+ * block_size positions: its queries then see nothing (out = 0, lse = -inf).  Where cu_tokens
+ * decreases or leaves [0, T], which sets SMCSD_ST_BAD_INPUT too, which rows are written is not
+ * defined.
+ * max_len: the largest ctx_lens[s] plus its new tokens, as far as the caller knows it (0:
+ * M_cap * block_size); it steers how the keys are split over workgroups, and is no bound.
+ * Limits: S, T >= 0, Hq a multiple of Hkv, 8 <= D <= 256 and D a multiple of 8 (16 for 8-bit
+ * pages); |scale| <= 2^127; 16-byte aligned pointers and strides of a multiple of 8 elements
+ * (16 for 8-bit pages); M_cap * block_size < 2^31 - 4096, T*Hq < 2^30, S*Hkv < 2^22,
+ * S*M_cap < 2^31.  out overlaps neither q nor the caches.
+ * workspace: smcsd_workspace_bytes(SMCSD_OP_PROMPT_ATTN, S, T, D, Hq * D, Hkv).
+ */
+int smcsd_prompt_attention(const void *q, int dtype, int64_t q_stride, int cache_dtype,
+                           const void *k_cache, const void *v_cache, int64_t page_stride,
+                           int64_t token_stride, int64_t head_stride, const uint8_t *k_scales,
+                           const uint8_t *v_scales, const int32_t *block_tables, int M_cap,
+                           int block_size, int64_t P, const int32_t *ctx_lens,
+                           const int32_t *cu_tokens, int S, int T, int Hq, int Hkv, int D,
+                           float scale, int64_t max_len, void *out, float *lse, int32_t *status,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * smcsd_token_logprobs - what a sampler reports about rows of logits, from one streaming

@@ -17,11 +17,11 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsmcsd.so")
 
-DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
+DTYPE_F32, DTYPE_BF16, DTYPE_F16, DTYPE_E4M3 = 0, 1, 2, 3
 MODE_SMC, MODE_SPS, MODE_SMC_RACE = 0, 1, 2  # MODE_SMC_RACE: SMC with the exponential-race bonus
 OP_VERIFY_SMC, OP_VERIFY_SPS, OP_KV, OP_DRAFT, OP_KV_CHECK = 0, 1, 2, 3, 4
-OP_TREE_ATTN, OP_LOGPROBS, OP_KV_FREE, OP_KV_COMPACT = 5, 6, 7, 8
-KV_COPY_MAX_CACHES = 256
+OP_TREE_ATTN, OP_LOGPROBS, OP_KV_FREE, OP_KV_COMPACT, OP_PROMPT_ATTN = 5, 6, 7, 8, 9
+KV_COPY_MAX_CACHES, KV_COPY_SCALED_MAX_CACHES = 256, 128
 STATIC_SCRATCH_BYTES = 4 << 20  # smcsd_verify_static's per-GPU scratch array
 
 ST_NAN_INPUT = 1
@@ -40,10 +40,13 @@ EXPORTED = ("smcsd_version", "smcsd_status_string", "smcsd_workspace_bytes", "sm
             "smcsd_verify_static", "smcsd_draft_sample", "smcsd_resample", "smcsd_kv_reassign",
             "smcsd_resample_kv_reassign", "smcsd_step", "smcsd_kv_check", "smcsd_philox4x32_10",
             "smcsd_stream_read", "smcsd_kv_fork", "smcsd_kv_free", "smcsd_kv_compact",
-            "smcsd_kv_copy", "smcsd_qk_norm_rope", "smcsd_tree_attention", "smcsd_token_logprobs")
+            "smcsd_kv_copy", "smcsd_kv_copy_scaled", "smcsd_qk_norm_rope", "smcsd_kv_append",
+            "smcsd_tree_attention", "smcsd_tree_attention_e4m3", "smcsd_prompt_attention",
+            "smcsd_token_logprobs")
 
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _DT_KV = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_E4M3 = torch.float8_e4m3fn
 
 
 class SmcsdError(RuntimeError):
@@ -110,6 +113,19 @@ def load_library(path: str = LIB_PATH):
                                          P, i32, i32, i32, i32, i32, i32, f32, i64, P, P, P, P, sz,
                                          P]
     lib.smcsd_tree_attention.restype = i32
+    lib.smcsd_kv_copy_scaled.argtypes = [P, P, i32, i32, i64, i32, i64, i64, i32, P, P, i64, i64, P, P]
+    lib.smcsd_kv_copy_scaled.restype = i32
+    lib.smcsd_kv_append.argtypes = [P, P, P, i32, i64, i64, i64, i32, i32, P, i32, i32, i32, P, P, f32,
+                                    P, i64, i32, i32, P, P, P, i32, i32, i64, i32, P, P, i64, i64, i64,
+                                    P, P, P, P, P]
+    lib.smcsd_kv_append.restype = i32
+    lib.smcsd_tree_attention_e4m3.argtypes = [P, i32, i64, P, P, i64, i64, i64, P, P, P, i32, i32, i64,
+                                              P, P, P, i32, i32, i32, i32, i32, i32, f32, i64, P, P, P,
+                                              P, sz, P]
+    lib.smcsd_tree_attention_e4m3.restype = i32
+    lib.smcsd_prompt_attention.argtypes = [P, i32, i64, i32, P, P, i64, i64, i64, P, P, P, i32, i32, i64,
+                                           P, P, i32, i32, i32, i32, i32, f32, i64, P, P, P, P, sz, P]
+    lib.smcsd_prompt_attention.restype = i32
     lib.smcsd_token_logprobs.argtypes = [P, i32, i64, i32, i32, f32, P, i32, i32, P, P, P, P, P, P,
                                          P, sz, P]
     lib.smcsd_token_logprobs.restype = i32
@@ -559,15 +575,59 @@ def _pages(t, name: str, dtype, dev: int):
     raise SmcsdError("%s is on device %d, the call runs on device %d" % (name, t.get_device(), dev))
 
 
+def _codes(t, name: str, P: int, Hkv: int, dev: int) -> int:
+    """The address of the scales' codes [P, Hkv] uint8 of 8-bit pages."""
+    p = _need(t, name, torch.uint8, 0, dev)
+    if tuple(t.shape) != (P, Hkv):
+        raise SmcsdError("%s must be [%d, %d]" % (name, P, Hkv))
+    return p
+
+
+def _cache_dtype(k_cache, dtype):
+    """The type of the pages' elements: 8 bits where k_cache has them, or `dtype`."""
+    return _E4M3 if getattr(k_cache, "dtype", None) is _E4M3 else dtype
+
+
+def _scale_pair(k_cache, k_scales, v_scales, P: int, Hkv: int, dev: int):
+    """(whether the pages are of 8 bits, addresses of their scales' codes)."""
+    if k_cache.dtype is not _E4M3:
+        if k_scales is not None or v_scales is not None:
+            raise SmcsdError("scales belong to float8_e4m3fn caches")
+        return False, None, None
+    return (True, _codes(k_scales, "k_scales", P, Hkv, dev), _codes(v_scales, "v_scales", P, Hkv, dev))
+
+
+def _packed(t, name: str, T: int, D: int, dtype, dev: int):
+    """(address, heads, stride between tokens) of [T, H, D] with each token's heads contiguous."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3:
+        return _heads(t.unsqueeze(1), name, T, 1, D, dtype, dev)
+    _dev(t, name, dtype, contiguous=False)
+    raise SmcsdError("%s must be [T, heads, D]" % name)
+
+
+def _lengths(cu_tokens, ctx_lens, dev: int):
+    """(S, addresses) of cu_tokens [S + 1] and ctx_lens [S] (None: none)."""
+    if not isinstance(cu_tokens, torch.Tensor) or cu_tokens.dim() != 1 or cu_tokens.numel() < 1:
+        raise SmcsdError("cu_tokens must be [S + 1]")
+    S = cu_tokens.numel() - 1
+    return (S, _need(cu_tokens, "cu_tokens", torch.int32, 1, dev),
+            _addr(ctx_lens, "ctx_lens", torch.int32, S, dev))
+
+
 def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Tensor,
-            status: torch.Tensor, stream=None) -> None:
+            status: torch.Tensor, stream=None,
+            scales: Optional[Sequence[torch.Tensor]] = None) -> None:
     """smcsd_kv_copy: runs a list of (source, destination, tokens) entries, as kv_reassign
     (copy-on-write) and kv_compact write them, on every cache.  caches: tensors seen as
     [P, block_size, Hkv, D], all of one shape, type and layout; a [P, Hkv, block_size, D]
-    cache is passed as its transpose(1, 2)."""
+    cache is passed as its transpose(1, 2).  scales: for caches of 8-bit pages, the scales [P,
+    Hkv] uint8 of each, copied along (smcsd_kv_copy_scaled; at most KV_COPY_SCALED_MAX_CACHES)."""
     n = len(caches)
-    if n > KV_COPY_MAX_CACHES:
-        raise SmcsdError("at most %d caches a call" % KV_COPY_MAX_CACHES)
+    most = KV_COPY_MAX_CACHES if scales is None else KV_COPY_SCALED_MAX_CACHES
+    if n > most:
+        raise SmcsdError("at most %d caches a call" % most)
+    if scales is not None and len(scales) != n:
+        raise SmcsdError("scales must be given for every cache")
     dev = _device_of(status, "status")
     if not isinstance(moves, torch.Tensor) or moves.dim() != 2 or moves.shape[1] != 3:
         raise SmcsdError("moves must be [capacity, 3]")
@@ -593,6 +653,17 @@ def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Te
         segments, seg, tok = H, head, D * e
     else:
         raise SmcsdError("a token's heads, or a head's tokens, must be contiguous")
+    if scales is not None:
+        if dtype is not _E4M3:
+            raise SmcsdError("caches with scales must be float8_e4m3fn")
+        codes = (ctypes.c_void_p * n)()
+        for i, x in enumerate(scales):
+            codes[i] = _codes(x, "scales[%d]" % i, P, H, dev)
+        rc = _L().smcsd_kv_copy_scaled(ptrs, codes, n, H, page, segments, seg, tok, bs, mp, cp,
+                                       moves.shape[0], P, sp, _queue(stream, dev))
+        if rc:
+            _check(rc, "smcsd_kv_copy_scaled")
+        return
     rc = _L().smcsd_kv_copy(ptrs, n, page, segments, seg, tok, bs, mp, cp, moves.shape[0], P, sp,
                             _queue(stream, dev))
     if rc:
@@ -681,14 +752,97 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ctx_lens: to
         _check(rc, "smcsd_qk_norm_rope")
 
 
+def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor,
+              ctx_lens: Optional[torch.Tensor], block_tables: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, q_out: Optional[torch.Tensor], status: torch.Tensor,
+              k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+              positions: Optional[torch.Tensor] = None, stream=None) -> None:
+    """smcsd_kv_append.  q [T, Hq, D], k, v [T, Hkv, D] (bf16 or f16; views into a fused
+    projection will do), cu_tokens [S + 1] and ctx_lens [S] int32 (None: empty caches), q_out [T,
+    Hq, D] (q and q_out None: keys and values alone); k_cache, v_cache seen as [P, block_size,
+    Hkv, D] with any strides between rows of D, of k's type or float8_e4m3fn with k_scales,
+    v_scales [P, Hkv] uint8; cos_sin [max_pos, rot_dim] fp32 (None: no rotation), positions [T]
+    int32 (None: ctx_lens + place in the sequence)."""
+    dev = _device_of(status, "status")
+    dt = _kv_dtype(k)
+    dtype = k.dtype
+    if k.dim() != 3:
+        raise SmcsdError("k must be [T, heads, D]")
+    T, _, D = k.shape
+    kp, Hkv, ks = _packed(k, "k", T, D, dtype, dev)
+    vp, Hv, vs = _packed(v, "v", T, D, dtype, dev)
+    if (q is None) != (q_out is None):
+        raise SmcsdError("q and q_out must both be given, or neither")
+    qp, Hq, qs, qo = None, 1, D, None
+    if q is not None:
+        qp, Hq, qs = _packed(q, "q", T, D, dtype, dev)
+        qo = _need(q_out, "q_out", dtype, T * Hq * D, dev)
+    P, bs, H, page, token, head = _cache_pair(k_cache, v_cache, _cache_dtype(k_cache, dtype), D, dev)
+    if Hv != Hkv or H != Hkv:
+        raise SmcsdError("k, v and the caches must have the same heads (%d, %d, %d)" % (Hkv, Hv, H))
+    e4m3, sk, sv = _scale_pair(k_cache, k_scales, v_scales, P, Hkv, dev)
+    max_pos, rot = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise SmcsdError("cos_sin must be [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+    S, cu, ctx = _lengths(cu_tokens, ctx_lens, dev)
+    tables, _, M_cap = _tables(block_tables, S, dev)
+    i32 = torch.int32
+    rc = _L().smcsd_kv_append(
+        qp, kp, vp, dt, qs, ks, vs, S, T, cu, Hq, Hkv, D, _addr(q_weight, "q_weight", dtype, D, dev),
+        _addr(k_weight, "k_weight", dtype, D, dev), eps, _addr(cos_sin, "cos_sin", torch.float32, 0, dev),
+        max_pos, rot, 1 if interleaved else 0, _addr(positions, "positions", i32, T, dev), ctx, tables,
+        M_cap, bs, P, DTYPE_E4M3 if e4m3 else dt, k_cache.data_ptr(), v_cache.data_ptr(), page, token,
+        head, sk, sv, qo, _need(status, "status", i32, 1, dev), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_kv_append")
+
+
+def prompt_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, ctx_lens: Optional[torch.Tensor],
+                     cu_tokens: torch.Tensor, scale: float, out: torch.Tensor, status: torch.Tensor,
+                     workspace: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                     v_scales: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     max_len: int = 0, stream=None) -> None:
+    """smcsd_prompt_attention.  q [T, Hq, D] (bf16 or f16); k_cache, v_cache seen as [P,
+    block_size, Hkv, D] with any strides between rows of D, of q's type or float8_e4m3fn with
+    k_scales, v_scales [P, Hkv] uint8; ctx_lens [S] (None: empty caches) and cu_tokens [S + 1]
+    int32; out [T, Hq, D]; lse [T, Hq] fp32.  workspace from alloc_workspace(OP_PROMPT_ATTN, S, T,
+    K=D, V=Hq * D, P=Hkv)."""
+    dev = _device_of(status, "status")
+    dt = _kv_dtype(q)
+    dtype = q.dtype
+    if q.dim() != 3:
+        raise SmcsdError("q must be [T, heads, D]")
+    T, _, D = q.shape
+    qp, Hq, qs = _packed(q, "q", T, D, dtype, dev)
+    P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, _cache_dtype(k_cache, dtype), D, dev)
+    e4m3, sk, sv = _scale_pair(k_cache, k_scales, v_scales, P, Hkv, dev)
+    S, cu, ctx = _lengths(cu_tokens, ctx_lens, dev)
+    tables, _, M_cap = _tables(block_tables, S, dev)
+    rc = _L().smcsd_prompt_attention(
+        qp, dt, qs, DTYPE_E4M3 if e4m3 else dt, k_cache.data_ptr(), v_cache.data_ptr(), page, token,
+        head, sk, sv, tables, M_cap, bs, P, ctx, cu, S, T, Hq, Hkv, D, scale, max_len,
+        _need(out, "out", dtype, T * Hq * D, dev), _addr(lse, "lse", torch.float32, T * Hq, dev),
+        _need(status, "status", torch.int32, 1, dev), _need(workspace, "workspace", torch.uint8, 0, dev),
+        workspace.numel(), _queue(stream, dev))
+    if rc:
+        _check(rc, "smcsd_prompt_attention")
+
+
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_tables: torch.Tensor, ctx_lens: torch.Tensor, B: int, N: int,
                    scale: float, out: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
                    tree_mask: Optional[torch.Tensor] = None,
                    num_nodes: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                   max_len: int = 0, stream=None) -> None:
+                   max_len: int = 0, stream=None, k_scales: Optional[torch.Tensor] = None,
+                   v_scales: Optional[torch.Tensor] = None) -> None:
     """smcsd_tree_attention.  q [B*N, R, Hq, D] (bf16 or f16); k_cache, v_cache seen as [P,
-    block_size, Hkv, D] with any strides between rows of D; out [B*N, R, Hq, D]; tree_mask
+    block_size, Hkv, D] with any strides between rows of D, of q's type or float8_e4m3fn with
+    k_scales, v_scales [P, Hkv] uint8 (smcsd_tree_attention_e4m3); out [B*N, R, Hq, D]; tree_mask
     [B*N, R] int64 (bit j of row i: node i sees node j; None: a chain); lse [B*N, R, Hq]
     fp32.  workspace from alloc_workspace(OP_TREE_ATTN, B, N, K=R, V=Hq * D, P=Hkv)."""
     dev = _device_of(status, "status")
@@ -698,18 +852,20 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         raise SmcsdError("q must be [B*N, R, Hq, D]")
     S, R, Hq, D = q.shape
     qp, _, qs = _heads(q, "q", S, R, D, dtype, dev)
-    P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, dtype, D, dev)
+    P, bs, Hkv, page, token, head = _cache_pair(k_cache, v_cache, _cache_dtype(k_cache, dtype), D, dev)
     T, _, M_cap = _tables(block_tables, S, dev)
     i32 = torch.int32
-    rc = _L().smcsd_tree_attention(
-        qp, dt, qs, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, T, M_cap, bs, P,
+    e4m3, sk, sv = _scale_pair(k_cache, k_scales, v_scales, P, Hkv, dev)
+    entry, codes = (_L().smcsd_tree_attention_e4m3, (sk, sv)) if e4m3 else (_L().smcsd_tree_attention, ())
+    rc = entry(
+        qp, dt, qs, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, *codes, T, M_cap, bs, P,
         _need(ctx_lens, "ctx_lens", i32, S, dev), _addr(num_nodes, "num_nodes", i32, S, dev),
         _addr(tree_mask, "tree_mask", torch.int64, S * R, dev), B, N, R, Hq, Hkv, D, scale,
         max_len, _need(out, "out", dtype, S * R * Hq * D, dev),
         _addr(lse, "lse", torch.float32, S * R * Hq, dev), _need(status, "status", i32, 1, dev),
         _need(workspace, "workspace", torch.uint8, 0, dev), workspace.numel(), _queue(stream, dev))
     if rc:
-        _check(rc, "smcsd_tree_attention")
+        _check(rc, "smcsd_tree_attention_e4m3" if e4m3 else "smcsd_tree_attention")
 
 
 def token_logprobs(logits: torch.Tensor, n: int, V: int, temperature: float, status: torch.Tensor,

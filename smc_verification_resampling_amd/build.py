@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build", "smcsd")
 LIB = os.path.join(HERE, "libsmcsd.so")
 SOURCES = ["capi.hip", "verify.hip", "resample.hip", "kv.hip", "kvcheck.hip", "streamread.hip",
-           "kvpages.hip", "qknorm.hip", "treeattn.hip", "logprobs.hip"]
+           "kvpages.hip", "qknorm.hip", "kvappend.hip", "treeattn.hip", "promptattn.hip",
+           "logprobs.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -66,6 +66,12 @@ size_t smcsd_workspace_bytes(int op, int B, int N, int K, int V, int64_t P) {
       return 0;
     return tree_attn_ws_bytes(B, N, K, V, P);
   }
+  if (op == SMCSD_OP_PROMPT_ATTN) {
+    if (K < 8 || K > kMaxHeadDim || K % 8 || V < 1 || V % K || P < 1 || P > INT32_MAX || (V / K) % P ||
+        (int64_t)N * (V / K) > kMaxPromptRows || B * P > kMaxPromptHeads)
+      return 0;
+    return prompt_attn_ws_bytes(N, K, (int)(V / K / P));
+  }
   if (op == SMCSD_OP_LOGPROBS) {
     if (V < 1 || V > kMaxV || K < 0 || K > kMaxTop || K > V || S > INT32_MAX) return 0;
     return logprobs_ws_bytes(S, K, V);
@@ -449,7 +455,26 @@ int smcsd_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int s
   if (!caches || !list || !count || !status) return SMCSD_EINVAL;
   for (int i = 0; i < n_caches; ++i)
     if (!caches[i]) return SMCSD_EINVAL;
-  return hip_rc(launch_kv_copy(caches, n_caches, block_stride, segments, segment_stride,
+  return hip_rc(launch_kv_copy(caches, nullptr, 0, n_caches, block_stride, segments, segment_stride,
+                               token_bytes, block_size, list, count, capacity, P, status,
+                               as_stream(stream)));
+}
+
+int smcsd_kv_copy_scaled(void *const *caches, uint8_t *const *scales, int n_caches, int Hkv,
+                         int64_t block_stride, int segments, int64_t segment_stride,
+                         int64_t token_bytes, int block_size, const int32_t *list,
+                         const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
+                         void *stream) {
+  if (n_caches < 0 || n_caches > SMCSD_KV_COPY_SCALED_MAX_CACHES || segments < 1 || token_bytes < 1 ||
+      block_size < 1 || token_bytes > INT32_MAX || block_size * token_bytes > INT32_MAX ||
+      block_stride < 0 || segment_stride < 0 || P < 1 || P > INT32_MAX || capacity < 0 ||
+      capacity > INT32_MAX || Hkv < 1 || P * Hkv >= (1LL << 40))
+    return SMCSD_EINVAL;
+  if (n_caches == 0 || capacity == 0) return SMCSD_OK;
+  if (!caches || !scales || !list || !count || !status) return SMCSD_EINVAL;
+  for (int i = 0; i < n_caches; ++i)
+    if (!caches[i] || !scales[i]) return SMCSD_EINVAL;
+  return hip_rc(launch_kv_copy(caches, scales, Hkv, n_caches, block_stride, segments, segment_stride,
                                token_bytes, block_size, list, count, capacity, P, status,
                                as_stream(stream)));
 }
@@ -460,6 +485,11 @@ static bool paged_ok(const void *k, const void *v, int64_t page, int64_t token, 
   return k && v && aligned(k, 16) && aligned(v, 16) && page >= D && token >= D && head >= D &&
          page % 8 == 0 && token % 8 == 0 && head % 8 == 0 && tables && M_cap >= 1 &&
          block_size >= 1 && (int64_t)M_cap * block_size < INT32_MAX - 4096 && P >= 1 && P <= INT32_MAX;
+}
+// What 8-bit pages ask for beside that: rows that 16-byte loads divide, and scales.
+static bool e4m3_ok(int64_t page, int64_t token, int64_t head, int D, const void *k_scales,
+                    const void *v_scales) {
+  return D % 16 == 0 && page % 16 == 0 && token % 16 == 0 && head % 16 == 0 && k_scales && v_scales;
 }
 
 int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
@@ -521,9 +551,73 @@ int smcsd_qk_norm_rope(const void *q, const void *k, const void *v, int dtype, i
   return hip_rc(launch_qk_norm_rope(a, dtype, as_stream(stream)));
 }
 
-int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+int smcsd_kv_append(const void *q, const void *k, const void *v, int dtype, int64_t q_stride,
+                    int64_t k_stride, int64_t v_stride, int S, int T, const int32_t *cu_tokens,
+                    int Hq, int Hkv, int D, const void *q_weight, const void *k_weight, float eps,
+                    const float *cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                    const int32_t *positions, const int32_t *ctx_lens,
+                    const int32_t *block_tables, int M_cap, int block_size, int64_t P,
+                    int cache_dtype, void *k_cache, void *v_cache, int64_t page_stride,
+                    int64_t token_stride, int64_t head_stride, uint8_t *k_scales,
+                    uint8_t *v_scales, void *q_out, int32_t *status, void *stream) {
+  if (dtype != SMCSD_DTYPE_BF16 && dtype != SMCSD_DTYPE_F16) return SMCSD_EDTYPE;
+  const bool e4m3 = cache_dtype == SMCSD_DTYPE_E4M3;
+  if (!e4m3 && cache_dtype != dtype) return SMCSD_EDTYPE;
+  if (S < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq > INT32_MAX / 4 || Hkv > INT32_MAX / 8 || D < 8 ||
+      D > kMaxHeadDim || D % 8 || rot_dim < 0 || rot_dim > D || rot_dim % 16 || max_pos < 0 ||
+      !(eps >= 0.0f) || !std::isfinite(eps))
+    return SMCSD_EINVAL;
+  if (S == 0 || T == 0) return SMCSD_OK;
+  if ((int64_t)Hq * D >= INT32_MAX || (int64_t)Hkv * D >= INT32_MAX || T >= INT32_MAX ||
+      S >= INT32_MAX || (int64_t)T * (Hq + 2 * Hkv) >= INT32_MAX || (int64_t)S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if ((q && (q_stride < (int64_t)Hq * D || q_stride % 8)) || k_stride < (int64_t)Hkv * D ||
+      v_stride < (int64_t)Hkv * D || k_stride % 8 || v_stride % 8)
+    return SMCSD_EINVAL;
+  if (!k || !v || !q != !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+      !aligned(cos_sin, 16) || (rot_dim > 0 && !cos_sin) || !cu_tokens || !status)
+    return SMCSD_EINVAL;
+  if (!paged_ok(k_cache, v_cache, page_stride, token_stride, head_stride, block_tables, M_cap,
+                block_size, P, D))
+    return SMCSD_EINVAL;
+  if (e4m3 && !e4m3_ok(page_stride, token_stride, head_stride, D, k_scales, v_scales)) return SMCSD_EINVAL;
+  KvAppendArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k = static_cast<const uint16_t *>(k);
+  a.v = static_cast<const uint16_t *>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.S = S;
+  a.T = T;
+  a.cu = cu_tokens;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.q_weight = static_cast<const uint16_t *>(q_weight);
+  a.k_weight = static_cast<const uint16_t *>(k_weight);
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  a.positions = positions;
+  a.ctx_lens = ctx_lens;
+  a.cache = PagedCache{page_stride, token_stride, head_stride, block_tables, M_cap, block_size, P};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.q_out = static_cast<uint16_t *>(q_out);
+  a.status = status;
+  return hip_rc(launch_kv_append(a, dtype, e4m3, as_stream(stream)));
+}
+
+static int tree_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
                          const void *v_cache, int64_t page_stride, int64_t token_stride,
-                         int64_t head_stride, const int32_t *block_tables, int M_cap,
+                         int64_t head_stride, bool e4m3, const uint8_t *k_scales,
+                         const uint8_t *v_scales, const int32_t *block_tables, int M_cap,
                          int block_size, int64_t P, const int32_t *ctx_lens,
                          const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N, int R,
                          int Hq, int Hkv, int D, float scale, int64_t max_len, void *out,
@@ -544,13 +638,16 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
   if (!paged_ok(k_cache, v_cache, page_stride, token_stride, head_stride, block_tables, M_cap,
                 block_size, P, D))
     return SMCSD_EINVAL;
+  if (e4m3 && !e4m3_ok(page_stride, token_stride, head_stride, D, k_scales, v_scales)) return SMCSD_EINVAL;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < tree_attn_ws_bytes(B, N, R, (int64_t)Hq * D, Hkv))
     return SMCSD_EWORKSPACE;
   TreeAttnArgs a{};
   a.q = static_cast<const uint16_t *>(q);
-  a.k_cache = static_cast<const uint16_t *>(k_cache);
-  a.v_cache = static_cast<const uint16_t *>(v_cache);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = e4m3 ? k_scales : nullptr;
+  a.v_scales = e4m3 ? v_scales : nullptr;
   a.q_stride = q_stride;
   a.cache = PagedCache{page_stride, token_stride, head_stride, block_tables, M_cap, block_size, P};
   a.ctx_lens = ctx_lens;
@@ -569,6 +666,87 @@ int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void 
   a.status = status;
   a.ws = static_cast<char *>(workspace);
   return hip_rc(launch_tree_attn(a, dtype, as_stream(stream)));
+}
+
+int smcsd_tree_attention(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                         const void *v_cache, int64_t page_stride, int64_t token_stride,
+                         int64_t head_stride, const int32_t *block_tables, int M_cap,
+                         int block_size, int64_t P, const int32_t *ctx_lens,
+                         const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N, int R,
+                         int Hq, int Hkv, int D, float scale, int64_t max_len, void *out,
+                         float *lse, int32_t *status, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+  return tree_attention(q, dtype, q_stride, k_cache, v_cache, page_stride, token_stride, head_stride,
+                        false, nullptr, nullptr, block_tables, M_cap, block_size, P, ctx_lens,
+                        num_nodes, tree_mask, B, N, R, Hq, Hkv, D, scale, max_len, out, lse, status,
+                        workspace, workspace_bytes, stream);
+}
+
+int smcsd_tree_attention_e4m3(const void *q, int dtype, int64_t q_stride, const void *k_cache,
+                              const void *v_cache, int64_t page_stride, int64_t token_stride,
+                              int64_t head_stride, const uint8_t *k_scales,
+                              const uint8_t *v_scales, const int32_t *block_tables, int M_cap,
+                              int block_size, int64_t P, const int32_t *ctx_lens,
+                              const int32_t *num_nodes, const uint64_t *tree_mask, int B, int N,
+                              int R, int Hq, int Hkv, int D, float scale, int64_t max_len,
+                              void *out, float *lse, int32_t *status, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+  return tree_attention(q, dtype, q_stride, k_cache, v_cache, page_stride, token_stride, head_stride,
+                        true, k_scales, v_scales, block_tables, M_cap, block_size, P, ctx_lens,
+                        num_nodes, tree_mask, B, N, R, Hq, Hkv, D, scale, max_len, out, lse, status,
+                        workspace, workspace_bytes, stream);
+}
+
+int smcsd_prompt_attention(const void *q, int dtype, int64_t q_stride, int cache_dtype,
+                           const void *k_cache, const void *v_cache, int64_t page_stride,
+                           int64_t token_stride, int64_t head_stride, const uint8_t *k_scales,
+                           const uint8_t *v_scales, const int32_t *block_tables, int M_cap,
+                           int block_size, int64_t P, const int32_t *ctx_lens,
+                           const int32_t *cu_tokens, int S, int T, int Hq, int Hkv, int D,
+                           float scale, int64_t max_len, void *out, float *lse, int32_t *status,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+  if (dtype != SMCSD_DTYPE_BF16 && dtype != SMCSD_DTYPE_F16) return SMCSD_EDTYPE;
+  const bool e4m3 = cache_dtype == SMCSD_DTYPE_E4M3;
+  if (!e4m3 && cache_dtype != dtype) return SMCSD_EDTYPE;
+  if (S < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 8 || D > kMaxHeadDim || D % 8 ||
+      !(std::fabs(scale) <= 0x1p127f) || max_len < 0)
+    return SMCSD_EINVAL;  // (times log2(e), a scale past 2^127 could be infinite)
+  if (S == 0 || T == 0) return SMCSD_OK;
+  if ((int64_t)T * Hq > kMaxPromptRows || (int64_t)S * Hkv > kMaxPromptHeads ||
+      (int64_t)Hq * D >= INT32_MAX || (int64_t)S * M_cap >= INT32_MAX)
+    return SMCSD_EINVAL;
+  if (q_stride < (int64_t)Hq * D || q_stride % 8 || !q || !aligned(q, 16) || !out ||
+      !aligned(out, 16) || !cu_tokens || !status)
+    return SMCSD_EINVAL;
+  if (!paged_ok(k_cache, v_cache, page_stride, token_stride, head_stride, block_tables, M_cap,
+                block_size, P, D))
+    return SMCSD_EINVAL;
+  if (e4m3 && !e4m3_ok(page_stride, token_stride, head_stride, D, k_scales, v_scales)) return SMCSD_EINVAL;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < prompt_attn_ws_bytes(T, D, Hq / Hkv))
+    return SMCSD_EWORKSPACE;
+  PromptAttnArgs a{};
+  a.q = static_cast<const uint16_t *>(q);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = e4m3 ? k_scales : nullptr;
+  a.v_scales = e4m3 ? v_scales : nullptr;
+  a.q_stride = q_stride;
+  a.cache = PagedCache{page_stride, token_stride, head_stride, block_tables, M_cap, block_size, P};
+  a.ctx_lens = ctx_lens;
+  a.cu = cu_tokens;
+  a.S = S;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.scale = scale;
+  a.max_len = max_len;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.status = status;
+  a.ws = static_cast<char *>(workspace);
+  return hip_rc(launch_prompt_attn(a, dtype, as_stream(stream)));
 }
 
 int smcsd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int n, int V,

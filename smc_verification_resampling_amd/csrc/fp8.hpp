@@ -1,0 +1,68 @@
+// fp8.hpp - elements of 8-bit pages: e4m3 numbers and the codes of their scales, a power of
+// two 2^(x - 127) for each block and head.  The hardware converts eight e4m3 elements to a
+// 16-bit type in four instructions that take the scale along.
+#pragma once
+
+#include "device.hpp"
+#include "half.hpp"
+
+namespace smcsd {
+
+// The least code in [1, 247] whose scale holds magnitudes up to `top` (finite) in e4m3's range:
+// top = m * 2^k <= 448 * 2^e with 448 = 1.75 * 2^8, so e = k - 8, or one more where m > 1.75.
+__device__ __forceinline__ int code_for(float top) {
+  const uint32_t u = __float_as_uint(top);
+  const int k = (int)(u >> 23) - 127;
+  return max(1, min(247, k - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) + 127));
+}
+
+// The scale as the conversions take it, by its exponent alone: code 0 is 2^-127, 255 NaN.
+__device__ __forceinline__ float scale_of(int code) { return __uint_as_float((uint32_t)code << 23); }
+
+// Eight elements to the 16-bit type.  In f16 a value past the largest number is held there: it
+// can exceed it where the scale is 2^8 or more (448 * 2^7 is within).
+template <int DT>
+__device__ __forceinline__ uint4 widen8_e4m3(uint2 w, int code) {
+  const float s = scale_of(code);
+  uint4 r;
+  if (DT == SMCSD_DTYPE_BF16) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, s, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, s, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, s, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, s, true));
+    return r;
+  }
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, s, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, s, true));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, s, false));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, s, true));
+  if (code >= 127 + 8) {
+    auto hold = [](uint32_t v) {  // infinities (no NaN) become the largest number
+      if ((v & 0x7FFFu) == 0x7C00u) v -= 1;
+      if ((v & 0x7FFF0000u) == 0x7C000000u) v -= 0x10000u;
+      return v;
+    };
+    r.x = hold(r.x);
+    r.y = hold(r.y);
+    r.z = hold(r.z);
+    r.w = hold(r.w);
+  }
+  return r;
+}
+
+// Eight values to e4m3, to nearest even; past 448, and what is not finite: NaN.
+__device__ __forceinline__ uint2 narrow8_e4m3(f32x8 x) {
+  uint2 w;
+  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w.x, true);
+  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
+  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], w.y, true);
+  return w;
+}
+__device__ __forceinline__ f32x8 widen8_e4m3(uint2 w) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w.x, true);
+  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(w.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(w.y, true);
+  return f32x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+}  // namespace smcsd

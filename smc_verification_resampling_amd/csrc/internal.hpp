@@ -161,12 +161,13 @@ hipError_t launch_kv_free(const int32_t *freed, int64_t S, int32_t *T, int M, in
 hipError_t launch_kv_compact(int32_t *T, int64_t S, int M, int block_size, int32_t *rc, int32_t *fl,
                              int32_t *free_top, int64_t P, int32_t *moves, int32_t *move_count,
                              int32_t *status, char *ws, hipStream_t stream);
-hipError_t launch_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int segments,
+// scales: null, or n_caches arrays of Hkv codes a block
+hipError_t launch_kv_copy(void *const *caches, uint8_t *const *scales, int Hkv, int n_caches, int64_t block_stride, int segments,
                           int64_t segment_stride, int64_t token_bytes, int block_size, const int32_t *list,
                           const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
                           hipStream_t stream);
 
-// A paged cache of 16-bit elements: element d of head h of token t of block b lies at
+// A paged cache of 16- or 8-bit elements: element d of head h of token t of block b lies at
 // b * page + t * token + h * head + d (element units).
 struct PagedCache {
   int64_t page, token, head;
@@ -192,12 +193,35 @@ struct QkNormRopeArgs {
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a, int dtype, hipStream_t stream);
 
+// Packed tokens' norms, rotation and the write into pages of 16 or 8 bits (kvappend.hip).
+struct KvAppendArgs {
+  const uint16_t *q, *k, *v;  // q null: keys and values alone
+  int64_t q_stride, k_stride, v_stride;
+  int S, T;
+  const int32_t *cu;
+  int Hq, Hkv, D;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float *cos_sin;
+  int64_t max_pos;
+  int rot_dim, interleaved;
+  const int32_t *positions, *ctx_lens;  // ctx_lens null: 0
+  PagedCache cache;
+  void *k_cache, *v_cache;
+  uint8_t *k_scales, *v_scales;  // [P, Hkv]; null for 16-bit pages
+  uint16_t *q_out;
+  int32_t *status;
+};
+hipError_t launch_kv_append(const KvAppendArgs &a, int dtype, bool e4m3, hipStream_t stream);
+
 // Attention over the pages (treeattn.hip).
 constexpr int kMaxNodes = 64;
 constexpr int kMaxHeadDim = 256;
 constexpr int64_t kMaxAttnRows = (1 << 25) - 1;  // 128 threads take at least one row: fewer than 2^32 of them
 struct TreeAttnArgs {
-  const uint16_t *q, *k_cache, *v_cache;
+  const uint16_t *q;
+  const void *k_cache, *v_cache;
+  const uint8_t *k_scales, *v_scales;  // [P, Hkv]; null for 16-bit pages
   int64_t q_stride;
   PagedCache cache;
   const int32_t *ctx_lens, *num_nodes;
@@ -212,6 +236,27 @@ struct TreeAttnArgs {
 };
 size_t tree_attn_ws_bytes(int64_t B, int64_t N, int R, int64_t HqD, int64_t Hkv);
 hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream);
+
+// Causal attention of packed prompts over the pages (promptattn.hip).
+constexpr int64_t kMaxPromptRows = (1 << 30) - 1;
+constexpr int64_t kMaxPromptHeads = (1 << 22) - 1;
+struct PromptAttnArgs {
+  const uint16_t *q;
+  const void *k_cache, *v_cache;
+  const uint8_t *k_scales, *v_scales;  // [P, Hkv]; null for 16-bit pages
+  int64_t q_stride;
+  PagedCache cache;
+  const int32_t *ctx_lens, *cu;  // ctx_lens null: 0
+  int S, T, Hq, Hkv, D;
+  float scale;
+  int64_t max_len;
+  uint16_t *out;
+  float *lse;
+  int32_t *status;
+  char *ws;
+};
+size_t prompt_attn_ws_bytes(int64_t T, int D, int G);
+hipError_t launch_prompt_attn(const PromptAttnArgs &a, int dtype, hipStream_t stream);
 
 // Log-probabilities, entropy and alternatives (logprobs.hip).
 constexpr int kMaxTop = 64;

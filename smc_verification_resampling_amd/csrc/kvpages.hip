@@ -7,6 +7,8 @@
 // by the latency of a few launches (512 tables of 133 blocks, a pool of 24,576: fork 3.7 us,
 // free 3.7 + 2.2 + 2.9 us, compact 4.5 + 4.6 + 4.7 us); the order of every list they leave is
 // fixed by block ids alone, so the state does not depend on the order of the atomics.
+#include <type_traits>
+
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "internal.hpp"
@@ -281,6 +283,13 @@ struct CopyCaches {
   char *p[SMCSD_KV_COPY_MAX_CACHES];
 };
 
+// The codes of 8-bit blocks' scales, Hkv for each block of each cache; or none.
+struct CopyScales {
+  uint8_t *p[SMCSD_KV_COPY_SCALED_MAX_CACHES];
+  int Hkv;
+};
+struct NoScales {};
+
 constexpr int kCopyUnroll = 4;
 constexpr uint32_t kCopyWords = 1 << 20;
 
@@ -288,8 +297,8 @@ constexpr uint32_t kCopyWords = 1 << 20;
 // W: bytes moved at once.  Bound by memory: 1.6 GB of a compaction's moves take 320 us (5.0 TB/s
 // read and written, the rate of a large copy); 67 MB of copy-on-write tails 26 us (2.6 TB/s, their
 // pages lie scattered and each is a few KB).
-template <typename W>
-__global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, int n_caches, int64_t block_stride,
+template <typename W, typename Scales>
+__global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, Scales scales, int n_caches, int64_t block_stride,
                                                    int segments, int64_t segment_stride,
                                                    int64_t token_bytes, int block_size,
                                                    const int32_t *__restrict__ list,
@@ -313,6 +322,11 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, int n_cach
     char *to = caches.p[c] + dst * block_stride;
     const uint32_t per = (uint32_t)(tokens * token_bytes / (int)sizeof(W));  // words of a segment
     if (per == 0) continue;
+    if constexpr (std::is_same<Scales, CopyScales>::value) {
+      const uint8_t *from_s = scales.p[c] + (int64_t)src * scales.Hkv;
+      uint8_t *to_s = scales.p[c] + (int64_t)dst * scales.Hkv;
+      for (int h = threadIdx.x; h < scales.Hkv; h += kPgBlock) to_s[h] = from_s[h];
+    }
     // some segments at a time, few enough for 32-bit word numbers
     const int most = (int)max(1u, kCopyWords / per);
     for (int h0 = 0; h0 < segments; h0 += most) {
@@ -387,10 +401,10 @@ hipError_t launch_kv_compact(int32_t *T, int64_t S, int M, int block_size, int32
   return hipGetLastError();
 }
 
-hipError_t launch_kv_copy(void *const *caches, int n_caches, int64_t block_stride, int segments,
-                          int64_t segment_stride, int64_t token_bytes, int block_size, const int32_t *list,
-                          const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
-                          hipStream_t stream) {
+template <typename Scales>
+static hipError_t launch_copy(void *const *caches, const Scales &scales, int n_caches, int64_t block_stride, int segments,
+                              int64_t segment_stride, int64_t token_bytes, int block_size, const int32_t *list,
+                              const int32_t *count, int64_t capacity, int64_t P, int32_t *status, hipStream_t stream) {
   CopyCaches cc{};
   uint64_t low = (uint64_t)block_stride | (uint64_t)segment_stride | (uint64_t)token_bytes;
   for (int i = 0; i < n_caches; ++i) {
@@ -399,15 +413,29 @@ hipError_t launch_kv_copy(void *const *caches, int n_caches, int64_t block_strid
   }
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(capacity * n_caches, 2048)));
   if (low % 16 == 0)
-    hipLaunchKernelGGL(k_copy<uint4>, grid, dim3(kPgBlock), 0, stream, cc, n_caches, block_stride, segments,
+    hipLaunchKernelGGL((k_copy<uint4, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
                        segment_stride, token_bytes, block_size, list, count, capacity, P, status);
   else if (low % 4 == 0)
-    hipLaunchKernelGGL(k_copy<uint32_t>, grid, dim3(kPgBlock), 0, stream, cc, n_caches, block_stride, segments,
+    hipLaunchKernelGGL((k_copy<uint32_t, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
                        segment_stride, token_bytes, block_size, list, count, capacity, P, status);
   else
-    hipLaunchKernelGGL(k_copy<uint8_t>, grid, dim3(kPgBlock), 0, stream, cc, n_caches, block_stride, segments,
+    hipLaunchKernelGGL((k_copy<uint8_t, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
                        segment_stride, token_bytes, block_size, list, count, capacity, P, status);
   return hipGetLastError();
+}
+
+hipError_t launch_kv_copy(void *const *caches, uint8_t *const *scales, int Hkv, int n_caches, int64_t block_stride, int segments,
+                          int64_t segment_stride, int64_t token_bytes, int block_size, const int32_t *list,
+                          const int32_t *count, int64_t capacity, int64_t P, int32_t *status,
+                          hipStream_t stream) {
+  if (!scales)
+    return launch_copy(caches, NoScales{}, n_caches, block_stride, segments, segment_stride, token_bytes, block_size, list, count,
+                       capacity, P, status, stream);
+  CopyScales cs{};
+  for (int i = 0; i < n_caches; ++i) cs.p[i] = scales[i];
+  cs.Hkv = Hkv;
+  return launch_copy(caches, cs, n_caches, block_stride, segments, segment_stride, token_bytes, block_size, list, count, capacity, P,
+                     status, stream);
 }
 
 }  // namespace smcsd

@@ -1,0 +1,40 @@
+// packed.hpp - sequences of different lengths packed one after the other: sequence s has the
+// tokens cu[s] .. cu[s + 1] - 1.  Which sequence a workgroup's item belongs to is found on the
+// device, by a wave, 64 sequences at a time.
+#pragma once
+
+#include "device.hpp"
+
+namespace smcsd {
+
+// cu[s] held within [0, T], so that whatever stands there, what is derived from it stays small.
+__device__ __forceinline__ int held_cu(const int32_t *cu, int s, int T) { return max(0, min(cu[s], T)); }
+
+// The largest s in [0, S) with first(s) <= x, where first does not decrease (0 if there is
+// none): every wave for itself, two rounds of loads for up to 4096 sequences.
+template <class F>
+__device__ __forceinline__ int find_sequence(int S, int64_t x, F first) {
+  const int lane = threadIdx.x % kWave;
+  int lo = 0, n = S;
+  while (n > 1) {
+    const int step = (n + kWave - 1) / kWave;
+    const int at = lo + min(lane * step, n - 1);
+    const bool below = lane * step < n && first(at) <= x;
+    const int count = max(1, (int)__popcll(__ballot(below)));
+    lo += (count - 1) * step;
+    n = min(step, n - (count - 1) * step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Whether the workgroup's share of the S pairs is in order; pairs are shared out over the grid.
+__device__ __forceinline__ bool lengths_in_order(const int32_t *cu, int S, int T) {
+  bool good = true;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < S; i += (int64_t)gridDim.x * blockDim.x) {
+    const int32_t a = cu[i], b = cu[i + 1];
+    good &= a >= 0 && b >= a && b <= T;
+  }
+  return good;
+}
+
+}  // namespace smcsd

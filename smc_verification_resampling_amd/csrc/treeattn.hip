@@ -16,9 +16,11 @@
 // Long contexts are split over workgroups (each a range of keys of equal length) and the
 // parts (m, l, O) joined in fp32.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/smcsd.h"
 #include "device.hpp"
+#include "fp8.hpp"
 #include "half.hpp"
 #include "internal.hpp"
 
@@ -27,6 +29,7 @@ namespace smcsd {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Reads of a tile.  In assembly, each with its wait: the compiler, which knows no buffers,
 // would let a read of one wait for all loads to LDS, those of the next tiles too.
@@ -263,7 +266,7 @@ __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothin
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 5.6 us, all of it latency.
-template <int DT, int DP, int NW, bool PREFIX>
+template <int DT, int DP, int NW, bool PREFIX, bool E4>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
@@ -275,7 +278,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   constexpr int RW = kWave / CH;             // rows of a wave's load
   constexpr int NLD = KT / (RW * NW);        // loads of keys (and as many of values) of a wave for a tile
   __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
-  __shared__ uint32_t sOdd[PREFIX ? 1 : KT];  // a new token whose values are not all finite
+  __shared__ uint32_t sOdd[PREFIX ? 1 : E4 ? 2 * KT : KT];  // a new token whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int hw = lane / 32, col = lane % 32;
   const Cut &cut = PREFIX ? p.prefix : p.suffix;
@@ -317,8 +320,9 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   // rows itself, one to a lane (row lane % KT), and its lanes take their rows' places from
   // there.
   const int32_t *table = a.cache.tables + (int64_t)s0 * a.cache.M_cap;
-  const uint16_t *const kbase = a.k_cache + (int64_t)hk * a.cache.head;
-  const uint16_t *const vbase = a.v_cache + (int64_t)hk * a.cache.head;
+  typedef typename std::conditional<E4, uint8_t, uint16_t>::type Elem;
+  const Elem *const kbase = static_cast<const Elem *>(a.k_cache) + (int64_t)hk * a.cache.head;
+  const Elem *const vbase = static_cast<const Elem *>(a.v_cache) + (int64_t)hk * a.cache.head;
   typedef __attribute__((address_space(3))) char lds_char;
   typedef __attribute__((address_space(3))) void lds_void;
   typedef __attribute__((address_space(1))) const void glb_void;
@@ -329,20 +333,25 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   int32_t ids = 0;
   int id0 = -kWave;
   bool bad_page = false;
-  // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Rows that may not
-  // be, and the padding of a head, become 0, as what such a lane loads is (0 * NaN is no 0).
-  auto fetch_tile = [&](int buf, int base) {
+  // The place of row lane % KT of the tile at `base`, -1 if it may not be read; its block.
+  auto place_row = [&](int base, int32_t &pg) {
     if ((int)div_by(p.page, min(base + KT, k1) - 1) >= id0 + kWave) {
       id0 = div_by(p.page, base);
       ids = table[min(id0 + lane, (int)div_by(p.page, k1 - 1))];
       asm volatile("" : "+v"(ids));  // waited for here, not by every tile
     }
     const int pos = base + lane % KT, block = div_by(p.page, pos);
-    const int32_t pg = __shfl(ids, min(block - id0, kWave - 1), kWave);
+    pg = __shfl(ids, min(block - id0, kWave - 1), kWave);
     const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
     bad_page |= !page_ok && pos < k1;
-    const uint64_t rows = __ballot(ok);
-    const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
+    return ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
+  };
+  // Starts a tile's loads into buffer `buf`; which of its rows may be read.  Rows that may not
+  // be, and the padding of a head, become 0, as what such a lane loads is (0 * NaN is no 0).
+  auto fetch_tile = [&](int buf, int base) {
+    int32_t pg;
+    const int64_t off = place_row(base, pg);
+    const uint64_t rows = __ballot(off >= 0);
     constexpr int NAT = NLD < 4 ? NLD : 4;  // looked up together
     // Up to 64 rows are one workgroup's, and it alone reads its keys: past the caches (nt).  256
     // sequences of 9 x 32 heads, 3.2 GB, 608 us against 660, of one x 32 heads 577 against 628 (both
@@ -362,8 +371,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
         const int first = ((i0 + i) * NW + wave) * RW;
         const int chunk = (lane % CH) ^ place_of<CH>(first + lane / CH);
         const bool in = at[i] >= 0 && chunk * 8 < a.D;
-        const uint16_t *const k = in ? kbase + at[i] + chunk * 8 : (const uint16_t *)&kNothing;
-        const uint16_t *const v = in ? vbase + at[i] + chunk * 8 : (const uint16_t *)&kNothing;
+        const Elem *const k = in ? kbase + at[i] + chunk * 8 : (const Elem *)&kNothing;
+        const Elem *const v = in ? vbase + at[i] + chunk * 8 : (const Elem *)&kNothing;
         __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * RB), 16, 0, kPolicy);
         __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB + buf) * TB + first * RB), 16, 0, kPolicy);
       }
@@ -430,6 +439,66 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       const uint64_t any = __ballot(odd);
       if (odd) *reinterpret_cast<uint4 *>(v) = w;
       if (lane % CH == 0) sOdd[row] = (any >> lane) & ((1ull << CH) - 1) ? 1 : 0;
+    }
+  };
+
+  // 8-bit pages: a tile comes through registers, 16 elements to a lane, and is widened with its
+  // blocks' scales on its way to LDS, where it lies as a tile of 16-bit pages does.  Two tiles are
+  // on their way while a third is computed.  What `mend` does for new tokens happens on the way.
+  constexpr int CH8 = DP / 16;                        // 16-byte chunks of a row of 8-bit elements
+  constexpr int NL8 = (KT * CH8 + NW * kWave - 1) / (NW * kWave);
+  struct Tile {
+    u32x4 k[NL8], v[NL8];
+    int ks, vs;     // codes of the scales of row lane % KT
+    uint64_t rows;  // which may be read
+  };
+  auto ask_tile = [&](Tile &t, int base) {
+    int32_t pg;
+    const int64_t off = place_row(base, pg);
+    t.rows = __ballot(off >= 0);
+    t.ks = t.vs = 127;
+    if (off >= 0) {
+      t.ks = a.k_scales[(int64_t)pg * a.Hkv + hk];
+      t.vs = a.v_scales[(int64_t)pg * a.Hkv + hk];
+    }
+    int64_t at[NL8];
+#pragma unroll
+    for (int i = 0; i < NL8; ++i) at[i] = __shfl((long long)off, min(((i * NW + wave) * kWave + lane) / CH8, KT - 1), kWave);
+#pragma unroll
+    for (int i = 0; i < NL8; ++i) {
+      const int chunk = lane % CH8;
+      const bool in = at[i] >= 0 && chunk * 16 < a.D;
+      const u32x4 *const k = in ? (const u32x4 *)(kbase + at[i] + chunk * 16) : (const u32x4 *)&kNothing;
+      const u32x4 *const v = in ? (const u32x4 *)(vbase + at[i] + chunk * 16) : (const u32x4 *)&kNothing;
+      t.k[i] = *k;
+      t.v[i] = *v;
+    }
+  };
+  auto put_tile = [&](const Tile &t, int buf, int base) {
+    const bool fresh = !PREFIX && base + KT > ctx;
+#pragma unroll
+    for (int i = 0; i < NL8; ++i) {
+      const int idx = (i * NW + wave) * kWave + lane, row = idx / CH8, chunk = 2 * (idx % CH8);
+      const int ks = __shfl(t.ks, min(row, KT - 1), kWave), vs = __shfl(t.vs, min(row, KT - 1), kWave);
+      uint4 k[2] = {widen8_e4m3<DT>(make_uint2(t.k[i][0], t.k[i][1]), ks), widen8_e4m3<DT>(make_uint2(t.k[i][2], t.k[i][3]), ks)};
+      uint4 v[2] = {widen8_e4m3<DT>(make_uint2(t.v[i][0], t.v[i][1]), vs), widen8_e4m3<DT>(make_uint2(t.v[i][2], t.v[i][3]), vs)};
+      if (fresh) {
+        bool odd = false;
+        if (base + row >= ctx)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) odd |= (finite(v[c].x) & finite(v[c].y) & finite(v[c].z) & finite(v[c].w)) != ~0u;
+        const uint64_t any = __ballot(odd);
+        if (lane % CH8 == 0 && row < KT) sOdd[buf * KT + row] = (any >> lane) & ((1ull << CH8) - 1) ? 1 : 0;
+      }
+      if (KT * CH8 % (NW * kWave) == 0 || row < KT) {
+        const int place = place_of<CH>(row);
+        char *const kr = sKV + buf * TB + row * RB, *const vr = kr + NB * TB;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          *reinterpret_cast<uint4 *>(kr + ((chunk + c) ^ place) * 16) = k[c];
+          *reinterpret_cast<uint4 *>(vr + ((chunk + c) ^ place) * 16) = v[c];
+        }
+      }
     }
   };
 
@@ -522,7 +591,47 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   uint64_t odd = 0;  // new tokens, by node, whose values are not all finite
   // a wave without rows only loads (of four, the last one of a tile of 96 rows among them)
   const bool busy = wave * kRowsWave < cut.tile_rows && tile * cut.tile_rows + wave * kRowsWave < cut.rows;
-  if (k0 < k1) {
+  auto turn_buffers = [&](int d) {
+#pragma unroll
+    for (int st = 0; st < NKA; ++st) ka[st] += d;
+#pragma unroll
+    for (int t = 0; t < NVT; ++t) {
+      va[t][0] += d;
+      va[t][1] += d;
+    }
+  };
+  if constexpr (E4) {
+    if (k0 < k1) {
+      Tile even, uneven;
+      ask_tile(even, k0);
+      put_tile(even, 0, k0);
+      uint64_t ok = even.rows;
+      if (k0 + KT < k1) ask_tile(even, k0 + KT);
+      if (k0 + 2 * KT < k1) ask_tile(uneven, k0 + 2 * KT);
+      // the tile at `base` in buffer `buf`; `next`: the one behind it, then the one three further
+      auto turn = [&](Tile &next, int buf, int base) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const uint64_t now = ok;
+        if (!PREFIX && base + KT > ctx) {
+          const uint64_t rows = __ballot(lane < KT && sOdd[buf * KT + lane % KT]);
+          odd |= base >= ctx ? rows << (base - ctx) : rows >> (ctx - base);
+        }
+        if (base + KT < k1) {
+          put_tile(next, buf ^ 1, base + KT);
+          ok = next.rows;
+          if (base + 3 * KT < k1) ask_tile(next, base + 3 * KT);
+        }
+        if (busy) step(base, now);
+        turn_buffers(buf ? -TB : TB);
+      };
+      for (int base = k0; base < k1; base += 2 * KT) {
+        turn(even, 0, base);
+        if (base + KT < k1) turn(uneven, 1, base + KT);
+      }
+    }
+  } else if (k0 < k1) {
     uint64_t next_ok = fetch_tile(0, k0);
     int buf = 0;
     for (int base = k0; base < k1; base += KT) {
@@ -542,15 +651,8 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       }
       if (busy) step(base, ok);
       // the next buffer's offsets
-      const int d = buf ? -TB : TB;
+      turn_buffers(buf ? -TB : TB);
       buf ^= 1;
-#pragma unroll
-      for (int st = 0; st < NKA; ++st) ka[st] += d;
-#pragma unroll
-      for (int t = 0; t < NVT; ++t) {
-        va[t][0] += d;
-        va[t][1] += d;
-      }
     }
   }
   while (!PREFIX && odd) {
@@ -558,13 +660,20 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     const int node = __builtin_ctzll(odd), pos = ctx + node;
     odd &= odd - 1;
     const int block = div_by(p.page, pos);
-    const uint16_t *vp = vbase + table[block] * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token;
+    const Elem *vp = vbase + table[block] * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token;
     const bool seen = (bits >> node) & 1;
 #pragma unroll
     for (int t = 0; t < NA; ++t)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int d = 32 * t + 8 * b + 4 * hw;
+        if constexpr (E4) {  // no number but NaN is not finite: by element, or by the block's scale
+          uint32_t x = 0;
+          if (d < a.D) x = a.v_scales[(int64_t)table[block] * a.Hkv + hk] == 255 ? ~0u : *reinterpret_cast<const uint32_t *>(vp + d);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[t][4 * b + c] += seen && ((x >> (8 * c)) & 0x7F) == 0x7F ? NAN : 0.0f;
+          continue;
+        }
         uint16_t x[4] = {0, 0, 0, 0};
         if (d < a.D) *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(vp + d);
 #pragma unroll
@@ -701,25 +810,25 @@ __global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p
   }
 }
 
-template <int DT, int DP, bool PREFIX>
+template <int DT, int DP, bool PREFIX, bool E4>
 void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const Cut &c = PREFIX ? p.prefix : p.suffix;
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
   if (c.waves == 2)
-    hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX, E4>), grid, block, 0, stream, a, p);
   else
-    hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX, E4>), grid, block, 0, stream, a, p);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool E4>
 void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStream_t stream) {
   const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
   if (p.prefix.splits > 0) {
     hipLaunchKernelGGL(k_shared_len, dim3(grid_blocks(a.B, kShareBlock)), dim3(kShareBlock), 0, stream, a, shared_len);
-    launch_part<DT, DP, true>(a, p, stream);
+    launch_part<DT, DP, true, E4>(a, p, stream);
   }
-  launch_part<DT, DP, false>(a, p, stream);
+  launch_part<DT, DP, false, E4>(a, p, stream);
   if (p.suffix.splits > 1) {
     // four parts or more to a group
     const int width = join_width(a.D), parts = p.prefix.splits + p.suffix.splits;
@@ -727,6 +836,19 @@ void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStr
     while (per < kJoinBlock / width && 8 * per <= parts) per *= 2;
     hipLaunchKernelGGL(k_attn_join<DT>, dim3(grid_blocks(ceil_div(rows * per * width, kJoinBlock), kJoinBlock)),
                        dim3(kJoinBlock), 0, stream, a, p, rows, width, per);
+  }
+}
+
+template <int DT>
+void launch_pages(const TreeAttnArgs &a, const Plan &p, int DP, int32_t *shared_len, hipStream_t stream) {
+  if (a.k_scales) {
+    if (DP == 64) launch_dp<DT, 64, true>(a, p, shared_len, stream);
+    else if (DP == 128) launch_dp<DT, 128, true>(a, p, shared_len, stream);
+    else launch_dp<DT, 256, true>(a, p, shared_len, stream);
+  } else {
+    if (DP == 64) launch_dp<DT, 64, false>(a, p, shared_len, stream);
+    else if (DP == 128) launch_dp<DT, 128, false>(a, p, shared_len, stream);
+    else launch_dp<DT, 256, false>(a, p, shared_len, stream);
   }
 }
 
@@ -761,15 +883,8 @@ hipError_t launch_tree_attn(const TreeAttnArgs &a, int dtype, hipStream_t stream
   p.acc = reinterpret_cast<float *>(at + align256(sizeof(float) * 2 * (size_t)(parts * rows)));
   p.c = std::max(std::fabs(a.scale) * 1.44269504088896340736f, 1e-30f);
   p.negate = a.scale < 0.0f;
-  if (dtype == SMCSD_DTYPE_BF16) {
-    if (DP == 64) launch_dp<SMCSD_DTYPE_BF16, 64>(a, p, shared_len, stream);
-    else if (DP == 128) launch_dp<SMCSD_DTYPE_BF16, 128>(a, p, shared_len, stream);
-    else launch_dp<SMCSD_DTYPE_BF16, 256>(a, p, shared_len, stream);
-  } else {
-    if (DP == 64) launch_dp<SMCSD_DTYPE_F16, 64>(a, p, shared_len, stream);
-    else if (DP == 128) launch_dp<SMCSD_DTYPE_F16, 128>(a, p, shared_len, stream);
-    else launch_dp<SMCSD_DTYPE_F16, 256>(a, p, shared_len, stream);
-  }
+  if (dtype == SMCSD_DTYPE_BF16) launch_pages<SMCSD_DTYPE_BF16>(a, p, DP, shared_len, stream);
+  else launch_pages<SMCSD_DTYPE_F16>(a, p, DP, shared_len, stream);
   return hipGetLastError();
 }
 

@@ -1,0 +1,293 @@
+"""smcsd_tree_attention_e4m3 and smcsd_kv_copy_scaled: attention of drafted trees over 8-bit pages
+against the definition in 64 bits (bounds in attention_checks), and copies that take the blocks'
+scales along."""
+import math
+
+import pytest
+import torch
+
+import smc_verification_resampling_amd as sm
+from attention_checks import DT, E4M3, check_rows, on_gpu, pages, tokens_at
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+class Case:
+    """A batch over 8-bit pages in shuffled order, `shared` leading tokens common to a prompt's
+    particles, everything that no node sees NaN, scales of unused blocks among it."""
+
+    def __init__(self, dt="bf16", B=1, N=1, R=1, Hq=4, Hkv=2, D=64, lens=(17,), bs=16, shared=0, tree=False, nodes=None, layout="token", seed=0, loud=1.0,
+                 scale=None):
+        g = torch.Generator().manual_seed(seed)
+        self.dt, self.B, self.N, self.R, self.Hq, self.Hkv, self.D, self.bs = dt, B, N, R, Hq, Hkv, D, bs
+        S = self.S = B * N
+        self.lens = [lens[i % len(lens)] for i in range(S)]
+        self.nodes = [R if nodes is None else nodes[i % len(nodes)] for i in range(S)]
+        M = max(-(-(x + R) // bs) for x in self.lens) + 1
+        first = shared // bs
+        P = B * first + S * (M - first) + 3
+        ids = iter(torch.randperm(P, generator=g).tolist())
+        tables = torch.full((S, M), -1, dtype=torch.int32)
+        for b in range(B):
+            head = [next(ids) for _ in range(first)]
+            for s in range(b * N, b * N + N):
+                used = -(-(self.lens[s] + self.nodes[s]) // bs)
+                row = (head + [next(ids) for _ in range(max(0, used - first))])[:used]
+                tables[s, :used] = torch.tensor(row, dtype=torch.int32)
+        (k, sk), (v, sv) = (pages(P, bs, Hkv, D, dt, True, layout, g) for _ in range(2))
+        live = torch.zeros(P, bs, dtype=torch.bool)
+        for s in range(S):
+            p = torch.arange(self.lens[s] + self.nodes[s])
+            live[tables[s].long()[p // bs], p % bs] = True
+        for c, x in ((k, sk), (v, sv)):
+            c.view(torch.uint8)[~live] = 0x7F
+            x[~live.any(1)] = 255
+        self.tables, self.k, self.v, self.sk, self.sv = tables.cuda(), on_gpu(k), on_gpu(v), sk.cuda(), sv.cuda()
+        self.q = (loud * torch.randn((S, R, Hq, D), generator=g)).to(DT[dt]).cuda()
+        self.mask = None
+        if tree:
+            bits = torch.zeros(S, R, dtype=torch.int64)
+            for s in range(S):
+                for i in range(R):
+                    up = int(torch.randint(0, i, (1,), generator=g)) if i else None
+                    bits[s, i] = (0 if up is None else bits[s, up]) | (1 << i if i < 63 else -(1 << 63))
+            self.mask = bits.cuda()
+        self.scale = D ** -0.5 if scale is None else scale
+        self.lens_t = torch.tensor(self.lens, **I32)
+        self.nodes_t = None if nodes is None else torch.tensor(self.nodes, **I32)
+        self.out = torch.full((S, R, Hq, D), 77.0, dtype=DT[dt], device="cuda")
+        self.lse = torch.full((S, R, Hq), 77.0, device="cuda")
+        self.status = torch.zeros(1, **I32)
+        self.ws = sm.alloc_workspace(sm.OP_TREE_ATTN, B, N, K=R, V=Hq * D, P=Hkv)
+        self.ws.fill_(0xFF)
+
+    def call(self, **kw):
+        a = dict(tree_mask=self.mask, num_nodes=self.nodes_t, lse=self.lse, k_scales=self.sk, v_scales=self.sv)
+        a.update(kw)
+        sm.tree_attention(self.q, self.k, self.v, self.tables, self.lens_t, self.B, self.N, self.scale, self.out, self.status, self.ws, **a)
+        return self
+
+    def check(self, rows=None):
+        assert int(self.status) == 0
+        for s in range(self.S) if rows is None else rows:
+            n, ctx = self.nodes[s], self.lens[s]
+            assert (self.out[s, n:] == 77).all() and (self.lse[s, n:] == 77).all()
+            if n == 0:
+                continue
+            pos = torch.arange(ctx + n, device="cuda")
+            at = self.tables[s].long()[pos // self.bs]
+            k, v = (tokens_at(c, x, at, pos % self.bs, DT[self.dt]) for c, x in ((self.k, self.sk), (self.v, self.sv)))
+            sees = torch.ones(n, ctx + n, dtype=torch.bool, device="cuda")
+            j = torch.arange(n, device="cuda")
+            sees[:, ctx:] = j[None] <= j[:, None] if self.mask is None else ((self.mask[s, :n, None] >> j[None]) & 1).bool()
+            check_rows(self.q[s, :n], k, v, sees, self.scale, self.out[s, :n], self.lse[s, :n], self.dt, s)
+        return self
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 128, 192, 256])
+def test_head_sizes(dt, D):
+    Case(dt, N=2, R=3, D=D, lens=(37, 70), layout="head").call().check()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (7, 1), (16, 2), (8, 8), (32, 2)])
+@pytest.mark.parametrize("R", [1, 2, 5, 16])
+def test_head_groups_and_nodes(Hq, Hkv, R):
+    Case(Hq=Hq, Hkv=Hkv, R=R, N=2, lens=(45, 130)).call().check()
+
+
+@pytest.mark.parametrize("L", [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 300])
+@pytest.mark.parametrize("R", [1, 4])
+def test_lengths(L, R):
+    Case(lens=(L,), R=R, B=2, N=1).call().check()
+
+
+@pytest.mark.parametrize("bs", [1, 2, 3, 16, 24, 100, 256])
+@pytest.mark.parametrize("layout", ["token", "head"])
+def test_page_sizes(bs, layout):
+    Case(bs=bs, layout=layout, N=3, R=5, lens=(250, 97, 3)).call().check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R", [1, 7, 33, 64])
+@pytest.mark.parametrize("ctx", [0, 50])
+def test_trees(dt, R, ctx):
+    Case(dt, N=2, R=R, tree=True, lens=(ctx, ctx + 9), Hq=8, Hkv=1).call().check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("R", [1, 6, 40])
+def test_long_context_is_split_and_joined(D, R):
+    c = Case(B=1, N=1, R=R, Hq=8, Hkv=2, D=D, lens=(9000,), tree=True)
+    c.call(max_len=9000 + R).check()
+    first = c.out.clone(), c.lse.clone()
+    c.call(max_len=9000 + R)
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+    c.call(max_len=1).check()
+
+
+@pytest.mark.parametrize("N,shared", [(2, 64), (3, 100), (16, 512), (5, 1000)])
+@pytest.mark.parametrize("R,Hq", [(1, 2), (5, 8)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_shared_prefix(N, shared, R, Hq, D):
+    lens = tuple(shared + x for x in (0, 1, 40, 17, 133))
+    Case(B=2, N=N, R=R, Hq=Hq, Hkv=2, D=D, lens=lens, shared=shared, tree=R > 1, layout="head").call().check()
+
+
+def test_ragged_nodes_leave_rows_alone():
+    Case(B=2, N=3, R=6, nodes=(6, 0, 1, 4), lens=(40, 0, 129), tree=True).call().check()
+    Case(B=1, N=5, R=4, nodes=(0, 4, 2), lens=(300, 310), shared=288).call().check()
+
+
+def test_rows_that_see_nothing():
+    c = Case(B=1, N=4, R=5, lens=(0, 0, 30, 0), tree=True)
+    c.mask[0] = 0
+    c.mask[1, 2] = 0
+    c.mask[3, :] = 1 << 4
+    c.call().check()
+    assert (c.out[0] == 0).all() and (c.lse[0] == -math.inf).all() and (c.out[1, 2] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L", [5, 30, 31, 3000])
+def test_a_value_that_is_not_a_number_is_seen_by_its_rows_alone(D, L):
+    c, d = (Case(R=3, Hq=4, Hkv=2, D=D, lens=(L,)) for _ in range(2))
+    c.call()
+    p = L + 1
+    d.v.view(torch.uint8)[int(d.tables[0, p // 16]), p % 16, 1, 13] = 0xFF
+    d.call()
+    assert int(d.status) == 0
+    assert torch.equal(c.out[0, 0], d.out[0, 0]) and torch.equal(c.out[0, :, :2], d.out[0, :, :2])
+    assert d.out[0, 1:, 2:, 13].isnan().all()
+    rest = [i for i in range(D) if i != 13]
+    assert torch.equal(c.out[..., rest], d.out[..., rest]) and torch.equal(c.lse, d.lse)
+
+
+def test_a_new_block_that_is_no_number():
+    """Node 2 begins a block whose values' scale is NaN: nodes 0 and 1 do not see it."""
+    c, d = (Case(R=3, lens=(30,)) for _ in range(2))
+    c.call()
+    d.sv[int(d.tables[0, 2]), 0] = 255
+    d.call()
+    assert torch.equal(c.out[0, :2], d.out[0, :2]) and torch.equal(c.out[0, 2, 2:], d.out[0, 2, 2:])
+    assert d.out[0, 2, :2].isnan().all()
+
+
+def test_scales_at_the_ends_of_their_range():
+    for dt in ("bf16", "f16"):
+        c = Case(dt, R=2, lens=(100,), Hq=2, Hkv=1, scale=1e-4)
+        b = c.tables[0].long()
+        c.sv[b[1]], c.sv[b[2]], c.sv[b[3]], c.sk[b[4]] = 0, 1, 140, 0
+        c.call().check()
+
+
+def test_loud_scores():
+    Case(B=1, N=2, R=4, Hq=8, Hkv=2, D=128, lens=(333, 150), loud=40.0).call().check()
+    Case("f16", B=1, N=4, R=4, Hq=8, Hkv=2, D=128, lens=(333, 350), shared=320, loud=40.0).call().check()
+
+
+def test_bad_blocks_are_flagged_and_never_followed():
+    good = Case(B=1, N=4, R=2, lens=(100,)).call().check()
+    P = good.k.shape[0]
+    for bad in (P, -1, 2 ** 31 - 1, -2 ** 31):
+        d = Case(B=1, N=4, R=2, lens=(100,))
+        d.tables[1, 2] = bad
+        d.call()
+        assert int(d.status) == sm.ST_BAD_INPUT
+        assert torch.equal(d.out[[0, 2, 3]], good.out[[0, 2, 3]])
+        pos = torch.tensor([p for p in range(101) if p // 16 != 2], device="cuda")
+        at = d.tables[1].long()[pos // 16]
+        k, v = (tokens_at(c, x, at, pos % 16, DT[d.dt]) for c, x in ((d.k, d.sk), (d.v, d.sv)))
+        check_rows(d.q[1, :1], k, v, pos[None] >= 0, d.scale, d.out[1, :1], d.lse[1, :1], d.dt)
+
+
+def test_stream_and_graph():
+    c = Case(B=2, N=4, R=5, lens=(600, 610, 640), shared=592, tree=True)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    c.call(stream=st)
+    st.synchronize()
+    c.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call()
+    for t in range(4):
+        c.q.copy_(torch.randn_like(c.q))
+        if t == 2:
+            c.lens[1] = 599
+            c.lens_t[1] = 599
+        c.out.fill_(77)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check()
+
+
+def test_pages_past_32_bits():
+    page = 1 << 31  # bytes: block 2 begins 2^32 bytes in
+    buf = torch.zeros(2 * page + (1 << 20), dtype=torch.uint8, device="cuda").view(E4M3)
+    c = Case(B=1, N=2, R=3, Hq=4, Hkv=2, D=64, lens=(30, 12))
+    k = buf.as_strided((3, 16, 2, 64), (page, 128, 64, 1))
+    v = buf.as_strided((3, 16, 2, 64), (page, 128, 64, 1), 1 << 16)
+    c.tables = torch.tensor([[2, 0, 1], [2, -1, -1]], **I32)
+    for x in (k, v):
+        x.copy_(torch.randn(3, 16, 2, 64, device="cuda").to(E4M3))
+    c.k, c.v = k, v
+    c.sk, c.sv = (torch.randint(120, 130, (3, 2), dtype=torch.uint8, device="cuda") for _ in range(2))
+    c.call().check()
+
+
+@pytest.mark.parametrize("N,R,Hq", [(8, 5, 8), (1, 33, 8), (2, 64, 9)])
+def test_row_tiles_of_three_waves(N, R, Hq):
+    Case(B=2, N=N, R=R, Hq=Hq, Hkv=2 if Hq % 2 == 0 else 3, D=128, lens=(300, 311), shared=288 if N > 1 else 0, tree=True).call().check()
+
+
+# ------------------------------------------------------------------------------------------------ copies with scales
+def copied(caches, scales, moves, bs):
+    caches, scales = [c.view(torch.uint8).clone() for c in caches], [x.clone() for x in scales]
+    for src, dst, n in moves:
+        if dst < 0 or n == 0:
+            continue
+        for c, x in zip(caches, scales):
+            c[dst, :n] = c[src, :n]
+            x[dst] = x[src]
+    return caches, scales
+
+
+@pytest.mark.parametrize("Hkv,D,bs,layout", [(1, 16, 1, "token"), (2, 64, 16, "token"), (8, 128, 16, "head"), (3, 80, 24, "head"), (300, 16, 4, "token"),
+                                             (5, 8, 3, "token")])
+@pytest.mark.parametrize("n", [1, 2, 7])
+def test_copies_take_their_scales_along(Hkv, D, bs, layout, n):
+    g = torch.Generator().manual_seed(D)
+    P = 40
+    caches, scales = zip(*(pages(P, bs, Hkv, D, "bf16", True, layout, g) for _ in range(n)))
+    caches, scales = [on_gpu(c) for c in caches], [x.cuda() for x in scales]
+    ids = torch.randperm(P, generator=g).tolist()
+    moves = [(ids[i], ids[20 + i], [bs, 1, 0, bs // 2, bs][i % 5]) for i in range(15)] + [(ids[0], -1, bs), (ids[16], ids[17], bs), (ids[18], ids[18], bs)]
+    used = moves[:16]  # the count leaves the rest out
+    st = torch.zeros(1, **I32)
+    want = copied(caches, scales, used, bs)
+    sm.kv_copy(caches, torch.tensor(moves, **I32), torch.tensor([16], **I32), st, scales=scales)
+    assert int(st) == 0
+    for c, x, wc, wx in zip(caches, scales, *want):
+        assert torch.equal(c.view(torch.uint8), wc) and torch.equal(x, wx)
+
+
+def test_copies_of_bad_entries_leave_scales_alone():
+    g = torch.Generator().manual_seed(3)
+    c, x = pages(10, 4, 2, 16, "bf16", True, "token", g)
+    c, x = c.cuda(), x.cuda()
+    moves = [(0, 10, 4), (-1, 1, 4), (2, 3, 5), (2, 3, -1), (4, -2, 1), (5, 6, 3)]
+    st = torch.zeros(1, **I32)
+    want = copied([c], [x], moves[5:], 4)
+    sm.kv_copy([c], torch.tensor(moves, **I32), torch.tensor([6], **I32), st, scales=[x])
+    assert int(st) == sm.ST_BAD_INPUT
+    assert torch.equal(c.view(torch.uint8), want[0][0]) and torch.equal(x, want[1][0])

@@ -1,0 +1,357 @@
+"""smcsd_prompt_attention against the definition in 64 bits (bounds in attention_checks): types,
+16- and 8-bit pages, head layouts and sizes, packed lengths from nothing to long, contexts, page
+sizes that end inside a tile, garbage wherever nothing may be read, values that are not finite
+among tokens that some rows see, and the calls a server makes."""
+import math
+
+import pytest
+import torch
+
+import smc_verification_resampling_amd as sm
+from attention_checks import DT, E4M3, check_rows, on_gpu, pages, tokens_at
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+class Case:
+    def __init__(self, dt="bf16", e4m3=False, new=(17, 40, 1, 0), ctx=(0,), S=4, Hq=4, Hkv=2, D=64, bs=16, layout="token", junk=True, seed=0, before=0,
+                 behind=0, qpad=0, scale=None, loud=1.0, no_ctx=False, spare=3):
+        g = torch.Generator().manual_seed(seed)
+        self.dt, self.e4m3, self.S, self.Hq, self.Hkv, self.D, self.bs = dt, e4m3, S, Hq, Hkv, D, bs
+        self.new = [new[i % len(new)] for i in range(S)]
+        self.ctx = [0 if no_ctx else ctx[i % len(ctx)] for i in range(S)]
+        used = [-(-(c + n) // bs) for c, n in zip(self.ctx, self.new)]
+        M = max(used) + 1
+        P = sum(used) + spare
+        ids = iter(torch.randperm(P, generator=g).tolist())
+        tables = torch.full((S, M), -1, dtype=torch.int32)
+        for s in range(S):
+            for j in range(used[s]):
+                tables[s, j] = next(ids)
+        (k, self.sk), (v, self.sv) = (pages(P, bs, Hkv, D, dt, e4m3, layout, g) for _ in range(2))
+        if junk:  # nothing but what a sequence holds
+            live = torch.zeros(P, bs, dtype=torch.bool)
+            for s in range(S):
+                p = torch.arange(self.ctx[s] + self.new[s])
+                live[tables[s].long()[p // bs], p % bs] = True
+            for c in (k, v):
+                if e4m3:
+                    c.view(torch.uint8)[~live] = 0x7F
+                else:
+                    c[~live] = math.nan
+            if e4m3:
+                for c in (self.sk, self.sv):
+                    c[~live.any(1)] = 255
+        self.tables, self.k, self.v = tables.cuda(), on_gpu(k), on_gpu(v)
+        if e4m3:
+            self.sk, self.sv = self.sk.cuda(), self.sv.cuda()
+        cu = [before]
+        for n in self.new:
+            cu.append(cu[-1] + n)
+        self.cu, self.T = cu, cu[-1] + behind
+        self.cu_t = torch.tensor(cu, **I32)
+        self.ctx_t = None if no_ctx else torch.tensor(self.ctx, **I32)
+        self.q = (loud * torch.randn((self.T, Hq + qpad, D), generator=g)).to(DT[dt]).cuda()[:, :Hq]
+        self.scale = D ** -0.5 if scale is None else scale
+        self.out = torch.full((self.T, Hq, D), 77.0, dtype=DT[dt], device="cuda")
+        self.lse = torch.full((self.T, Hq), 77.0, device="cuda")
+        self.status = torch.zeros(1, **I32)
+        self.ws = sm.alloc_workspace(sm.OP_PROMPT_ATTN, S, self.T, K=D, V=Hq * D, P=Hkv)
+        self.ws.fill_(0xFF)  # no initial contents needed
+        self.longest = max(c + n for c, n in zip(self.ctx, self.new))
+
+    def call(self, **kw):
+        a = dict(k_scales=self.sk, v_scales=self.sv, lse=self.lse, max_len=self.longest)
+        a.update(kw)
+        ws = a.pop("workspace", self.ws)
+        sm.prompt_attention(self.q, self.k, self.v, self.tables, self.ctx_t, self.cu_t, self.scale, self.out, self.status, ws, **a)
+        return self
+
+    def check(self, only=None, status=0, sample=None):
+        assert int(self.status) == status
+        for a, b in ((0, self.cu[0]), (self.cu[-1], self.T)):
+            assert (self.out[a:b] == 77).all() and (self.lse[a:b] == 77).all()
+        for s in range(self.S) if only is None else only:
+            n, ctx = self.new[s], self.ctx[s]
+            if n == 0:
+                continue
+            pos = torch.arange(ctx + n, device="cuda")
+            at = self.tables[s].long()[pos // self.bs]
+            k, v = (tokens_at(c, x, at, pos % self.bs, DT[self.dt]) for c, x in ((self.k, self.sk), (self.v, self.sv)))
+            rows = torch.arange(n, device="cuda")
+            if sample:
+                rows = rows[:: max(1, n // sample)].clone()
+                rows[-1] = n - 1
+            for r in rows.split(1024):
+                t = self.cu[s] + r
+                check_rows(self.q[t], k, v, pos[None] <= ctx + r[:, None], self.scale, self.out[t], self.lse[t], self.dt, s)
+        return self
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 112, 128, 144, 192, 208, 256])
+def test_head_sizes(dt, e4m3, D):
+    Case(dt, e4m3, D=D, new=(70, 3, 129), ctx=(0, 37), layout="head").call().check()
+
+
+@pytest.mark.parametrize("D", [8, 24, 72, 136, 200])
+def test_head_sizes_of_16_bit_pages_alone(D):
+    Case(D=D, new=(70, 3, 129), ctx=(0, 37)).call().check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (3, 1), (7, 1), (16, 2), (8, 8), (32, 2), (33, 3)])
+def test_head_groups(e4m3, Hq, Hkv):
+    Case(e4m3=e4m3, Hq=Hq, Hkv=Hkv, new=(45, 130, 300, 1), ctx=(0, 9)).call().check()
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+@pytest.mark.parametrize("ctx", [0, 1, 63, 64, 200])
+def test_lengths(n, ctx):
+    Case(new=(n,), ctx=(ctx,), S=2, Hq=3, Hkv=1).call().check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("bs", [1, 2, 3, 16, 24, 100, 256])
+@pytest.mark.parametrize("layout", ["token", "head"])
+def test_page_sizes(e4m3, bs, layout):
+    Case(e4m3=e4m3, bs=bs, layout=layout, new=(250, 97, 3), ctx=(5, 0, 130, 64)).call().check()
+
+
+@pytest.mark.parametrize("S", [1, 63, 64, 65, 130, 4097])
+def test_numbers_of_sequences(S):
+    c = Case(S=S, new=(1, 0, 3, 0, 0, 70, 2) if S < 1000 else (1, 0, 2), ctx=(0, 5), bs=4, Hq=2, Hkv=1, D=16)
+    c.call().check(only=range(0, S, max(1, S // 100)))
+
+
+@pytest.mark.parametrize("new", [(0,), (0, 0, 5), (5, 0, 0, 0), (0, 300, 0)])
+def test_empty_sequences_and_tokens_of_none(new):
+    Case(new=new, S=6, before=3, behind=5, qpad=3).call().check()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_a_chunk_behind_a_long_context_is_split_and_joined(dt, e4m3, D):
+    c = Case(dt, e4m3, S=2, new=(33, 5), ctx=(9000, 4100), Hq=8, Hkv=2, D=D)
+    c.call().check()
+    first = c.out.clone(), c.lse.clone()
+    for hint in (0, 1, 2000, 10 ** 9):  # a hint, and no bound: whatever it says, every token is seen
+        c.out.fill_(77)
+        c.call(max_len=hint).check()
+    c.call()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])  # and runs repeat bit for bit
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_prompts(e4m3):
+    Case(e4m3=e4m3, S=3, new=(5000, 1777, 2500), ctx=(0, 3333), Hq=4, Hkv=1, D=128).call().check(sample=200)
+
+
+def test_tokens_by_one_or_in_chunks_agree_with_the_whole():
+    """A prompt's rows do not depend on how it is cut, but for the order of sums: each cut is
+    held to the definition."""
+    whole = Case(S=1, new=(150,), Hq=4, Hkv=2, D=128).call().check()
+    for size in (1, 64, 100):
+        for i in range(0, 150, size):
+            n = min(size, 150 - i)
+            c = Case(S=1, new=(150,), Hq=4, Hkv=2, D=128)
+            c.q, c.cu_t = c.q[i:i + n], torch.tensor([0, n], **I32)
+            c.ctx_t.fill_(i)
+            c.out, c.lse = c.out[:n], c.lse[:n]
+            c.call()
+            pos = torch.arange(i + n, device="cuda")
+            at = c.tables[0].long()[pos // 16]
+            k, v = (tokens_at(x, None, at, pos % 16, None) for x in (c.k, c.v))
+            check_rows(c.q, k, v, pos[None] <= i + torch.arange(n, device="cuda")[:, None], c.scale, c.out, c.lse, c.dt, i)
+            if size > 1:
+                break
+
+
+def test_empty_caches():
+    Case(no_ctx=True, new=(33, 64, 1)).call().check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,D", [(1, 64), (4, 128), (2, 256)])
+def test_a_value_that_is_not_finite_is_seen_by_its_rows_alone(e4m3, dt, Hq, D):
+    """NaN and infinite values (NaN alone in 8 bits) at tokens 0, 5, 31, 32, 99 and 250 of 300 behind 20:
+    rows before a token are as without it, rows from there on are not finite at that element."""
+    for poison in (math.nan,) if e4m3 else (math.nan, math.inf, -math.inf):
+        a, b = (Case(dt, e4m3, S=1, new=(300,), ctx=(20,), Hq=Hq, Hkv=1, D=D) for _ in range(2))
+        a.call().check()
+        spots = [(0, 3), (5, 4), (31, 5), (32, 0), (99, D - 1), (250, 9)]
+        for j, d in spots:
+            p = 20 + j
+            b.v[int(b.tables[0, p // 16]), p % 16, 0, d] = poison
+        b.call()
+        assert int(b.status) == 0
+        for j, d in spots:
+            assert torch.equal(a.out[:j, :, d], b.out[:j, :, d])
+            hit = b.out[j:, :, d].float()
+            assert (hit.isnan() if math.isnan(poison) else hit == poison).all(), (j, d)
+        rest = [d for d in range(D) if d not in [x for _, x in spots]]
+        assert torch.equal(a.out[:, :, rest], b.out[:, :, rest]) and torch.equal(a.lse, b.lse)
+
+
+@pytest.mark.parametrize("poison", [math.nan, math.inf, -math.inf])
+def test_a_key_that_is_not_finite_cannot_reach_earlier_rows(poison):
+    a, b = (Case(S=1, new=(200,), ctx=(7,), Hq=4, Hkv=2) for _ in range(2))
+    a.call()
+    p = 7 + 77
+    b.k[int(b.tables[0, p // 16]), p % 16] = poison
+    b.v[int(b.tables[0, p // 16]), p % 16] = poison
+    b.call()
+    assert torch.equal(a.out[:77], b.out[:77]) and torch.equal(a.lse[:77], b.lse[:77])
+    assert not b.out[77:].isfinite().all(-1).any()
+
+
+def test_scales_at_the_ends_of_their_range():
+    """Codes 0 and 1 (values far below any other), 135 and more (past f16's largest number, held there),
+    and a block that is no number, seen from its first token on."""
+    for dt in ("bf16", "f16"):
+        c = Case(dt, True, S=1, new=(100,), Hq=2, Hkv=1, scale=1e-4)
+        b = c.tables[0].long()
+        c.sv[b[1]], c.sv[b[2]], c.sv[b[3]] = 0, 1, 140
+        c.sk[b[4]] = 0
+        c.call().check()
+        d = Case(dt, True, S=1, new=(100,), Hq=2, Hkv=1, scale=1e-4)
+        d.sv[b[1]], d.sv[b[2]], d.sv[b[3]] = 0, 1, 140
+        d.sk[b[4]] = 0
+        d.sv[b[5]] = 255
+        d.call()
+        assert torch.equal(d.out[:80], c.out[:80]) and d.out[80:].isnan().all()
+
+
+def test_loud_scores_and_other_scales():
+    Case(S=2, new=(333, 150), Hq=8, Hkv=2, D=128, loud=40.0).call().check()
+    Case("f16", S=2, new=(333, 150), ctx=(100,), Hq=8, Hkv=2, D=128, loud=40.0).call().check()
+    for scale in (0.0, -0.3):
+        Case(new=(100, 30), scale=scale).call().check()
+
+
+def test_bad_indexes_are_flagged_and_never_followed():
+    good = Case(new=(100,), ctx=(60,)).call().check()
+    P = good.k.shape[0]
+    for bad in (P, P + 5, -1, -2, 2 ** 31 - 1, -2 ** 31):
+        c = Case(new=(100,), ctx=(60,))
+        c.tables[1, 7] = bad
+        c.call()
+        assert int(c.status) == sm.ST_BAD_INPUT
+        for s in (0, 2, 3):
+            assert torch.equal(c.out[100 * s: 100 * s + 100], good.out[100 * s: 100 * s + 100])
+        pos = torch.tensor([p for p in range(160) if p // 16 != 7], device="cuda")  # the rest of the sequence is seen
+        at = c.tables[1].long()[pos // 16]
+        k, v = (tokens_at(x, None, at, pos % 16, None) for x in (c.k, c.v))
+        rows = torch.arange(100, device="cuda")
+        check_rows(c.q[100:200], k, v, pos[None] <= 60 + rows[:, None], c.scale, c.out[100:200], c.lse[100:200], c.dt)
+    for n in (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31):
+        c = Case(new=(100,), ctx=(60,))
+        c.ctx_t[2] = n
+        c.call()
+        assert int(c.status) == sm.ST_BAD_INPUT
+        assert (c.out[200:300] == 0).all() and (c.lse[200:300] == -math.inf).all()
+        for s in (0, 1, 3):
+            assert torch.equal(c.out[100 * s: 100 * s + 100], good.out[100 * s: 100 * s + 100])
+
+
+@pytest.mark.parametrize("ctx", [0, 5000])
+def test_lengths_out_of_order_are_flagged(ctx):
+    for at, value in ((1, -1), (1, 10 ** 6), (2, 3), (0, -5), (4, 2 ** 31 - 1), (3, -2 ** 31)):
+        c = Case(S=4, new=(17, 40, 1, 9), ctx=(ctx,))
+        c.cu_t[at] = value
+        c.call()
+        assert int(c.status) & sm.ST_BAD_INPUT
+
+
+def test_without_lse_and_on_another_stream():
+    c = Case(new=(77, 300, 5), ctx=(3,))
+    c.call()
+    want = c.out.clone()
+    c.out.fill_(77)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    c.call(stream=st, lse=None)
+    st.synchronize()
+    assert torch.equal(c.out, want)
+    c.check()
+
+
+def test_one_workspace_for_several_calls():
+    a = Case(S=2, new=(20,), ctx=(5000, 800), seed=1)
+    b = Case(S=2, new=(20,), ctx=(100, 7000), seed=2)
+    for _ in range(3):
+        a.call()
+        b.call(workspace=a.ws)
+    a.check()
+    b.check()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_graph_replays(e4m3):
+    c = Case(e4m3=e4m3, S=3, new=(100, 7, 33), ctx=(50, 0, 300))
+    long = Case(e4m3=e4m3, S=1, new=(20,), ctx=(5000,))
+    c.call()
+    long.call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call()
+        long.call()
+    for t in range(4):
+        c.q.copy_(torch.randn_like(c.q))
+        long.q.copy_(torch.randn_like(long.q))
+        if t == 2:  # lengths are device data: a replay follows them
+            c.ctx = [41, 0, 299]
+            c.ctx_t.copy_(torch.tensor(c.ctx, dtype=torch.int32))
+            c.new, c.cu = [60, 7, 33], [0, 60, 67, 100]
+            c.cu_t.copy_(torch.tensor(c.cu, dtype=torch.int32))
+            long.ctx = [777]
+            long.ctx_t.fill_(777)
+        c.out.fill_(77)
+        c.lse.fill_(77)
+        long.out.fill_(77)
+        g.replay()
+        torch.cuda.synchronize()
+        c.check()
+        long.check()
+        torch.randn(1000, device="cuda").sum()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pages_past_32_bits(e4m3):
+    page = 1 << 31  # elements: block 2 begins 2^32 elements in
+    c = Case(e4m3=e4m3, S=2, new=(30, 12), Hq=4, Hkv=2, D=64)
+    buf = torch.empty(2 * page + (1 << 20), dtype=E4M3 if e4m3 else torch.bfloat16, device="cuda")
+    k = buf.as_strided((3, 16, 2, 64), (page, 128, 64, 1))
+    v = buf.as_strided((3, 16, 2, 64), (page, 128, 64, 1), 1 << 16)
+    c.tables = torch.tensor([[2, 0], [1, -1]], **I32)
+    for x in (k, v):
+        x.copy_(torch.randn(3, 16, 2, 64, device="cuda").to(x.dtype))
+    c.k, c.v = k, v
+    if e4m3:
+        c.sk, c.sv = (torch.randint(120, 130, (3, 2), dtype=torch.uint8, device="cuda") for _ in range(2))
+    c.call().check()
+
+
+@pytest.mark.parametrize("ctx", [100, 3000])
+def test_every_key_of_a_context_counts_once(ctx):
+    """Keys of zeros and values that count: out is the mean of the positions seen."""
+    c = Case(S=1, new=(70,), ctx=(ctx,), Hq=2, Hkv=1, D=64)
+    c.k.zero_()
+    c.v.fill_(1.0)
+    c.call()
+    assert (c.out == 1).all()
+    n = (ctx + 1 + torch.arange(70, device="cuda").double()).log()
+    assert ((c.lse.double() - n[:, None]).abs() <= (ctx + 134) * 2.0 ** -24 + 2.0 ** -23 * n[:, None]).all()

@@ -1,0 +1,123 @@
+"""Host checks of the operators that bring prompts into the cache and hold it in 8 bits (CPU only:
+every call here is refused, or answered, before anything is enqueued)."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import smc_verification_resampling_amd as sm
+
+P0 = ctypes.c_void_p(0x1000)  # never dereferenced
+ODD = ctypes.c_void_p(0x1008)  # not 16-byte aligned
+BIG = (1 << 31) - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(sm.LIB_PATH):
+        from smc_verification_resampling_amd import build
+        build.build()
+    return sm.load_library()
+
+
+def caller(fn, base):
+    def call(**kw):
+        a = dict(base)
+        a.update(kw)
+        assert len(a) == len(base)
+        return fn(*a.values())
+    return call
+
+
+APPEND = dict(q=P0, k=P0, v=P0, dt=1, qs=512, ks=128, vs=128, S=2, T=6, cu=P0, Hq=8, Hkv=2, D=64, qw=P0, kw=P0, eps=1e-6, cs=P0, maxpos=100, rot=64,
+              il=0, pos=None, ctx=P0, tab=P0, M=8, bs=16, P=64, cdt=3, kc=P0, vc=P0, page=2048, tok=128, head=64, sk=P0, sv=P0, qo=P0, st=P0, s=None)
+
+
+def test_kv_append(lib):
+    f = caller(lib.smcsd_kv_append, APPEND)
+    for kw in (dict(dt=0), dict(dt=3), dict(cdt=0), dict(cdt=2), dict(dt=2, cdt=1), dict(cdt=4)):
+        assert f(**kw) == -2, kw
+    for kw in (dict(S=-1), dict(T=-1), dict(Hq=0), dict(Hkv=0), dict(D=0), dict(D=12), dict(D=264), dict(D=72), dict(rot=72), dict(rot=24), dict(rot=-16),
+               dict(maxpos=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(qs=504), dict(qs=516), dict(ks=64), dict(vs=64),
+               dict(ks=132), dict(vs=132), dict(M=0), dict(bs=0), dict(P=0), dict(P=1 << 31), dict(page=32), dict(tok=32), dict(head=32), dict(page=2056),
+               dict(tok=136), dict(head=72), dict(M=1 << 20, bs=1 << 12), dict(S=BIG), dict(T=BIG), dict(T=1 << 28), dict(S=1 << 28, M=8), dict(qw=ODD),
+               dict(kw=ODD), dict(cs=ODD), dict(cs=None), dict(q=None), dict(qo=None), dict(sk=None), dict(sv=None)):
+        assert f(**kw) == -1, kw
+    for n in ("q", "k", "v", "qo", "kc", "vc"):
+        assert f(**{n: ODD}) == -1, n
+    for n in ("k", "v", "kc", "vc", "cu", "tab", "st"):
+        assert f(**{n: None}) == -1, n
+    assert f(S=0) == 0 and f(T=0) == 0 and f(S=0, cu=None, tab=None) == 0
+    g = caller(lib.smcsd_kv_append, dict(APPEND, cdt=1, T=0))
+    assert g(D=72, qs=576, ks=144, vs=144, page=2056) == 0  # (16-bit pages take what 8-bit ones do not; no tokens)
+
+
+PROMPT = dict(q=P0, dt=1, qs=512, cdt=3, kc=P0, vc=P0, page=2048, tok=128, head=64, sk=P0, sv=P0, tab=P0, M=8, bs=16, P=64, ctx=P0, cu=P0, S=2, T=6, Hq=8,
+              Hkv=2, D=64, scale=0.125, ml=0, out=P0, lse=None, st=P0, ws=P0, wsb=1 << 40, s=None)
+
+
+def test_prompt_attention(lib):
+    f = caller(lib.smcsd_prompt_attention, PROMPT)
+    for kw in (dict(dt=0), dict(dt=3), dict(cdt=0), dict(cdt=2), dict(dt=2, cdt=1)):
+        assert f(**kw) == -2, kw
+    for kw in (dict(S=-1), dict(T=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=7), dict(D=0), dict(D=12), dict(D=264), dict(D=72), dict(scale=float("nan")),
+               dict(scale=float("inf")), dict(scale=3e38), dict(ml=-1), dict(qs=504), dict(qs=516), dict(M=0), dict(bs=0), dict(P=0), dict(P=1 << 31),
+               dict(page=32), dict(tok=32), dict(head=32), dict(page=2056), dict(tok=136), dict(head=72), dict(M=1 << 20, bs=1 << 12), dict(T=1 << 27),
+               dict(S=1 << 21), dict(S=1 << 20, M=1 << 11), dict(sk=None), dict(sv=None)):
+        assert f(**kw) == -1, kw
+    for n in ("q", "out", "kc", "vc"):
+        assert f(**{n: None}) == -1 and f(**{n: ODD}) == -1, n
+    for n in ("cu", "tab", "st"):
+        assert f(**{n: None}) == -1, n
+    assert f(ws=None) == -4 and f(ws=ctypes.c_void_p(0x1010)) == -4
+    assert f(wsb=sm.workspace_bytes(sm.OP_PROMPT_ATTN, 2, 6, 64, 512, 2) - 1) == -4
+    assert f(S=0) == 0 and f(T=0) == 0
+
+
+def test_prompt_attention_workspace(lib):
+    w = sm.workspace_bytes
+    assert w(sm.OP_PROMPT_ATTN, 1, 1, 64, 512, 2) > 0 and w(sm.OP_PROMPT_ATTN, 0, 0, 64, 512, 2) > 0
+    for bad in ((-1, 1, 64, 512, 2), (1, -1, 64, 512, 2), (1, 1, 0, 512, 2), (1, 1, 12, 48, 2), (1, 1, 264, 528, 2), (1, 1, 64, 500, 2), (1, 1, 64, 512, 3),
+                (1, 1, 64, 512, 0), (1, 1 << 27, 64, 512, 2), (1 << 21, 1, 64, 512, 2)):
+        assert w(sm.OP_PROMPT_ATTN, *bad) == 0, bad
+    # parts are for few rows: no more than some hundred MB, whatever the batch, and enough for any smaller call
+    sizes = [w(sm.OP_PROMPT_ATTN, S, T, 128, 4096, 8) for S, T in ((1, 0), (1, 1), (8, 63), (1, 64), (4, 2000), (32, 40000), (1, 131072))]
+    assert sizes == sorted(sizes) and 0 < sizes[0] and sizes[-1] < 3e8
+
+
+def test_tree_attention_e4m3(lib):
+    base = dict(q=P0, dt=1, qs=512, kc=P0, vc=P0, page=2048, tok=128, head=64, sk=P0, sv=P0, tab=P0, M=8, bs=16, P=64, ctx=P0, nn=None, mask=None, B=2, N=2,
+                R=3, Hq=8, Hkv=2, D=64, scale=0.125, ml=0, out=P0, lse=None, st=P0, ws=P0, wsb=1 << 30, s=None)
+    f = caller(lib.smcsd_tree_attention_e4m3, base)
+    assert f(dt=0) == -2 and f(dt=3) == -2
+    for kw in (dict(R=0), dict(R=65), dict(Hq=7), dict(D=72, qs=576), dict(D=264), dict(scale=float("nan")), dict(page=2056), dict(tok=136), dict(head=72),
+               dict(sk=None), dict(sv=None), dict(q=ODD), dict(kc=ODD), dict(out=None), dict(ctx=None), dict(P=0)):
+        assert f(**kw) == -1, kw
+    assert f(ws=None) == -4 and f(wsb=sm.workspace_bytes(sm.OP_TREE_ATTN, 2, 2, 3, 512, 2) - 1) == -4
+    assert f(B=0) == 0 and f(N=0) == 0
+
+
+def test_kv_copy_scaled(lib):
+    two = (ctypes.c_void_p * 2)(0x1000, 0x2000)
+    half = (ctypes.c_void_p * 2)(0x1000, None)
+    f = caller(lib.smcsd_kv_copy_scaled, dict(c=two, x=two, n=2, Hkv=8, page=4096, seg=8, segs=512, tok=32, bs=16, list=P0, count=P0, cap=4, P=64, st=P0, s=None))
+    for kw in (dict(n=-1), dict(n=129), dict(Hkv=0), dict(Hkv=-1), dict(seg=0), dict(tok=0), dict(bs=0), dict(tok=1 << 31), dict(tok=1 << 28), dict(page=-1),
+               dict(segs=-1), dict(P=0), dict(P=1 << 31), dict(cap=-1), dict(cap=1 << 31), dict(c=None), dict(x=None), dict(list=None), dict(count=None),
+               dict(st=None), dict(c=half), dict(x=half), dict(P=BIG, Hkv=BIG)):
+        assert f(**kw) == -1, kw
+    assert f(n=0) == 0 and f(cap=0) == 0
+
+
+def test_binding_refuses(lib):
+    i = torch.zeros(8, dtype=torch.int32)
+    t = torch.zeros(2, 4, dtype=torch.int32)
+    c = torch.zeros(2, 4, 1, 16, dtype=torch.bfloat16)
+    x = torch.zeros(2, 1, 16, dtype=torch.bfloat16)
+    u8 = torch.zeros(1 << 16, dtype=torch.uint8)
+    for call in (lambda: sm.kv_append(x, x, x, i, i, t, c, c, x, i), lambda: sm.prompt_attention(x, c, c, t, i, i, 1.0, x, i, u8),
+                 lambda: sm.kv_copy([c], torch.zeros(2, 3, dtype=torch.int32), i, i, scales=[u8]), lambda: sm.kv_copy([c], t, i, i, scales=[]),
+                 lambda: sm.kv_copy([c] * 129, t, i, i, scales=[u8] * 129),
+                 lambda: sm.tree_attention(c, c, c, t, i, 1, 2, 1.0, c, i, u8, k_scales=u8, v_scales=u8)):
+        with pytest.raises(sm.SmcsdError):
+            call()
