@@ -28,10 +28,14 @@ COMPILE_FLAGS = [
     "-Wall", "-Wno-unused-function",
 ]
 
+# What one source wants beside that.  promptattn.hip: scores in ordinary registers, where the softmax needs
+# them; the compiler's default form leaves every product in accumulation registers, a move for each score.
+SOURCE_FLAGS = {"promptattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC] + COMPILE_FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC] + COMPILE_FLAGS + SOURCE_FLAGS.get(src, []) + ["-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("hipcc failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))

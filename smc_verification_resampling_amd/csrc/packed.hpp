@@ -27,6 +27,31 @@ __device__ __forceinline__ int find_sequence(int S, int64_t x, F first) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// The same with what stands there: a lane that looks at a sequence loads its bounds and context (ctx
+// null: 0) along, and the wave takes those of the one it finds.
+struct Sequence {
+  int s, begin, end, ctx;
+};
+template <class F>
+__device__ __forceinline__ Sequence sequence_of(const int32_t *cu, const int32_t *ctx, int S, int64_t x, F first) {
+  const int lane = threadIdx.x % kWave;
+  int lo = 0, n = S;
+  for (;;) {
+    const int step = (n + kWave - 1) / kWave;
+    const int at = lo + min(lane * step, n - 1);
+    const int32_t begin = cu[at], end = cu[at + 1], have = ctx ? ctx[at] : 0;
+    const bool below = lane * step < n && first(at, begin) <= x;
+    const int count = max(1, (int)__popcll(__ballot(below)));
+    if (step == 1) {
+      const int w = count - 1;
+      return Sequence{__builtin_amdgcn_readfirstlane(lo + w), __builtin_amdgcn_readlane(begin, w), __builtin_amdgcn_readlane(end, w),
+                      __builtin_amdgcn_readlane(have, w)};
+    }
+    lo += (count - 1) * step;
+    n = min(step, n - (count - 1) * step);
+  }
+}
+
 // Whether the workgroup's share of the S pairs is in order; pairs are shared out over the grid.
 __device__ __forceinline__ bool lengths_in_order(const int32_t *cu, int S, int T) {
   bool good = true;

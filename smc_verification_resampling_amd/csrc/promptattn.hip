@@ -43,7 +43,6 @@ template <> struct Mma<SMCSD_DTYPE_F16> {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRowsWave = 32;
-constexpr int KT = 64;       // keys of a tile in LDS
 constexpr float kLag = 8.0f; // a running maximum may fall behind by a factor of 2^8
 constexpr int kItems = 1024; // workgroups that the splits of a launch aim at
 
@@ -77,8 +76,8 @@ struct Plan {
 
 // Row tiles of all sequences are numbered with room to spare: sequence s's begin at
 // floor(cu[s] * G / M) + s.
-__device__ __forceinline__ int64_t first_tile(const PromptAttnArgs &a, int s, int M) {
-  return (int64_t)held_cu(a.cu, s, a.T) * (a.Hq / a.Hkv) / M + s;
+__device__ __forceinline__ int64_t first_tile(const PromptAttnArgs &a, int s, int32_t cu, int M) {
+  return (int64_t)max(0, min(cu, a.T)) * (a.Hq / a.Hkv) / M + s;
 }
 
 __device__ __forceinline__ float2 both_halves(float x) {
@@ -94,12 +93,6 @@ __device__ __forceinline__ float max_halves(float x) {
   return fmaxf(h.x, h.y);
 }
 
-// A row's 16-byte chunks are stored permuted, as in the tree attention's tiles.
-template <int CH>
-__device__ __forceinline__ int place_of(int r) {
-  return CH < 16 ? ((r & 2) << 1) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
-}
-
 __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothing to load
 
 template <class T>
@@ -112,21 +105,24 @@ __device__ __forceinline__ s16x4 lds_read_column(const char *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
 }
 
-// DC: head size padded to a multiple of 32; a row of LDS has DP >= DC elements, a power of two.
+// DC: head size padded to a multiple of 32.
 template <int DT, int DC, int RT, bool E4>
 __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
   typedef typename std::conditional<E4, uint8_t, uint16_t>::type Elem;
-  constexpr int DP = DC <= 64 ? 64 : DC <= 128 ? 128 : 256;
-  constexpr int CH = DP / 8, RB = DP * 2, TB = KT * RB;
+  constexpr int KT = DC > 128 ? 32 : 64;  // keys of a tile in LDS
+  // Rows of LDS are padded: sixteen rows' 16 bytes of keys (a score's read), and four rows' 64 bytes
+  // of values (the transposing read), then lie on different ones of the 64 banks, and every read's place
+  // is one address and a constant.
+  constexpr int KR = 2 * DC + 16, VR = DC == 96 ? 192 : 2 * DC + 64, KB = KT * KR, VB = KT * VR;
   constexpr int NS = DC / 16, NA = DC / 32;
   constexpr int M = kWaves * kRowsWave * RT;
-  constexpr int EC = E4 ? 16 : 8;                 // elements of a 16-byte load
-  constexpr int CL = DP / EC;                     // loads of a row
+  constexpr int EC = E4 ? 16 : 8;                            // elements of a 16-byte load
+  constexpr int CL = (DC <= 64 ? 64 : DC <= 128 ? 128 : 256) / EC;  // threads that load a row
   constexpr int NL = KT * CL / kThreads;          // loads of keys (and as many of values) of a thread
   static_assert(KT * CL % kThreads == 0, "whole loads");
-  __shared__ __attribute__((aligned(16))) char sKV[4 * TB];  // keys' two buffers, then values'
+  __shared__ __attribute__((aligned(16))) char sK[3 * KB], sV[3 * VB];
   __shared__ uint32_t sOdd[M / 32 + 1];  // tokens of the tile whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int hw = lane / 32, col = lane % 32;
@@ -140,14 +136,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   const int split = (int)(it % (uint32_t)p.splits);
   it /= (uint32_t)p.splits;
   const int64_t item = p.tiles - 1 - (int64_t)it;
-  const int s = find_sequence(a.S, item, [&](int i) { return first_tile(a, i, M); });
-  const int64_t tile = item - first_tile(a, s, M);
-  const int t0 = a.cu[s], t1 = a.cu[s + 1];
+  const Sequence seq = sequence_of(a.cu, a.ctx_lens, a.S, item, [&](int i, int32_t cu) { return first_tile(a, i, cu, M); });
+  const int s = seq.s, t0 = seq.begin, t1 = seq.end;
+  const int64_t tile = item - first_tile(a, s, t0, M);
   if (t0 < 0 || t1 <= t0 || t1 > a.T || tile < 0) return;
   const int n = t1 - t0, rows = n * G;
   if (tile * M >= rows) return;
   const int r0 = (int)(tile * M);
-  int ctx = a.ctx_lens ? a.ctx_lens[s] : 0;
+  int ctx = seq.ctx;
   const bool none = ctx < 0 || (int64_t)ctx + n > (int64_t)a.cache.M_cap * a.cache.block_size;
   if (none) {
     if (tid == 0 && hk == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
@@ -187,6 +183,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
       w.z ^= flip;
       w.w ^= flip;
       q[x][st] = __builtin_bit_cast(V8, w);
+      asm volatile("" : "+a"(q[x][st]));  // accumulation registers, from which the matrix instructions take it as well
     }
   }
   const int wr = r0 + wave * RT * kRowsWave;  // the wave's first row
@@ -210,168 +207,401 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   bool bad_page = false;
   struct Tile {
     u32x4 k[NL], v[NL];
-    int ks, vs;     // 8-bit pages: codes of the scales of row `lane`
+    int ks, vs;     // 8-bit pages: codes of the scales of row lane % KT
     uint64_t rows;  // which may be read
-  } next;
-  auto ask_tile = [&](int base) {
-    const int pos = base + lane, block = div_by(p.page, pos);
-    const int32_t pg = pos < k1 ? table[block] : -1;
-    const bool ok = pg >= 0 && pg < a.cache.P;
-    bad_page |= !ok && pos < k1;
-    next.rows = __ballot(ok);
-    const int64_t off = ok ? pg * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token : -1;
-    if (E4) {
-      next.ks = next.vs = 127;
-      if (ok) {
-        next.ks = a.k_scales[(int64_t)pg * a.Hkv + hk];
-        next.vs = a.v_scales[(int64_t)pg * a.Hkv + hk];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int64_t at = __shfl((long long)off, (i * kThreads + tid) / CL, kWave);
-      const int chunk = tid % CL;
-      const bool in = at >= 0 && chunk * EC < a.D;
-      next.k[i] = *(in ? (const u32x4 *)(kbase + at + chunk * EC) : (const u32x4 *)&kNothing);
-      next.v[i] = *(in ? (const u32x4 *)(vbase + at + chunk * EC) : (const u32x4 *)&kNothing);
-    }
   };
+  const int chunk = tid % CL;
+  const bool outside = chunk * EC >= DC, padding = chunk * EC >= a.D;  // this thread's part of a row is none
+  const char *const kat = reinterpret_cast<const char *>(kbase + (padding ? 0 : chunk * EC));
+  const char *const vat = reinterpret_cast<const char *>(vbase + (padding ? 0 : chunk * EC));
+  // The loads of a tile in three parts.  The block of row lane % KT of the tile at `base` (rows from k1
+  // on: the last one's) ...
+  auto look_up = [&](int64_t base, int &block) {
+    block = div_by(p.page, (int)min(base + lane % KT, (int64_t)k1 - 1));
+    return table[block];
+  };
+  // ... the row's place in bytes, that of block 0 (which there is) where it may not be read; which may ...
+  auto place_rows = [&](Tile &t, int64_t base, int block, int32_t pg) {
+    const int64_t pos = base + lane % KT;
+    const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
+    bad_page |= !page_ok && pos < k1;
+    t.rows = __ballot(ok);
+    pg = ok ? pg : 0;
+    if (E4) {
+      t.ks = a.k_scales[(int64_t)pg * a.Hkv + hk];
+      t.vs = a.v_scales[(int64_t)pg * a.Hkv + hk];
+    }
+    return (int64_t)sizeof(Elem) * (pg * a.cache.page + (ok ? (int)pos - block * (int)p.page.d : 0) * a.cache.token);
+  };
+  // ... and the loads.
+  auto row_of = [&](int i) { return (i * kThreads + tid) / CL; };
+  auto load_row = [&](Tile &t, int i, int64_t at) {
+    t.k[i] = *reinterpret_cast<const u32x4 *>(kat + at);
+    t.v[i] = *reinterpret_cast<const u32x4 *>(vat + at);
+  };
+  auto ask_tile = [&](Tile &t, int64_t base) {
+    int block;
+    const int32_t pg = look_up(base, block);
+    const int64_t off = place_rows(t, base, block, pg);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) load_row(t, i, __shfl((long long)off, row_of(i), kWave));
+  };
+  // Elements of a word that are not finite become 0; the mask of the others.
   constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
   auto finite = [&](uint32_t &w) {
+    if constexpr (E4) {
+      uint32_t left = 0;
+#pragma unroll
+      for (int b = 0; b < 32; b += 8) left |= ((w >> b) & 0x7F) == 0x7F ? 0 : 0xFFu << b;
+      w &= left;
+      return left;
+    }
     const uint32_t lo16 = (w & kExp) == kExp ? 0xFFFF0000u : ~0u;
     const uint32_t hi16 = (w & (kExp << 16)) == kExp << 16 ? 0xFFFFu : ~0u;
     w &= lo16 & hi16;
     return lo16 & hi16;
   };
-  // Values of tokens that not all rows see and that are not finite become 0: a probability of 0
-  // then takes nothing from them, and the rows that do see them get them after the last tile.
-  auto mend = [&](uint4 &w, int pos) {
-    const bool odd = (finite(w.x) & finite(w.y) & finite(w.z) & finite(w.w)) != ~0u;
-    if (odd) atomicOr(&sOdd[(pos - own) / 32], 1u << ((pos - own) % 32));
+  // whether a tile goes to LDS as it came
+  auto plain = [&](const Tile &t, int64_t base) { return t.rows == ~0ull && base + KT <= own && a.D >= DC; };
+  // What a tile needs that does not: rows that may not be read and the padding of a head become 0, and
+  // so do values of tokens that not all rows see and that are not finite: a probability of 0 then takes
+  // nothing from them, and the rows that do see them get them after the last tile.
+  auto clean = [&](Tile &t, int64_t base) {
+#pragma unroll 1
+    for (int i = 0; i < NL; ++i) {
+      const int row = row_of(i), pos = (int)base + row;
+      u32x4 k = t.k[0], v = t.v[0];
+#pragma unroll
+      for (int j = 1; j < NL; ++j) {
+        k = i == j ? t.k[j] : k;
+        v = i == j ? t.v[j] : v;
+      }
+      if (padding || !((t.rows >> row) & 1)) k = v = u32x4{0, 0, 0, 0};
+      const bool no_number = E4 && __shfl(t.vs, row, kWave) == 255;
+      if (pos >= own) {
+        bool odd = no_number && !padding;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w = v[c];
+          odd |= finite(w) != ~0u;
+          v[c] = no_number ? 0 : w;
+        }
+        if (odd) atomicOr(&sOdd[(pos - own) / 32], 1u << ((pos - own) % 32));
+      }
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        t.k[j] = i == j ? k : t.k[j];
+        t.v[j] = i == j ? v : t.v[j];
+      }
+    }
+    if (E4 && base + lane % KT >= own && t.vs == 255) t.vs = 127;
   };
-  auto put_tile = [&](int buf, int base) {
-    const bool edge = base + KT > own;
+  constexpr int PC = E4 ? 2 : 1;  // chunks of 16-bit elements that a load becomes
+  auto widened = [&](const Tile &t, int i, uint4 (&k)[PC], uint4 (&v)[PC]) {
+    if constexpr (E4) {
+      const int ks = __shfl(t.ks, row_of(i), kWave), vs = __shfl(t.vs, row_of(i), kWave);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        k[c] = widen8_e4m3<DT>(make_uint2(t.k[i][2 * c], t.k[i][2 * c + 1]), ks);
+        v[c] = widen8_e4m3<DT>(make_uint2(t.v[i][2 * c], t.v[i][2 * c + 1]), vs);
+      }
+    } else {
+      k[0] = __builtin_bit_cast(uint4, t.k[i]);
+      v[0] = __builtin_bit_cast(uint4, t.v[i]);
+    }
+  };
+  char *const put_k = sK + tid / CL * KR + chunk * PC * 16, *const put_v = sV + tid / CL * VR + chunk * PC * 16;
+  auto put_row = [&](int buf, int i, const uint4 (&k)[PC], const uint4 (&v)[PC]) {
+    if (outside) return;
+#pragma unroll
+    for (int c = 0; c < PC; ++c) {
+      *reinterpret_cast<uint4 *>(put_k + buf * KB + i * (kThreads / CL) * KR + 16 * c) = k[c];
+      *reinterpret_cast<uint4 *>(put_v + buf * VB + i * (kThreads / CL) * VR + 16 * c) = v[c];
+    }
+  };
+  auto put_tile = [&](Tile &t, int buf, int64_t base) {
+    if (!plain(t, base)) clean(t, base);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int row = (i * kThreads + tid) / CL, chunk = tid % CL;
-      const int place = place_of<CH>(row);
-      char *const kr = sKV + buf * TB + row * RB, *const vr = kr + 2 * TB;
-      if (E4) {
-        const int ks = __shfl(next.ks, row, kWave), vs = __shfl(next.vs, row, kWave);
-        uint4 k[2] = {widen8_e4m3<DT>(make_uint2(next.k[i][0], next.k[i][1]), ks), widen8_e4m3<DT>(make_uint2(next.k[i][2], next.k[i][3]), ks)};
-        uint4 v[2] = {widen8_e4m3<DT>(make_uint2(next.v[i][0], next.v[i][1]), vs), widen8_e4m3<DT>(make_uint2(next.v[i][2], next.v[i][3]), vs)};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (edge && base + row >= own) {
-            uint4 w = v[c];
-            mend(w, base + row);
-            v[c] = w;
-          }
-          *reinterpret_cast<uint4 *>(kr + ((2 * chunk + c) ^ place) * 16) = k[c];
-          *reinterpret_cast<uint4 *>(vr + ((2 * chunk + c) ^ place) * 16) = v[c];
-        }
-      } else {
-        uint4 v = __builtin_bit_cast(uint4, next.v[i]);
-        if (edge && base + row >= own) mend(v, base + row);
-        *reinterpret_cast<u32x4 *>(kr + (chunk ^ place) * 16) = next.k[i];
-        *reinterpret_cast<uint4 *>(vr + (chunk ^ place) * 16) = v;
-      }
+      uint4 k[PC], v[PC];
+      widened(t, i, k, v);
+      put_row(buf, i, k, v);
     }
   };
 
-  // ---- LDS offsets of a step's operands: keys, chunk 2 st + hw of row col; values, row 16h +
-  // 8x + 4hw + i16/4, chunk 4t + 2dh + (i16%4)/2
-  constexpr int NKA = NS < 8 ? NS : 8;
-  constexpr int NVT = NA < 4 ? NA : 4;
+  // ---- LDS places of a step's operands: keys, chunk 2 st + hw of row col; values, row 16h + 8x +
+  // 4hw + i16/4, 8-byte part 8t + 4dh + i16%4
   const int i16 = lane % 16, dh = (lane / 16) & 1;
-  int ka[NKA], va[NVT][2];
-#pragma unroll
-  for (int st = 0; st < NKA; ++st) ka[st] = col * RB + (((2 * st + hw) ^ place_of<CH>(col)) * 16);
-#pragma unroll
-  for (int t = 0; t < NVT; ++t)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = 8 * x + 4 * hw + i16 / 4;
-      va[t][x] = 2 * TB + row * RB + ((4 * t + 2 * dh + (i16 % 4) / 2) ^ place_of<CH>(row)) * 16 + (i16 & 1) * 8;
-    }
+  const char *const key_at = sK + col * KR + hw * 16;
+  const char *const value_at = sV + (4 * hw + i16 / 4) * VR + dh * 32 + i16 % 4 * 8;
+  auto key_part = [&](const char *at, int st) { return lds_read<V8>(at + 32 * st); };
+  auto value_part = [&](const char *at, int h, int t) {
+    struct { s16x4 v[2]; } two = {{lds_read_column(at + 16 * h * VR + 64 * t), lds_read_column(at + (16 * h + 8) * VR + 64 * t)}};
+    return __builtin_bit_cast(V8, two);
+  };
 
-  // 32 keys from position `base` on, in LDS from row `at` of buffer `buf`; ok: which may be read
-  auto step = [&](int base, int buf, int at, uint32_t ok) {
-    const char *const tile_at = sKV + buf * TB + at * RB;
-    f32x16 z[RT];
+  // ---- the parts of a step of 32 keys, of tile rows 32 u .. in buffer `buf`
+  V8 kf[NS], vf[2][NA];
+  auto keys_of = [&](int buf, int u) { return key_at + buf * KB + 32 * u * KR; };
+  auto values_of = [&](int buf, int u) { return value_at + buf * VB + 32 * u * VR; };
+  auto read_keys = [&](const char *at) {
 #pragma unroll
-    for (int x = 0; x < RT; ++x) z[x] = f32x16{};
-#pragma unroll
-    for (int st = 0; st < NS; ++st) {
-      const V8 kf = lds_read<V8>(tile_at + ka[st % NKA] + (st / NKA) * 256);
-#pragma unroll
-      for (int x = 0; x < RT; ++x) z[x] = Mma<DT>::run(kf, q[x][st], z[x]);
-    }
-    V8 pr[RT][2];
-#pragma unroll
-    for (int x = 0; x < RT; ++x) {
-      if (ok != ~0u || base + 31 > wfirst) {
-        const int lim = limit[x] - base;  // the last key seen
-        const uint32_t see = (lim >= 31 ? ~0u : lim >= 0 ? (2u << lim) - 1 : 0u) & ok;
-        const uint32_t mine = see >> (4 * hw);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[x][i] = (mine >> (8 * (i / 4) + i % 4)) & 1 ? z[x][i] : kNegInf;
-      }
-      float top = z[x][0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, z[x][i]);
-      top = max_halves(top) * p.c;
-      if (__any(top > m[x] + kLag)) {
-        const float mn = fmaxf(m[x], top);
-        const float f = m[x] == kNegInf ? 0.0f : fast_exp2(m[x] - mn);
-        m[x] = mn;
-        l[x] *= f;
-#pragma unroll
-        for (int t = 0; t < NA; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[x][t][i] *= f;
-      }
-      const float ms = m[x] == kNegInf ? 0.0f : m[x];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x8 e;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[x][8 * h + i], p.c, -ms));
-        l[x] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        pr[x][h] = __builtin_convertvector(e, V8);
-      }
-    }
+    for (int st = 0; st < NS; ++st) kf[st] = key_part(at, st);
+  };
+  auto read_values = [&](const char *at) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int t = 0; t < NA; ++t) {
-        struct { s16x4 v[2]; } two = {{lds_read_column(tile_at + va[t % NVT][0] + 16 * h * RB + (t / 4) * 256),
-                                       lds_read_column(tile_at + va[t % NVT][1] + 16 * h * RB + (t / 4) * 256)}};
-        const V8 vf = __builtin_bit_cast(V8, two);
+      for (int t = 0; t < NA; ++t) vf[h][t] = value_part(at, h, t);
+  };
+  auto scores = [&](int x) {
+    f32x16 z = f32x16{};
 #pragma unroll
-        for (int x = 0; x < RT; ++x) o[x][t] = Mma<DT>::run(vf, pr[x][h], o[x][t]);
-      }
+    for (int st = 0; st < NS; ++st) z = Mma<DT>::run(kf[st], q[x][st], z);
+    return z;
+  };
+  auto highest = [&](const f32x16 &z) {
+    float top = z[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
+    return max_halves(top) * p.c;
+  };
+  // The reference of the exponents moves where the maximum has passed it by 2^kLag.
+  auto rescale = [&](int x, float top) {
+    if (__any(top > m[x] + kLag)) {
+      const float mn = fmaxf(m[x], top);
+      const float f = m[x] == kNegInf ? 0.0f : fast_exp2(m[x] - mn);
+      m[x] = mn;
+      l[x] *= f;
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[x][t][i] *= f;
+    }
+  };
+  auto shares = [&](const f32x16 &z, int x, V8 (&pr)[2]) {
+    const float ms = m[x] == kNegInf ? 0.0f : m[x];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x8 e;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = fast_exp2(fmaf(z[8 * h + i], p.c, -ms));
+      l[x] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      pr[h] = __builtin_convertvector(e, V8);
+    }
+  };
+  auto product = [&](const V8 (&pr)[2], int x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < NA; ++t) o[x][t] = Mma<DT>::run(vf[h][t], pr[h], o[x][t]);
+  };
+  // of the 32 keys from `from` on, this lane's 16 that row tile x sees; ok: which may be read
+  auto seen = [&](int x, int64_t from, uint32_t ok) {
+    const int lim = (int)min((int64_t)limit[x] - from, (int64_t)31);
+    return ((lim >= 31 ? ~0u : lim >= 0 ? (2u << lim) - 1 : 0u) & ok) >> (4 * hw);
+  };
+  auto hide = [&](f32x16 &z, uint32_t see) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = (see >> (8 * (i / 4) + i % 4)) & 1 ? z[i] : kNegInf;
   };
 
+  // Tile t lies in buffer t % 3.  While it is computed the next one is in LDS or on its way there, the
+  // one after that in registers.  Every wave runs the same staging and barriers.
   if (k0 < k1) {
-    ask_tile(k0);
-    __syncthreads();  // sOdd is clear
-    put_tile(0, k0);
-    uint64_t ok = next.rows;
-    int buf = 0;
-    if (k0 + KT < k1) ask_tile(k0 + KT);
-    for (int base = k0; base < k1; base += KT) {
-      __syncthreads();
-      const uint64_t now = ok;
-      if (base + KT < k1) {
-        put_tile(buf ^ 1, base + KT);
-        ok = next.rows;
-        if (base + 2 * KT < k1) ask_tile(base + 2 * KT);
-      }
+    uint64_t ok, ok1;
+    Tile next;
+    {
+      Tile first;
+      ask_tile(first, k0);
+      ask_tile(next, k0 + KT);
+      __syncthreads();  // sOdd is clear
+      put_tile(first, 0, k0);
+      ok = first.rows;
+      put_tile(next, 1, k0 + KT);
+      ok1 = next.rows;
+      ask_tile(next, k0 + 2 * KT);
+    }
+    __syncthreads();
+    int buf = 0, base = k0;
+    auto turn_in = [&] {  // the tile behind the next one goes to LDS, another is asked for
+      const int far = buf == 0 ? 2 : buf - 1;
+      put_tile(next, far, (int64_t)base + 2 * KT);
+      const uint64_t rows = next.rows;
+      ask_tile(next, (int64_t)base + 3 * KT);
+      ok = ok1;
+      ok1 = rows;
+      buf = buf == 2 ? 0 : buf + 1;
+      base += KT;
+    };
+    // Waves without rows, and those whose rows see no more keys, only take part in the staging.
+    const bool busy = wlast >= 0;
+    auto in_sight = [&](int64_t tiles) {  // whether all rows see all keys of the present tile and of `tiles` - 1 behind it
+      return base + tiles * KT <= own && ok == ~0ull && (tiles == 1 || ok1 == ~0ull);
+    };
+    if constexpr (RT == 2) {
+      if (busy) {
+        // A step is 32 keys, in two phases: while one row tile's scores become probabilities, the matrix
+        // instructions form the other one's next scores and products.  A phase is a row of NP pieces, each a
+        // matrix instruction and as much of the arithmetic as it takes the time of; the compiler moves
+        // nothing between pieces.  Keys and values are read once for both row tiles.
+        constexpr int NP = NS + 2 * NA;
+        f32x16 z0, z1;
+        V8 p0[2], p1[2];
+        float top0, top1;
+        read_keys(keys_of(buf, 0));
+        z0 = scores(0);
+        hide(z0, seen(0, base, (uint32_t)ok));
+        top0 = highest(z0);
 #pragma unroll
-      for (int u = 0; u < KT / 32; ++u)
-        if (base + 32 * u <= wlast) step(base + 32 * u, buf, 32 * u, (uint32_t)(now >> (32 * u)));
-      buf ^= 1;
+        for (int h = 0; h < 2; ++h) {
+          p1[h] = V8{};
+#pragma unroll
+          for (int t = 0; t < NA; ++t) vf[h][t] = V8{};
+        }
+        auto share_piece = [&](int i, const f32x16 &z, float ms, float (&e)[16], float &sum, V8 (&pr)[2]) {
+#pragma unroll
+          for (int j = 16 * i / NP; j < 16 * (i + 1) / NP; ++j) {
+            e[j] = fast_exp2(fmaf(z[j], p.c, -ms));
+            sum += e[j];
+            if (j % 2 == 1) {
+              typedef typename Half<DT>::T T2 __attribute__((ext_vector_type(2)));
+              const T2 two = __builtin_convertvector((f32x2{e[j - 1], e[j]}), T2);
+              pr[j / 8][j % 8 - 1] = two[0];
+              pr[j / 8][j % 8] = two[1];
+            }
+          }
+        };
+        // the maximum of the scores that a phase forms, in the pieces behind the last of them
+        auto top_piece = [&](int i, const f32x16 &z, float &top) {
+          constexpr int N = 2 * NA - 1;
+          const int n = i - (NP - N);
+          if (n >= 0)
+#pragma unroll
+            for (int j = 16 * n / N; j < 16 * (n + 1) / N; ++j) top = fmaxf(top, z[j]);
+        };
+        // ... of which an edge tile hides some
+        auto hide_some = [&](int x, f32x16 &z, float &top, int from, uint32_t which) {
+          hide(z, seen(x, (int64_t)base + from, which));
+          top = highest(z);
+        };
+        // u: the step of the tile; keys: of the step behind; values: of this one
+        auto phases = [&](int u, bool edge, const char *keys, const char *values, auto first, auto second) {
+          rescale(0, top0);
+          {
+            const float ms = m[0] == kNegInf ? 0.0f : m[0];
+            float e[16], sum = 0.0f, top = kNegInf;
+            z1 = f32x16{};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (i < NS) {
+                z1 = Mma<DT>::run(kf[i], q[RT - 1][i], z1);
+                kf[i] = key_part(keys, i);
+              } else {
+                const int h = (i - NS) / NA, t = (i - NS) % NA;
+                o[RT - 1][t] = Mma<DT>::run(vf[h][t], p1[h], o[RT - 1][t]);
+                vf[h][t] = value_part(values, h, t);
+              }
+              share_piece(i, z0, ms, e, sum, p0);
+              top_piece(i, z1, top);
+              first(i);
+              asm volatile("" : "+v"(sum), "+v"(top));  // they belong to this piece
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            l[0] += sum;
+            top1 = max_halves(top) * p.c;
+            asm volatile("" : "+v"(p0[0]), "+v"(p0[1]));  // here, not behind the branch
+          }
+          if (edge) hide_some(RT - 1, z1, top1, 32 * u, (uint32_t)(ok >> (32 * u)));
+          rescale(RT - 1, top1);
+          {
+            const float ms = m[RT - 1] == kNegInf ? 0.0f : m[RT - 1];
+            float e[16], sum = 0.0f, top = kNegInf;
+            z0 = f32x16{};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (i < NS) {
+                z0 = Mma<DT>::run(kf[i], q[0][i], z0);
+              } else {
+                const int h = (i - NS) / NA, t = (i - NS) % NA;
+                o[0][t] = Mma<DT>::run(vf[h][t], p0[h], o[0][t]);
+              }
+              share_piece(i, z1, ms, e, sum, p1);
+              top_piece(i, z0, top);
+              second(i);
+              asm volatile("" : "+v"(sum), "+v"(top));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            l[RT - 1] += sum;
+            top0 = max_halves(top) * p.c;
+            asm volatile("" : "+v"(p1[0]), "+v"(p1[1]));
+          }
+          if (edge) hide_some(0, z0, top0, 32 * u + 32, (uint32_t)(u ? ok1 : ok >> 32));
+        };
+        while (base < k1 && base <= wlast) {
+          const bool edge = !in_sight(2);
+          const int there = buf == 2 ? 0 : buf + 1, far = buf == 0 ? 2 : buf - 1;
+          const int64_t asked = (int64_t)base + 3 * KT;
+          const uint64_t rows = next.rows;
+          int block;
+          int32_t pg;
+          int64_t at[NL];
+          phases(0, edge, keys_of(buf, 1), values_of(buf, 0), [](int) {}, [](int) {});
+          __syncthreads();
+          if (!plain(next, (int64_t)base + 2 * KT)) clean(next, (int64_t)base + 2 * KT);
+          phases(1, edge, keys_of(there, 0), values_of(buf, 1),
+                 [&](int i) {
+                   if (i == 0) pg = look_up(asked, block);
+                 },
+                 [&](int i) {
+                   const int n = i * NL / (NP / 2);
+                   if (i < NP / 2) {
+                     if (i == n * (NP / 2) / NL) {
+                       uint4 k[PC], v[PC];
+                       widened(next, n, k, v);
+                       put_row(far, n, k, v);
+                     }
+                   } else if (i == NP / 2) {
+                     const int64_t off = place_rows(next, asked, block, pg);
+#pragma unroll
+                     for (int r = 0; r < NL; ++r) at[r] = __shfl((long long)off, row_of(r), kWave);
+                   } else if (i == NP - 1) {
+#pragma unroll
+                     for (int r = 0; r < NL; ++r) load_row(next, r, at[r]);
+                   }
+                 });
+          ok = ok1;
+          ok1 = rows;
+          buf = there;
+          base += KT;
+        }
+        product(p1, RT - 1);
+      }
+    }
+    for (; base < k1;) {
+      if constexpr (RT == 1) {
+        auto step = [&](auto edge) {
+#pragma unroll
+          for (int u = 0; u < KT / 32; ++u) {
+            read_keys(keys_of(buf, u));
+            read_values(values_of(buf, u));
+            f32x16 z = scores(0);
+            if constexpr (decltype(edge)::value) {
+              hide(z, seen(0, (int64_t)base + 32 * u, (uint32_t)(ok >> (32 * u))));
+            }
+            rescale(0, highest(z));
+            V8 pr[2];
+            shares(z, 0, pr);
+            product(pr, 0);
+          }
+        };
+        if (busy && in_sight(1)) step(std::false_type{});
+        else if (base <= wlast) step(std::true_type{});
+      }
+      __syncthreads();
+      turn_in();
     }
     __syncthreads();
     // of a value that is not finite any share is not finite either
