@@ -122,7 +122,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   constexpr int CL = (DC <= 64 ? 64 : DC <= 128 ? 128 : 256) / EC;  // threads that load a row
   constexpr int NL = KT * CL / kThreads;          // loads of keys (and as many of values) of a thread
   static_assert(KT * CL % kThreads == 0, "whole loads");
-  __shared__ __attribute__((aligned(16))) char sK[3 * KB], sV[3 * VB];
+  __shared__ __attribute__((aligned(16))) char sKV[3 * KB + 3 * VB];  // keys' three buffers, then values'
+  char *const sK = sKV, *const sV = sKV + 3 * KB;
   __shared__ uint32_t sOdd[M / 32 + 1];  // tokens of the tile whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int hw = lane / 32, col = lane % 32;
@@ -158,48 +159,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
 
   if (tid < M / 32 + 1) sOdd[tid] = 0;
 
-  // ---- this lane's query rows
-  int tok[RT], limit[RT];
-  int64_t orow[RT];
-  bool live[RT];
-  V8 q[RT][NS];
-#pragma unroll
-  for (int x = 0; x < RT; ++x) {
-    const int r = r0 + (wave * RT + x) * kRowsWave + col;
-    live[x] = r < rows;
-    tok[x] = div_by(p.group, min(r, rows - 1));
-    const int g = min(r, rows - 1) - tok[x] * G;
-    limit[x] = live[x] && !none ? ctx + tok[x] : -1;
-    orow[x] = (int64_t)(t0 + tok[x]) * a.Hq + hk * G + g;
-    const uint16_t *qp = a.q + (int64_t)(t0 + tok[x]) * a.q_stride + (int64_t)(hk * G + g) * a.D;
-    const uint32_t flip = p.negate ? 0x80008000u : 0u;
-#pragma unroll
-    for (int st = 0; st < NS; ++st) {
-      const int d = 16 * st + 8 * hw;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (live[x] && d < a.D) w = *reinterpret_cast<const uint4 *>(qp + d);
-      w.x ^= flip;
-      w.y ^= flip;
-      w.z ^= flip;
-      w.w ^= flip;
-      q[x][st] = __builtin_bit_cast(V8, w);
-      asm volatile("" : "+a"(q[x][st]));  // accumulation registers, from which the matrix instructions take it as well
-    }
-  }
-  const int wr = r0 + wave * RT * kRowsWave;  // the wave's first row
-  const int wfirst = ctx + div_by(p.group, min(wr, rows - 1));
-  const int wlast = wr < rows && !none ? ctx + (int)div_by(p.group, min(wr + RT * kRowsWave, rows) - 1) : -1;
-
-  f32x16 o[RT][NA];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int x = 0; x < RT; ++x) {
-#pragma unroll
-    for (int t = 0; t < NA; ++t) o[x][t] = f32x16{};
-    m[x] = kNegInf;
-    l[x] = 0.0f;
-  }
-
   // ---- staging
   const int32_t *table = a.cache.tables + (int64_t)s * a.cache.M_cap;
   const Elem *const kbase = static_cast<const Elem *>(a.k_cache) + (int64_t)hk * a.cache.head;
@@ -220,6 +179,62 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     block = div_by(p.page, (int)min(base + lane % KT, (int64_t)k1 - 1));
     return table[block];
   };
+  // the first three tiles' blocks are on their way while the queries are asked for
+  int first_block[3] = {0, 0, 0};
+  int32_t first_page[3] = {-1, -1, -1};
+  if (k0 < k1)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) first_page[i] = look_up((int64_t)k0 + i * KT, first_block[i]);
+
+  // ---- this lane's query rows
+  int tok[RT], limit[RT];
+  int64_t orow[RT];
+  bool live[RT];
+  uint4 raw[RT][NS];
+#pragma unroll
+  for (int x = 0; x < RT; ++x) {
+    const int r = r0 + (wave * RT + x) * kRowsWave + col;
+    live[x] = r < rows;
+    tok[x] = div_by(p.group, min(r, rows - 1));
+    const int g = min(r, rows - 1) - tok[x] * G;
+    limit[x] = live[x] && !none ? ctx + tok[x] : -1;
+    orow[x] = (int64_t)(t0 + tok[x]) * a.Hq + hk * G + g;
+    const uint16_t *qp = a.q + (int64_t)(t0 + tok[x]) * a.q_stride + (int64_t)(hk * G + g) * a.D;
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      const int d = 16 * st + 8 * hw;
+      raw[x][st] = *reinterpret_cast<const uint4 *>(qp + (d < a.D ? d : 0));
+    }
+  }
+  V8 q[RT][NS];
+  auto take_queries = [&] {
+    const uint32_t flip = p.negate ? 0x80008000u : 0u;
+#pragma unroll
+    for (int x = 0; x < RT; ++x)
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        uint4 w = raw[x][st];
+        if (a.D < DC && 16 * st + 8 * hw >= a.D) w = make_uint4(0, 0, 0, 0);
+        if (p.negate) w = make_uint4(w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip);
+        q[x][st] = __builtin_bit_cast(V8, w);
+        asm volatile("" : "+a"(q[x][st]));  // accumulation registers, from which the matrix instructions take it as well
+      }
+  };
+  const int wr = r0 + wave * RT * kRowsWave;  // the wave's first row
+  const int wfirst = ctx + div_by(p.group, min(wr, rows - 1));
+  const int wlast = wr < rows && !none ? ctx + (int)div_by(p.group, min(wr + RT * kRowsWave, rows) - 1) : -1;
+
+  f32x16 o[RT][NA];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int x = 0; x < RT; ++x) {
+#pragma unroll
+    for (int t = 0; t < NA; ++t) o[x][t] = f32x16{};
+    m[x] = kNegInf;
+    l[x] = 0.0f;
+  }
+
+  // ---- a tile's loads
   // ... the row's place in bytes, that of block 0 (which there is) where it may not be read; which may ...
   auto place_rows = [&](Tile &t, int64_t base, int block, int32_t pg) {
     const int64_t pos = base + lane % KT;
@@ -230,6 +245,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     if (E4) {
       t.ks = a.k_scales[(int64_t)pg * a.Hkv + hk];
       t.vs = a.v_scales[(int64_t)pg * a.Hkv + hk];
+      if (!ok) t.ks = t.vs = 127;
     }
     return (int64_t)sizeof(Elem) * (pg * a.cache.page + (ok ? (int)pos - block * (int)p.page.d : 0) * a.cache.token);
   };
@@ -239,12 +255,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     t.k[i] = *reinterpret_cast<const u32x4 *>(kat + at);
     t.v[i] = *reinterpret_cast<const u32x4 *>(vat + at);
   };
+  auto load_tile = [&](Tile &t, int64_t off) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) load_row(t, i, __shfl((long long)off, row_of(i), kWave));
+  };
   auto ask_tile = [&](Tile &t, int64_t base) {
     int block;
     const int32_t pg = look_up(base, block);
-    const int64_t off = place_rows(t, base, block, pg);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) load_row(t, i, __shfl((long long)off, row_of(i), kWave));
+    load_tile(t, place_rows(t, base, block, pg));
   };
   // Elements of a word that are not finite become 0; the mask of the others.
   constexpr uint32_t kExp = DT == SMCSD_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
@@ -267,32 +285,32 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   // so do values of tokens that not all rows see and that are not finite: a probability of 0 then takes
   // nothing from them, and the rows that do see them get them after the last tile.
   auto clean = [&](Tile &t, int64_t base) {
-#pragma unroll 1
+    if (t.rows != ~0ull || a.D < DC) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (padding || !((t.rows >> row_of(i)) & 1)) t.k[i] = t.v[i] = u32x4{0, 0, 0, 0};
+    }
+    if (base + KT <= own) return;
+    uint32_t any = 0;  // the bits above exponents that are all ones, with one added to them
+    constexpr uint32_t kOnes = E4 ? 0x7F7F7F7Fu : kExp * 0x10001u, kOne = E4 ? 0x01010101u : (0x8000u - kExp) * 0x10001u;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) any |= ((t.v[i][c] & kOnes) + kOne) & ~kOnes & (E4 ? 0x80808080u : 0x80008000u);
+    if (!__any(any != 0 || (E4 && t.vs == 255))) return;
+#pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int row = row_of(i), pos = (int)base + row;
-      u32x4 k = t.k[0], v = t.v[0];
-#pragma unroll
-      for (int j = 1; j < NL; ++j) {
-        k = i == j ? t.k[j] : k;
-        v = i == j ? t.v[j] : v;
-      }
-      if (padding || !((t.rows >> row) & 1)) k = v = u32x4{0, 0, 0, 0};
       const bool no_number = E4 && __shfl(t.vs, row, kWave) == 255;
-      if (pos >= own) {
-        bool odd = no_number && !padding;
+      if (pos < own) continue;
+      bool odd = no_number && !padding && ((t.rows >> row) & 1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w = v[c];
-          odd |= finite(w) != ~0u;
-          v[c] = no_number ? 0 : w;
-        }
-        if (odd) atomicOr(&sOdd[(pos - own) / 32], 1u << ((pos - own) % 32));
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w = t.v[i][c];
+        odd |= finite(w) != ~0u;
+        t.v[i][c] = no_number ? 0 : w;
       }
-#pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        t.k[j] = i == j ? k : t.k[j];
-        t.v[j] = i == j ? v : t.v[j];
-      }
+      if (odd) atomicOr(&sOdd[(pos - own) / 32], 1u << ((pos - own) % 32));
     }
     if (E4 && base + lane % KT >= own && t.vs == 255) t.vs = 127;
   };
@@ -320,7 +338,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     }
   };
   auto put_tile = [&](Tile &t, int buf, int64_t base) {
-    if (!plain(t, base)) clean(t, base);
+    if (base < k1 && !plain(t, base)) clean(t, base);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       uint4 k[PC], v[PC];
@@ -413,14 +431,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     Tile next;
     {
       Tile first;
-      ask_tile(first, k0);
-      ask_tile(next, k0 + KT);
+      load_tile(first, place_rows(first, k0, first_block[0], first_page[0]));
+      load_tile(next, place_rows(next, (int64_t)k0 + KT, first_block[1], first_page[1]));
+      take_queries();
       __syncthreads();  // sOdd is clear
       put_tile(first, 0, k0);
       ok = first.rows;
       put_tile(next, 1, k0 + KT);
       ok1 = next.rows;
-      ask_tile(next, k0 + 2 * KT);
+      load_tile(next, place_rows(next, (int64_t)k0 + 2 * KT, first_block[2], first_page[2]));
     }
     __syncthreads();
     int buf = 0, base = k0;
@@ -550,7 +569,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
           int64_t at[NL];
           phases(0, edge, keys_of(buf, 1), values_of(buf, 0), [](int) {}, [](int) {});
           __syncthreads();
-          if (!plain(next, (int64_t)base + 2 * KT)) clean(next, (int64_t)base + 2 * KT);
+          if ((int64_t)base + 2 * KT < k1 && !plain(next, (int64_t)base + 2 * KT)) clean(next, (int64_t)base + 2 * KT);
           phases(1, edge, keys_of(there, 0), values_of(buf, 1),
                  [&](int i) {
                    if (i == 0) pg = look_up(asked, block);
@@ -605,8 +624,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
     }
     __syncthreads();
     // of a value that is not finite any share is not finite either
-    for (int w = 0; w < M / 32 + 1; ++w)
-      for (uint32_t odd = sOdd[w]; odd; odd &= odd - 1) {
+    for (uint64_t words = __ballot(lane < M / 32 + 1 && sOdd[min(lane, M / 32)] != 0); words; words &= words - 1)
+      for (uint32_t w = __builtin_ctzll(words), odd = sOdd[w]; odd; odd &= odd - 1) {
         const int pos = own + 32 * w + __builtin_ctz(odd), block = div_by(p.page, pos);
         const Elem *vp = vbase + table[block] * a.cache.page + (pos - block * (int)p.page.d) * a.cache.token;
 #pragma unroll
@@ -633,11 +652,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   }
   if (bad_page) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
 
+  static_assert(kWaves * RT * kRowsWave * KR <= 3 * VB + 3 * KB, "a wave's rows of the output in LDS");
+  char *const mine = sKV + wave * RT * kRowsWave * KR;  // (every wave is done with the tiles)
 #pragma unroll
   for (int x = 0; x < RT; ++x) {
     const float sum = sum_halves(l[x]);
-    if (!live[x]) continue;
     if (p.splits > 1) {
+      if (!live[x]) continue;
       const int64_t part = (int64_t)split * a.T * a.Hq + orow[x];
       if (hw == 0) *reinterpret_cast<float2 *>(p.ml + 2 * part) = make_float2(m[x], sum);
       if (sum == 0.0f) continue;
@@ -654,16 +675,37 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
       continue;
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *out = a.out + orow[x] * a.D;
 #pragma unroll
     for (int t = 0; t < NA; ++t)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int d = 32 * t + 8 * b + 4 * hw;
         const f32x4 y = {o[x][t][4 * b] * inv, o[x][t][4 * b + 1] * inv, o[x][t][4 * b + 2] * inv, o[x][t][4 * b + 3] * inv};
-        if (d < a.D) *reinterpret_cast<uint2 *>(out + d) = __builtin_bit_cast(uint2, __builtin_convertvector(y, V4));
+        *reinterpret_cast<uint2 *>(mine + (x * kRowsWave + col) * KR + 2 * (32 * t + 8 * b + 4 * hw)) =
+            __builtin_bit_cast(uint2, __builtin_convertvector(y, V4));
       }
-    if (a.lse && hw == 0) a.lse[orow[x]] = sum == 0.0f ? kNegInf : (float)(((double)m[x] + (double)log2f(sum)) * kLn2);
+    if (a.lse && hw == 0 && live[x]) a.lse[orow[x]] = sum == 0.0f ? kNegInf : (float)(((double)m[x] + (double)log2f(sum)) * kLn2);
+  }
+  if (p.splits > 1) return;
+  // Whole rows from LDS, 16 bytes to a lane: stores straight from the products' layout are 16 bytes of
+  // each of 32 rows.
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the lanes read each other's
+  constexpr int kParts = DC / 8, kOut = RT * kRowsWave * kParts / kWave, kAtOnce = kOut % 4 ? 3 : 4;
+  static_assert(kOut % kAtOnce == 0, "whole rounds");
+  const int64_t first_row = (int64_t)t0 * a.Hq + hk * G;  // row r of the tile: first_row + r + its token * (Hq - G)
+#pragma unroll 1
+  for (int i = 0; i < kOut; i += kAtOnce) {
+    uint4 y[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int n = (i + u) * kWave + lane;
+      y[u] = *reinterpret_cast<const uint4 *>(mine + n / kParts * KR + n % kParts * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int n = (i + u) * kWave + lane, r = wr + n / kParts, part = 8 * (n % kParts);
+      if (r < rows && part < a.D)
+        *reinterpret_cast<uint4 *>(a.out + (first_row + r + (int64_t)div_by(p.group, r) * (a.Hq - G)) * a.D + part) = y[u];
+    }
   }
 }
 
