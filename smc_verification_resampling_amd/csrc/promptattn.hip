@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t div_by(const FastDiv &f, uint32_t n) {
 }
 
 struct Plan {
-  FastDiv page, group;
+  FastDiv page, group, heads, split;  // block size, heads of a key/value head, key/value heads, splits
   int tiles, splits;  // row tiles of all sequences, with room to spare
   float *ml, *acc;    // parts: [splits][T * Hq] (max, sum) pairs, [splits][T * Hq][D]
   float c;            // |scale| * log2(e)
@@ -76,8 +76,8 @@ struct Plan {
 
 // Row tiles of all sequences are numbered with room to spare: sequence s's begin at
 // floor(cu[s] * G / M) + s.
-__device__ __forceinline__ int64_t first_tile(const PromptAttnArgs &a, int s, int32_t cu, int M) {
-  return (int64_t)max(0, min(cu, a.T)) * (a.Hq / a.Hkv) / M + s;
+__device__ __forceinline__ int64_t first_tile(const PromptAttnArgs &a, const Plan &p, int s, int32_t cu, int M) {
+  return (int64_t)((uint32_t)max(0, min(cu, a.T)) * p.group.d / M) + s;  // (T * Hq < 2^30)
 }
 
 __device__ __forceinline__ float2 both_halves(float x) {
@@ -127,19 +127,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   __shared__ uint32_t sOdd[M / 32 + 1];  // tokens of the tile whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int hw = lane / 32, col = lane % 32;
-  const int G = a.Hq / a.Hkv;
+  const int G = p.group.d;
 
   if (!lengths_in_order(a.cu, a.S, a.T)) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
   // item: key/value head fastest, then split, then row tile, the last tiles (of the most keys) first
-  uint32_t it = blockIdx.x;
-  const int hk = (int)(it % (uint32_t)a.Hkv);
-  it /= (uint32_t)a.Hkv;
-  const int split = (int)(it % (uint32_t)p.splits);
-  it /= (uint32_t)p.splits;
+  uint32_t it = div_by(p.heads, blockIdx.x);
+  const int hk = (int)(blockIdx.x - it * p.heads.d);
+  const uint32_t of_split = div_by(p.split, it);
+  const int split = (int)(it - of_split * p.split.d);
+  it = of_split;
   const int64_t item = p.tiles - 1 - (int64_t)it;
-  const Sequence seq = sequence_of(a.cu, a.ctx_lens, a.S, item, [&](int i, int32_t cu) { return first_tile(a, i, cu, M); });
+  const Sequence seq = sequence_of(a.cu, a.ctx_lens, a.S, item, [&](int i, int32_t cu) { return first_tile(a, p, i, cu, M); });
   const int s = seq.s, t0 = seq.begin, t1 = seq.end;
-  const int64_t tile = item - first_tile(a, s, t0, M);
+  const int64_t tile = item - first_tile(a, p, s, t0, M);
   if (t0 < 0 || t1 <= t0 || t1 > a.T || tile < 0) return;
   const int n = t1 - t0, rows = n * G;
   if (tile * M >= rows) return;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
   const int i0 = div_by(p.group, r0), i1 = div_by(p.group, min(r0 + M, rows) - 1);  // first and last token
   const int hi = none ? 0 : ctx + i1 + 1;
   // this split's keys: an equal share in whole tiles
-  const int share = ((hi + p.splits - 1) / p.splits + KT - 1) / KT * KT;
+  const int share = ((int)div_by(p.split, hi + p.splits - 1) + KT - 1) / KT * KT;
   const int k0 = (int)min((int64_t)hi, (int64_t)split * share), k1 = (int)min((int64_t)hi, (int64_t)k0 + share);
   const int own = ctx + i0;  // keys from here on are not seen by all rows
 
@@ -783,9 +783,11 @@ hipError_t launch_prompt_attn(const PromptAttnArgs &a, int dtype, hipStream_t st
   Plan p{};
   p.page = fast_div((uint32_t)a.cache.block_size);
   p.group = fast_div((uint32_t)(a.Hq / a.Hkv));
+  p.heads = fast_div((uint32_t)a.Hkv);
   p.tiles = (int)tiles_of(a.S, a.T, a.Hq / a.Hkv, a.D);
   // a split's keys outweigh the part it leaves
   p.splits = (int)std::min<int64_t>(max_splits(a.S, a.T, a.D, a.Hq, a.Hkv), std::max<int64_t>(1, longest / 1024));
+  p.split = fast_div((uint32_t)p.splits);
   const size_t rows = (size_t)p.splits * (size_t)a.T * (size_t)a.Hq;
   p.ml = reinterpret_cast<float *>(a.ws);
   p.acc = reinterpret_cast<float *>(a.ws + align256(sizeof(float) * 2 * rows));
