@@ -44,7 +44,9 @@ constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRowsWave = 32;
 constexpr float kLag = 8.0f; // a running maximum may fall behind by a factor of 2^8
-constexpr int kItems = 1024; // workgroups that the splits of a launch aim at
+constexpr int kItems = 1024;  // workgroups that the splits of a launch stay below
+constexpr int kUnits = 256;   // compute units; a workgroup has one for itself
+constexpr int kPartKeys = 670;  // what a split costs a workgroup more, its start and its part, in keys
 
 inline int row_tiles(int D) { return D <= 128 ? 2 : 1; }
 inline int tile_rows(int D) { return kWaves * kRowsWave * row_tiles(D); }
@@ -741,7 +743,7 @@ __global__ __launch_bounds__(kJoinBlock) void k_prompt_join(PromptAttnArgs a, Pl
 }
 
 inline int64_t tiles_of(int64_t S, int64_t T, int G, int D) { return T * G / tile_rows(D) + S; }
-// The most splits: a launch's share of kItems.
+// The most splits: a launch's share of kItems (what the workspace holds).
 inline int max_splits(int64_t S, int64_t T, int D, int Hq, int Hkv) {
   return (int)std::max<int64_t>(1, kItems / std::max<int64_t>(1, tiles_of(S, T, Hq / Hkv, D) * Hkv));
 }
@@ -785,8 +787,20 @@ hipError_t launch_prompt_attn(const PromptAttnArgs &a, int dtype, hipStream_t st
   p.group = fast_div((uint32_t)(a.Hq / a.Hkv));
   p.heads = fast_div((uint32_t)a.Hkv);
   p.tiles = (int)tiles_of(a.S, a.T, a.Hq / a.Hkv, a.D);
-  // a split's keys outweigh the part it leaves
-  p.splits = (int)std::min<int64_t>(max_splits(a.S, a.T, a.D, a.Hq, a.Hkv), std::max<int64_t>(1, longest / 1024));
+  // `items` workgroups of L keys, cut in s, take ceil(items s / kUnits) rounds of L / s + kPartKeys keys: the
+  // s that makes that least, at 256 keys or more (each sequence has a tile at least).  4 chunks of 256 to 511
+  // tokens x 32 heads behind 30,000 tokens of 8-bit pages (4 by this rule): 898 us with 2, 765 with 4, 855
+  // with 7 and 852 with 9; 512 tokens x 32 heads behind 8000 (4): 138 us with 5, 111 with 8.
+  const int64_t items = std::max<int64_t>(a.S, ceil_div((int64_t)a.T * (a.Hq / a.Hkv), tile_rows(a.D))) * a.Hkv;
+  const int64_t most = std::min<int64_t>(max_splits(a.S, a.T, a.D, a.Hq, a.Hkv), longest / 256);
+  p.splits = 1;
+  for (int64_t s = 2, least = ceil_div(items, kUnits) * (longest + kPartKeys); s <= most; ++s) {
+    const int64_t keys = ceil_div(items * s, kUnits) * (longest / s + kPartKeys);
+    if (keys < least) {
+      least = keys;
+      p.splits = (int)s;
+    }
+  }
   p.split = fast_div((uint32_t)p.splits);
   const size_t rows = (size_t)p.splits * (size_t)a.T * (size_t)a.Hq;
   p.ml = reinterpret_cast<float *>(a.ws);
