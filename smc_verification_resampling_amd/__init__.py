@@ -599,10 +599,20 @@ def _scale_pair(k_cache, k_scales, v_scales, P: int, Hkv: int, dev: int):
 
 def _packed(t, name: str, T: int, D: int, dtype, dev: int):
     """(address, heads, stride between tokens) of [T, H, D] with each token's heads contiguous."""
-    if isinstance(t, torch.Tensor) and t.dim() == 3:
-        return _heads(t.unsqueeze(1), name, T, 1, D, dtype, dev)
+    try:
+        n, H, d = t.shape
+        tok, h, e = t.stride()
+        if n == T and d == D and t.dtype is dtype and t.get_device() == dev and (h == D or H == 1) and (
+                e == 1 or D == 1):
+            return t.data_ptr(), H, tok if T > 1 else H * D
+    except (AttributeError, ValueError):
+        pass
     _dev(t, name, dtype, contiguous=False)
-    raise SmcsdError("%s must be [T, heads, D]" % name)
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise SmcsdError("%s must be [%d, heads, %d]" % (name, T, D))
+    if t.get_device() != dev:
+        raise SmcsdError("%s is on device %d, the call runs on device %d" % (name, t.get_device(), dev))
+    raise SmcsdError("%s must hold each token's heads contiguously" % name)
 
 
 def _lengths(cu_tokens, ctx_lens, dev: int):

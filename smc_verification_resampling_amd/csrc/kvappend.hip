@@ -10,6 +10,8 @@
 // k_qk_norm_rope: the sum of squares is a butterfly over the group.
 // Blocks of all sequences are numbered with room to spare: sequence s's begin at
 // floor(cu[s] / block_size) + 2 s, since its n tokens touch at most floor(n / block_size) + 2.
+#include <type_traits>
+
 #include "../../include/smcsd.h"
 #include "device.hpp"
 #include "fp8.hpp"
@@ -24,6 +26,24 @@ namespace {
 constexpr int kAppendBlock = 256;
 constexpr int kAppendWaves = kAppendBlock / kWave;
 constexpr int kHold = 4;  // rounds of tokens whose values a wave keeps: 16 tokens of heads of 128
+
+// The sum over the LPH lanes of a head, in every one of them, by moves within the vector registers: lanes
+// 1 and 2 away, then the other four of eight, the other eight of a row of 16, the other row.
+template <int LPH>
+__device__ __forceinline__ float head_sum(float v) {
+  auto moved = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += moved(v, std::integral_constant<int, 0xB1>{});   // quad_perm 1 0 3 2
+  v += moved(v, std::integral_constant<int, 0x4E>{});   // quad_perm 2 3 0 1
+  v += moved(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
+  if (LPH >= 16) v += moved(v, std::integral_constant<int, 0x140>{});  // row_mirror
+  if (LPH >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
 
 // A lane's eight elements of a head: the norm over the head's LPH lanes (no norm where `weight`
 // is null) and the rotation by the angles at `angles` (null: none; read where `known`).
@@ -49,8 +69,7 @@ __device__ __forceinline__ f32x8 norm_rotate(f32x8 x, const uint16_t *weight, co
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor(ss, m, LPH);
+    ss = head_sum<LPH>(ss);
     const float r = rsqrtf(fmaf(ss, inv_D, a.eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
@@ -68,8 +87,14 @@ __device__ __forceinline__ f32x8 norm_rotate(f32x8 x, const uint16_t *weight, co
     const int other = rot ? (lo ? l + half / 8 : l - half / 8) : l;
     const float sign = lo ? -1.0f : 1.0f;
     f32x8 y;
+    if (LPH == 16 && half == 64) {  // the whole of a head of 128: lanes 8 apart, within a row of 16
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], other, LPH);
+      for (int i = 0; i < 8; ++i)
+        y[i] = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x[i]), 0x128, 0xf, 0xf, true));  // row_ror 8
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], other, LPH);
+    }
     if (rot) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], c[i], sign * (y[i] * sn[i]));
@@ -78,153 +103,177 @@ __device__ __forceinline__ f32x8 norm_rotate(f32x8 x, const uint16_t *weight, co
   return x;
 }
 
-// One head's keys or values of the tokens that sequence s puts into one block.
+// The keys and values of the tokens that one sequence puts into one block: a wave takes every
+// kAppendWaves-th head of both, its first tokens on their way while the head before is worked on.
 template <int DT, int LPH, bool E4>
-__device__ __forceinline__ void append_block(const KvAppendArgs &a, int64_t item, int which, int h, float inv_D) {
+__device__ __forceinline__ void append_block(const KvAppendArgs &a, int64_t item, int wave, float inv_D) {
   constexpr int TW = kWave / LPH;  // tokens of a round
   const int lane = threadIdx.x % kWave, l = lane % LPH, sub = lane / LPH;
   const int bs = a.cache.block_size;
-  auto first = [&](int s) { return (int64_t)(held_cu(a.cu, s, a.T) / bs) + 2 * (int64_t)s; };
-  const int s = find_sequence(a.S, item, first);
-  const int64_t j = item - first(s);
-  const int t0 = a.cu[s], t1 = a.cu[s + 1], ctx = a.ctx_lens ? a.ctx_lens[s] : 0;
-  if (t0 < 0 || t1 <= t0 || t1 > a.T || j < 0) return;
-  if (ctx < 0) {
-    if (lane == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
+  auto first = [&](int s, int32_t cu) { return (int64_t)(max(0, min(cu, a.T)) / bs) + 2 * (int64_t)s; };
+  const Sequence q = sequence_of(a.cu, a.ctx_lens, a.S, item, first);
+  const int64_t j = item - first(q.s, q.begin);
+  if (q.begin < 0 || q.end <= q.begin || q.end > a.T || j < 0) return;
+  if (q.ctx < 0) {
+    if (threadIdx.x == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
     return;
   }
-  const int64_t slot = ctx / bs + j;
-  const int64_t p0 = max((int64_t)ctx, slot * bs), p1 = min((int64_t)ctx + (t1 - t0), (slot + 1) * bs);
+  const int64_t slot = q.ctx / bs + j;
+  const int64_t p0 = max((int64_t)q.ctx, slot * bs), p1 = min((int64_t)q.ctx + (q.end - q.begin), (slot + 1) * bs);
   if (p0 >= p1) return;
-  const int32_t page = slot < a.cache.M_cap ? a.cache.tables[(int64_t)s * a.cache.M_cap + slot] : -1;
-  if (page < 0 || page >= a.cache.P) {
-    if (lane == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-    return;
-  }
+  const int32_t page = slot < a.cache.M_cap ? a.cache.tables[(int64_t)q.s * a.cache.M_cap + slot] : -1;
   const int count = (int)(p1 - p0), held = (int)(p0 - slot * bs);  // new tokens; older ones of the block
-  const int first_t = t0 + (int)(p0 - ctx);
-  const uint16_t *src = which ? a.v : a.k;
-  const int64_t stride = which ? a.v_stride : a.k_stride;
-  src += (int64_t)h * a.D + 8 * l;
+  const int first_t = q.begin + (int)(p0 - q.ctx);
   const bool in = 8 * l < a.D;
-  const uint16_t *weight = which ? nullptr : a.k_weight;
-  const bool turn = !which && a.rot_dim > 0;
-  const int64_t place = page * a.cache.page + held * a.cache.token + h * a.cache.head + 8 * l;
-  uint8_t *const dst8 = static_cast<uint8_t *>(which ? a.v_cache : a.k_cache) + place;
-  uint16_t *const dst16 = static_cast<uint16_t *>(which ? a.v_cache : a.k_cache) + place;
+  const int heads = 2 * a.Hkv;
 
-  auto load = [&](int i) {  // token i of the block's new ones, its lanes' part (0 past the last)
+  auto load = [&](int hw, int i) {  // token i of the block's new ones (0 past the last), head hw of keys, then values
     uint4 raw = make_uint4(0, 0, 0, 0);
-    if (in && i < count) raw = *reinterpret_cast<const uint4 *>(src + (first_t + i) * stride);
+    if (in && i < count)
+      raw = *reinterpret_cast<const uint4 *>(hw < a.Hkv ? a.k + (first_t + i) * a.k_stride + hw * a.D + 8 * l
+                                                        : a.v + (first_t + i) * a.v_stride + (hw - a.Hkv) * a.D + 8 * l);
     return raw;
   };
-  bool any = false;
-  // whether token i may be written, and its values
-  auto form = [&](int i, uint4 raw, bool &ok, f32x8 &x) {
-    ok = i < count;
-    const float *angles = nullptr;
-    if (a.rot_dim > 0) {
-      const int64_t pos = !ok ? -1 : a.positions ? a.positions[first_t + i] : p0 + i;
-      const bool good = pos >= 0 && pos < a.max_pos;
-      if (ok && !good && l == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
-      ok &= good;
-      angles = a.cos_sin + (good ? pos * a.rot_dim : 0);
-    }
-    x = widen8<DT>(raw);
-    if (weight || turn) x = norm_rotate<DT, LPH>(x, weight, turn ? angles : nullptr, ok, a, inv_D);
-    any |= ok;
-    ok &= in;
-  };
-  if (!E4) {
-    for (int i0 = 0; i0 < count; i0 += TW * kHold) {
-      uint4 raw[kHold];
+  uint4 next[kHold];
 #pragma unroll
-      for (int u = 0; u < kHold; ++u) raw[u] = load(i0 + u * TW + sub);
-#pragma unroll
-      for (int u = 0; u < kHold; ++u) {
-        const int i = i0 + u * TW + sub;
-        if (i0 + u * TW >= count) break;
-        bool ok;
-        f32x8 x;
-        form(i, raw[u], ok, x);
-        if (weight || turn) raw[u] = narrow8<DT>(x);
-        if (ok) *reinterpret_cast<uint4 *>(dst16 + i * a.cache.token) = raw[u];
-      }
-    }
+  for (int u = 0; u < kHold; ++u) next[u] = wave < heads ? load(wave, u * TW + sub) : make_uint4(0, 0, 0, 0);
+  // of a token: whether its position is in the table (looked at once for all heads), and its angles
+  auto place = [&](int i) { return i >= count ? (int64_t)-1 : a.positions ? (int64_t)a.positions[first_t + i] : p0 + i; };
+  auto known = [&](int64_t pos) { return a.rot_dim == 0 || (pos >= 0 && pos < a.max_pos); };
+  if (page < 0 || page >= a.cache.P) {
+    if (threadIdx.x == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
     return;
   }
-  float top = 0.0f;
-  f32x8 x[kHold];
-  bool ok[kHold];
-  auto most = [&](const f32x8 &y, bool good) {
+  // the scales of all heads (of the first 64) in one load, lane by lane
+  int codes = 0;
+  if (E4 && held > 0 && lane < heads)
+    codes = lane < a.Hkv ? a.k_scales[(int64_t)page * a.Hkv + lane] : a.v_scales[(int64_t)page * a.Hkv + lane - a.Hkv];
+  int64_t pos[kHold];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, good && fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.0f);
-  };
-  {
+  for (int u = 0; u < kHold; ++u) pos[u] = place(u * TW + sub);
+  for (int hw = wave; hw < heads; hw += kAppendWaves) {
+    const bool key = hw < a.Hkv;
+    const int h = key ? hw : hw - a.Hkv;
+    const uint16_t *weight = key ? a.k_weight : nullptr;
+    const bool turn = key && a.rot_dim > 0;
+    const int64_t at = page * a.cache.page + held * a.cache.token + h * a.cache.head + 8 * l;
+    uint8_t *const dst8 = static_cast<uint8_t *>(key ? a.k_cache : a.v_cache) + at;
+    uint16_t *const dst16 = static_cast<uint16_t *>(key ? a.k_cache : a.v_cache) + at;
+    uint8_t *const code = E4 ? (key ? a.k_scales : a.v_scales) + (int64_t)page * a.Hkv + h : nullptr;
+    const int was = !E4 || held == 0 ? 0 : hw < kWave ? __builtin_amdgcn_readlane(codes, hw) : *code;
     uint4 raw[kHold];
 #pragma unroll
-    for (int u = 0; u < kHold; ++u) raw[u] = load(u * TW + sub);
+    for (int u = 0; u < kHold; ++u) raw[u] = next[u];
+    if (hw + kAppendWaves < heads)
+#pragma unroll
+      for (int u = 0; u < kHold; ++u) next[u] = load(hw + kAppendWaves, u * TW + sub);
+    // whether token i may be written, and its values
+    auto form = [&](int i, int64_t where, uint4 w, bool &ok, f32x8 &x) {
+      ok = i < count && known(where);
+      x = widen8<DT>(w);
+      if (weight || turn) x = norm_rotate<DT, LPH>(x, weight, turn ? a.cos_sin + (ok ? where * a.rot_dim : 0) : nullptr, ok, a, inv_D);
+    };
+    if (!E4) {
+#pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        if (u * TW >= count) break;
+        bool ok;
+        f32x8 x;
+        form(u * TW + sub, pos[u], raw[u], ok, x);
+        if (weight || turn) raw[u] = narrow8<DT>(x);
+        if (ok && in) *reinterpret_cast<uint4 *>(dst16 + (u * TW + sub) * a.cache.token) = raw[u];
+      }
+      for (int i0 = kHold * TW; i0 < count; i0 += TW) {
+        bool ok;
+        f32x8 x;
+        uint4 w = load(hw, i0 + sub);
+        form(i0 + sub, place(i0 + sub), w, ok, x);
+        if (weight || turn) w = narrow8<DT>(x);
+        if (ok && in) *reinterpret_cast<uint4 *>(dst16 + (i0 + sub) * a.cache.token) = w;
+      }
+      continue;
+    }
+    float top = 0.0f;
+    f32x8 x[kHold];
+    bool ok[kHold], any = false;
+    auto most = [&](const f32x8 &y, bool good) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, good && fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.0f);
+      any |= good;
+    };
 #pragma unroll
     for (int u = 0; u < kHold; ++u) {
       ok[u] = false;
       if (u * TW < count) {
-        form(u * TW + sub, raw[u], ok[u], x[u]);
+        form(u * TW + sub, pos[u], raw[u], ok[u], x[u]);
         most(x[u], ok[u]);
       }
     }
-  }
-  for (int i0 = kHold * TW; i0 < count; i0 += TW) {
-    bool good;
-    f32x8 y;
-    form(i0 + sub, load(i0 + sub), good, y);
-    most(y, good);
-  }
-  if (!__any(any)) return;
-  top = wave_max_f32(top);
-  uint8_t *const code = (which ? a.v_scales : a.k_scales) + (int64_t)page * a.Hkv + h;
-  int now = code_for(top);
-  if (held > 0) {
-    const int was = *code;
-    now = max(now, was);
-    if (now != was)  // the block's older tokens follow
+    for (int i0 = kHold * TW; i0 < count; i0 += TW) {
+      bool good;
+      f32x8 y;
+      form(i0 + sub, place(i0 + sub), load(hw, i0 + sub), good, y);
+      most(y, good);
+    }
+    if (!__any(any)) continue;
+    const int now = max(code_for(wave_max_f32(top)), was);
+    if (held > 0 && now != was)  // the block's older tokens follow
       for (int i = sub; i < held; i += TW) {
-        uint2 *at = reinterpret_cast<uint2 *>(dst8 + (i - held) * a.cache.token);
+        uint2 *old = reinterpret_cast<uint2 *>(dst8 + (i - held) * a.cache.token);
         if (!in) continue;
-        f32x8 y = widen8_e4m3(*at);
+        f32x8 y = widen8_e4m3(*old);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = ldexpf(y[e], was - now);
-        *at = narrow8_e4m3(y);
+        *old = narrow8_e4m3(y);
       }
-  }
-  auto store = [&](int i, f32x8 y) {
+    auto store = [&](int i, f32x8 y) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = ldexpf(y[e], 127 - now);
-    *reinterpret_cast<uint2 *>(dst8 + i * a.cache.token) = narrow8_e4m3(y);
-  };
+      for (int e = 0; e < 8; ++e) y[e] = ldexpf(y[e], 127 - now);
+      *reinterpret_cast<uint2 *>(dst8 + i * a.cache.token) = narrow8_e4m3(y);
+    };
 #pragma unroll
-  for (int u = 0; u < kHold; ++u)
-    if (ok[u]) store(u * TW + sub, x[u]);
-  for (int i0 = kHold * TW; i0 < count; i0 += TW) {
-    bool good;
-    f32x8 y;
-    form(i0 + sub, load(i0 + sub), good, y);
-    if (good) store(i0 + sub, y);
+    for (int u = 0; u < kHold; ++u)
+      if (ok[u] && in) store(u * TW + sub, x[u]);
+    for (int i0 = kHold * TW; i0 < count; i0 += TW) {
+      bool good;
+      f32x8 y;
+      form(i0 + sub, place(i0 + sub), load(hw, i0 + sub), good, y);
+      if (good && in) store(i0 + sub, y);
+    }
+    if (lane == 0) *code = (uint8_t)now;
   }
-  if (lane == 0) *code = (uint8_t)now;
+  // a token without a place in the table of angles
+  if (a.rot_dim > 0 && a.positions == nullptr ? p1 > a.max_pos : a.rot_dim > 0)
+    for (int i = threadIdx.x; i < count; i += kAppendBlock)
+      if (!known(place(i))) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
 }
 
-// One token's queries.
+// One token's queries, kHeads rounds of heads in flight, the first ones before anything is known of the
+// token.
 template <int DT, int LPH>
 __device__ __forceinline__ void append_queries(const KvAppendArgs &a, int t, float inv_D) {
   constexpr int HW = kWave / LPH;  // heads of a round
+  constexpr int kHeads = 4;
   const int lane = threadIdx.x % kWave, l = lane % LPH, sub = lane / LPH;
-  const int s = find_sequence(a.S, t, [&](int i) { return (int64_t)held_cu(a.cu, i, a.T); });
-  const int t0 = a.cu[s], t1 = a.cu[s + 1], ctx = a.ctx_lens ? a.ctx_lens[s] : 0;
-  if (t0 < 0 || t1 > a.T || t < t0 || t >= t1) return;
+  const bool in = 8 * l < a.D;
+  const uint16_t *src = a.q + t * a.q_stride + 8 * l;
+  uint16_t *dst = a.q_out + (int64_t)t * a.Hq * a.D + 8 * l;
+  uint4 next[kHeads];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      const int h = h0 + u * HW + sub;
+      next[u] = make_uint4(0, 0, 0, 0);
+      if (in && h < a.Hq) next[u] = *reinterpret_cast<const uint4 *>(src + h * a.D);
+    }
+  };
+  load(0);
+  const Sequence q = sequence_of(a.cu, a.ctx_lens, a.S, t, [&](int, int32_t cu) { return (int64_t)max(0, min(cu, a.T)); });
+  if (q.begin < 0 || q.end > a.T || t < q.begin || t >= q.end) return;
   const float *angles = nullptr;
-  bool good = ctx >= 0;
+  bool good = q.ctx >= 0;
   if (a.rot_dim > 0) {
-    const int64_t pos = a.positions ? a.positions[t] : (int64_t)ctx + (t - t0);
+    const int64_t pos = a.positions ? a.positions[t] : (int64_t)q.ctx + (t - q.begin);
     good &= pos >= 0 && pos < a.max_pos;
     angles = a.cos_sin + pos * a.rot_dim;
   }
@@ -232,18 +281,11 @@ __device__ __forceinline__ void append_queries(const KvAppendArgs &a, int t, flo
     if (lane == 0) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
     return;
   }
-  const bool in = 8 * l < a.D;
-  const uint16_t *src = a.q + t * a.q_stride + 8 * l;
-  uint16_t *dst = a.q_out + (int64_t)t * a.Hq * a.D + 8 * l;
-  constexpr int kHeads = 4;  // rounds of heads in flight
   for (int h0 = 0; h0 < a.Hq; h0 += HW * kHeads) {
     uint4 raw[kHeads];
 #pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      const int h = h0 + u * HW + sub;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (in && h < a.Hq) raw[u] = *reinterpret_cast<const uint4 *>(src + h * a.D);
-    }
+    for (int u = 0; u < kHeads; ++u) raw[u] = next[u];
+    if (h0 + HW * kHeads < a.Hq) load(h0 + HW * kHeads);
 #pragma unroll
     for (int u = 0; u < kHeads; ++u) {
       const int h = h0 + u * HW + sub;
@@ -254,18 +296,16 @@ __device__ __forceinline__ void append_queries(const KvAppendArgs &a, int t, flo
 }
 
 // LPH: lanes of a head, the power of two that covers D/8 (8 for D <= 64, 16, 32 for D > 128).
-// The first `groups` items are four waves of blocks' heads each, the others four tokens' queries.
+// The first `blocks` items are a block each, the others kAppendWaves tokens' queries.
 template <int DT, int LPH, bool E4>
-__global__ __launch_bounds__(kAppendBlock) void k_kv_append(KvAppendArgs a, int64_t groups, int64_t items, float inv_D) {
+__global__ __launch_bounds__(kAppendBlock, 3) void k_kv_append(KvAppendArgs a, int64_t blocks, int64_t items, float inv_D) {
   if (!lengths_in_order(a.cu, a.S, a.T)) atomicOr(a.status, SMCSD_ST_BAD_INPUT);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    if (it < groups) {
-      const int64_t w = it * kAppendWaves + wave, block = w / (2 * a.Hkv);
-      const int hw = (int)(w - block * 2 * a.Hkv);
-      append_block<DT, LPH, E4>(a, block, hw >= a.Hkv, hw >= a.Hkv ? hw - a.Hkv : hw, inv_D);
+    if (it < blocks) {
+      append_block<DT, LPH, E4>(a, it, wave, inv_D);
     } else {
-      const int64_t t = (it - groups) * kAppendWaves + wave;
+      const int64_t t = (it - blocks) * kAppendWaves + wave;
       if (t < a.T) append_queries<DT, LPH>(a, (int)t, inv_D);
     }
   }
@@ -274,13 +314,12 @@ __global__ __launch_bounds__(kAppendBlock) void k_kv_append(KvAppendArgs a, int6
 template <int DT, bool E4>
 void launch_dt(const KvAppendArgs &a, hipStream_t stream) {
   const int64_t blocks = a.T / a.cache.block_size + 2 * (int64_t)a.S;
-  const int64_t groups = ceil_div(blocks * 2 * a.Hkv, kAppendWaves);
-  const int64_t items = groups + (a.q ? ceil_div(a.T, kAppendWaves) : 0);
+  const int64_t items = blocks + (a.q ? ceil_div(a.T, kAppendWaves) : 0);
   const dim3 grid(grid_blocks(items, kAppendBlock)), block(kAppendBlock);
   const float inv = 1.0f / (float)a.D;
-  if (a.D <= 64) hipLaunchKernelGGL((k_kv_append<DT, 8, E4>), grid, block, 0, stream, a, groups, items, inv);
-  else if (a.D <= 128) hipLaunchKernelGGL((k_kv_append<DT, 16, E4>), grid, block, 0, stream, a, groups, items, inv);
-  else hipLaunchKernelGGL((k_kv_append<DT, 32, E4>), grid, block, 0, stream, a, groups, items, inv);
+  if (a.D <= 64) hipLaunchKernelGGL((k_kv_append<DT, 8, E4>), grid, block, 0, stream, a, blocks, items, inv);
+  else if (a.D <= 128) hipLaunchKernelGGL((k_kv_append<DT, 16, E4>), grid, block, 0, stream, a, blocks, items, inv);
+  else hipLaunchKernelGGL((k_kv_append<DT, 32, E4>), grid, block, 0, stream, a, blocks, items, inv);
 }
 
 }  // namespace
