@@ -196,9 +196,18 @@ __device__ __forceinline__ void append_block(const KvAppendArgs &a, int64_t item
     float top = 0.0f;
     f32x8 x[kHold];
     bool ok[kHold], any = false;
+    // the largest magnitude (the maximum with NaN is the other number); infinities are left out where there
+    // are any
     auto most = [&](const f32x8 &y, bool good) {
+      float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, good && fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.0f);
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+      if (__any(m == INFINITY)) {
+        m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.0f);
+      }
+      top = good ? fmaxf(top, m) : top;
       any |= good;
     };
 #pragma unroll
