@@ -19,35 +19,34 @@ __device__ __forceinline__ int code_for(float top) {
 // The scale as the conversions take it, by its exponent alone: code 0 is 2^-127, 255 NaN.
 __device__ __forceinline__ float scale_of(int code) { return __uint_as_float((uint32_t)code << 23); }
 
-// Eight elements to the 16-bit type.  In f16 a value past the largest number is held there: it
-// can exceed it where the scale is 2^8 or more (448 * 2^7 is within).
-template <int DT>
-__device__ __forceinline__ uint4 widen8_e4m3(uint2 w, int code) {
+// Two elements to the 16-bit type.  In f16 a value past the largest number is held there: it can
+// exceed it where the scale is 2^8 or more (448 * 2^7 is within).
+template <int DT, bool UPPER>
+__device__ __forceinline__ uint32_t widen2_e4m3(uint32_t w, int code) {
   const float s = scale_of(code);
-  uint4 r;
-  if (DT == SMCSD_DTYPE_BF16) {
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, s, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, s, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, s, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, s, true));
-    return r;
+  if (DT == SMCSD_DTYPE_BF16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, UPPER));
+  uint32_t v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, UPPER));
+  if (code >= 127 + 8) {  // infinities (no NaN) become the largest number
+    if ((v & 0x7FFFu) == 0x7C00u) v -= 1;
+    if ((v & 0x7FFF0000u) == 0x7C000000u) v -= 0x10000u;
   }
-  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, s, false));
-  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, s, true));
-  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, s, false));
-  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, s, true));
-  if (code >= 127 + 8) {
-    auto hold = [](uint32_t v) {  // infinities (no NaN) become the largest number
-      if ((v & 0x7FFFu) == 0x7C00u) v -= 1;
-      if ((v & 0x7FFF0000u) == 0x7C000000u) v -= 0x10000u;
-      return v;
-    };
-    r.x = hold(r.x);
-    r.y = hold(r.y);
-    r.z = hold(r.z);
-    r.w = hold(r.w);
-  }
-  return r;
+  return v;
+}
+// Eight: with one scale, with one for each four, or each with its own.
+template <int DT>
+__device__ __forceinline__ uint4 widen8_e4m3(uint2 w, int code0, int code1) {
+  return make_uint4(widen2_e4m3<DT, false>(w.x, code0), widen2_e4m3<DT, true>(w.x, code0),
+                    widen2_e4m3<DT, false>(w.y, code1), widen2_e4m3<DT, true>(w.y, code1));
+}
+template <int DT>
+__device__ __forceinline__ uint4 widen8_e4m3(uint2 w, int code) { return widen8_e4m3<DT>(w, code, code); }
+template <int DT>
+__device__ __forceinline__ uint4 widen8_e4m3(uint2 w, const int (&code)[8]) {
+  auto both = [](uint32_t lo, uint32_t hi) { return (lo & 0xFFFFu) | (hi & 0xFFFF0000u); };
+  return make_uint4(both(widen2_e4m3<DT, false>(w.x, code[0]), widen2_e4m3<DT, false>(w.x, code[1])),
+                    both(widen2_e4m3<DT, true>(w.x, code[2]), widen2_e4m3<DT, true>(w.x, code[3])),
+                    both(widen2_e4m3<DT, false>(w.y, code[4]), widen2_e4m3<DT, false>(w.y, code[5])),
+                    both(widen2_e4m3<DT, true>(w.y, code[6]), widen2_e4m3<DT, true>(w.y, code[7])));
 }
 
 // Eight values to e4m3, to nearest even; past 448, and what is not finite: NaN.

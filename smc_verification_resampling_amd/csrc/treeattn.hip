@@ -29,6 +29,7 @@ namespace smcsd {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Reads of a tile.  In assembly, each with its wait: the compiler, which knows no buffers,
@@ -58,6 +59,38 @@ __device__ __forceinline__ void read_columns(V8 (&x)[2], uint32_t a, uint32_t b,
   }
 }
 
+// The same of tiles of 8 bits: N rows' 16 bytes each, and N times 8 keys of one column.
+template <int N>
+__device__ __forceinline__ void read_rows8(u32x4 (&x)[N], const uint32_t (&a)[N], int offset) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 2)
+    asm volatile(
+        "ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1])
+        : "v"(a[0]), "v"(a[1]), "i"(offset));
+  else
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+        "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(offset));
+}
+template <int N>
+__device__ __forceinline__ void read_columns8(u32x2 (&x)[N], const uint32_t (&a)[N], int offset) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 2)
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %2 offset:%4\n\tds_read_b64_tr_b8 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1])
+        : "v"(a[0]), "v"(a[1]), "i"(offset));
+  else
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %4 offset:%8\n\tds_read_b64_tr_b8 %1, %5 offset:%8\n\t"
+        "ds_read_b64_tr_b8 %2, %6 offset:%8\n\tds_read_b64_tr_b8 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "i"(offset));
+}
+
 template <int DT> struct Mma;
 template <> struct Mma<SMCSD_DTYPE_BF16> {
   typedef Half<SMCSD_DTYPE_BF16>::V8 V8;
@@ -82,6 +115,8 @@ constexpr int kRowsWave = 32;
 // (256 sequences of 8 heads, 3.2 GB) 687 us against 661, four buffers 802: what the loads gain
 // in flight, the workgroups lose that no longer fit beside each other.
 constexpr int KT = 32, NB = 2;
+// Keys of a tile of 8-bit pages, and its buffers.
+constexpr int KT8 = 64, NB8 = 2;
 constexpr int kWavesMax = 4;
 // Workgroups of one wave of rows that the splits of a launch aim at (half as many where two row tiles
 // of four waves share a head's keys): 64 rows x 16 heads over 131,071 keys take 120 us and 12 to join
@@ -256,6 +291,19 @@ __device__ __forceinline__ int place_of(int r) {
 // rescale nothing.
 constexpr float kLag = 8.0f;
 
+// The same for rows of 8 bits, of CH chunks of 16 elements.  The transposing read takes one chunk of
+// eight rows, four neighbours and the four that lie eight further, and its other half wave's chunk
+// beside it: those differ in the place's upper bits and its lowest.
+template <int CH>
+__device__ __forceinline__ int place8_of(int r) {
+  const int r2 = (r >> 2) & 1, r3 = (r >> 3) & 1;
+  return CH == 4 ? r2 | r3 << 1 : CH == 8 ? r2 | (r & 2) | r3 << 2 : r2 | (r & 3) << 1 | r3 << 3;
+}
+
+// What the pages hold: 16 bits, or 8 bits with scales, in blocks of a multiple of four tokens (any four
+// keys that an operand holds side by side are then of one block) or of any other number.
+enum { kPages16, kPages8, kPages8Any };
+
 __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothing to load
 
 // DP: head size padded to 64, 128 or 256.  NW: waves.
@@ -266,7 +314,7 @@ __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothin
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 5.6 us, all of it latency.
-template <int DT, int DP, int NW, bool PREFIX, bool E4>
+template <int DT, int DP, int NW, bool PREFIX, int PG>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
   typedef typename Half<DT>::V4 V4;
@@ -274,11 +322,13 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   constexpr int RB = DP * 2;       // bytes of a row
   constexpr int NS = DP / 16;      // product steps of a score
   constexpr int NA = DP / 32;      // accumulator tiles of an output row
-  constexpr int TB = KT * RB;      // bytes of a tile
+  constexpr bool E4 = PG != kPages16;
+  constexpr int KTP = E4 ? KT8 : KT, NBP = E4 ? NB8 : NB;
+  constexpr int TB = E4 ? KTP * DP : KTP * RB;  // bytes of a tile
   constexpr int RW = kWave / CH;             // rows of a wave's load
   constexpr int NLD = KT / (RW * NW);        // loads of keys (and as many of values) of a wave for a tile
-  __shared__ __attribute__((aligned(16))) char sKV[2 * NB * TB];  // keys' buffers, then values'
-  __shared__ uint32_t sOdd[PREFIX ? 1 : E4 ? 2 * KT : KT];  // a new token whose values are not all finite
+  __shared__ __attribute__((aligned(256))) char sKV[2 * NBP * TB];  // keys' buffers, then values'
+  __shared__ uint32_t sOdd[PREFIX ? 1 : KTP];  // a new token whose values are not all finite
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int hw = lane / 32, col = lane % 32;
   const Cut &cut = PREFIX ? p.prefix : p.suffix;
@@ -311,7 +361,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   }
   // this split's keys: an equal share in whole tiles
   const int per = (hi - lo + cut.splits - 1) / cut.splits;
-  const int64_t share = (int64_t)((per + KT - 1) / KT) * KT;
+  const int64_t share = (int64_t)((per + KTP - 1) / KTP) * KTP;
   const int k0 = (int)min((int64_t)hi, lo + split * share), k1 = (int)min((int64_t)hi, k0 + share);
 
   // Staging, by loads that go straight to LDS, 64 chunks of 16 bytes in a row for a wave's
@@ -333,14 +383,14 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   int32_t ids = 0;
   int id0 = -kWave;
   bool bad_page = false;
-  // The place of row lane % KT of the tile at `base`, -1 if it may not be read; its block.
+  // The place of row lane % KTP of the tile at `base`, -1 if it may not be read; its block.
   auto place_row = [&](int base, int32_t &pg) {
-    if ((int)div_by(p.page, min(base + KT, k1) - 1) >= id0 + kWave) {
+    if ((int)div_by(p.page, min(base + KTP, k1) - 1) >= id0 + kWave) {
       id0 = div_by(p.page, base);
       ids = table[min(id0 + lane, (int)div_by(p.page, k1 - 1))];
       asm volatile("" : "+v"(ids));  // waited for here, not by every tile
     }
-    const int pos = base + lane % KT, block = div_by(p.page, pos);
+    const int pos = base + lane % KTP, block = div_by(p.page, pos);
     pg = __shfl(ids, min(block - id0, kWave - 1), kWave);
     const bool page_ok = pg >= 0 && pg < a.cache.P, ok = page_ok && pos < k1;
     bad_page |= !page_ok && pos < k1;
@@ -404,7 +454,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     const uint32_t flip = p.negate ? 0x80008000u : 0u;
 #pragma unroll
     for (int st = 0; st < NS; ++st) {
-      const int d = 16 * st + 8 * hw;
+      const int d = E4 ? 32 * (st / 2) + 16 * hw + 8 * (st % 2) : 16 * st + 8 * hw;
       uint4 w = make_uint4(0, 0, 0, 0);
       if (live && d < a.D) w = *reinterpret_cast<const uint4 *>(qp + d);
       w.x ^= flip;
@@ -442,73 +492,72 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     }
   };
 
-  // 8-bit pages: a tile comes through registers, 16 elements to a lane, and is widened with its
-  // blocks' scales on its way to LDS, where it lies as a tile of 16-bit pages does.  Two tiles are
-  // on their way while a third is computed.  What `mend` does for new tokens happens on the way.
-  constexpr int CH8 = DP / 16;                        // 16-byte chunks of a row of 8-bit elements
-  constexpr int NL8 = (KT * CH8 + NW * kWave - 1) / (NW * kWave);
-  struct Tile {
-    u32x4 k[NL8], v[NL8];
-    int ks, vs;     // codes of the scales of row lane % KT
+  // 8-bit pages go to LDS as they are, 64 chunks of 16 elements to a wave's instruction, and are widened
+  // with their blocks' scales as the products take them.  The codes of a tile's scales: row `lane`'s.
+  constexpr int CH8 = DP / 16, RW8 = kWave / CH8, NLD8 = KT8 / (RW8 * NW);
+  struct Codes {
+    int k, v;
     uint64_t rows;  // which may be read
   };
-  auto ask_tile = [&](Tile &t, int base) {
+  auto fetch_tile8 = [&](int buf, int base) {
+    Codes c{127, 127, 0};
     int32_t pg;
     const int64_t off = place_row(base, pg);
-    t.rows = __ballot(off >= 0);
-    t.ks = t.vs = 127;
+    c.rows = __ballot(off >= 0);
     if (off >= 0) {
-      t.ks = a.k_scales[(int64_t)pg * a.Hkv + hk];
-      t.vs = a.v_scales[(int64_t)pg * a.Hkv + hk];
+      c.k = a.k_scales[(int64_t)pg * a.Hkv + hk];
+      c.v = a.v_scales[(int64_t)pg * a.Hkv + hk];
     }
-    int64_t at[NL8];
+    constexpr int kPolicy = NW < 4 ? 2 : 0;  // as for 16 bits
 #pragma unroll
-    for (int i = 0; i < NL8; ++i) at[i] = __shfl((long long)off, min(((i * NW + wave) * kWave + lane) / CH8, KT - 1), kWave);
-#pragma unroll
-    for (int i = 0; i < NL8; ++i) {
-      const int chunk = lane % CH8;
-      const bool in = at[i] >= 0 && chunk * 16 < a.D;
-      const u32x4 *const k = in ? (const u32x4 *)(kbase + at[i] + chunk * 16) : (const u32x4 *)&kNothing;
-      const u32x4 *const v = in ? (const u32x4 *)(vbase + at[i] + chunk * 16) : (const u32x4 *)&kNothing;
-      t.k[i] = *k;
-      t.v[i] = *v;
+    for (int i = 0; i < NLD8; ++i) {
+      const int first = (i * NW + wave) * RW8;
+      const int64_t at = __shfl((long long)off, first + lane / CH8, kWave);
+      const int chunk = (lane % CH8) ^ place8_of<CH8>(first + lane / CH8);
+      const bool in = at >= 0 && chunk * 16 < a.D;
+      const Elem *const k = in ? kbase + at + chunk * 16 : (const Elem *)&kNothing;
+      const Elem *const v = in ? vbase + at + chunk * 16 : (const Elem *)&kNothing;
+      __builtin_amdgcn_global_load_lds((glb_void *)k, (lds_void *)(lds + buf * TB + first * DP), 16, 0, kPolicy);
+      __builtin_amdgcn_global_load_lds((glb_void *)v, (lds_void *)(lds + (NB8 + buf) * TB + first * DP), 16, 0, kPolicy);
     }
+    return c;
   };
-  auto put_tile = [&](const Tile &t, int buf, int base) {
-    const bool fresh = !PREFIX && base + KT > ctx;
+  // Among 8 bits only NaN is not finite: the elements 0x7F and 0xFF.
+  auto mend8 = [&](int buf, int base) {
+#pragma unroll 1
+    for (int i = 0; i < NLD8; ++i) {
+      const int row = (i * NW + wave) * RW8 + lane / CH8;
+      u32x4 *const v = reinterpret_cast<u32x4 *>(sKV + (NB8 + buf) * TB + row * DP + lane % CH8 * 16);
+      u32x4 w = *v;
+      bool odd = false;
 #pragma unroll
-    for (int i = 0; i < NL8; ++i) {
-      const int idx = (i * NW + wave) * kWave + lane, row = idx / CH8, chunk = 2 * (idx % CH8);
-      const int ks = __shfl(t.ks, min(row, KT - 1), kWave), vs = __shfl(t.vs, min(row, KT - 1), kWave);
-      uint4 k[2] = {widen8_e4m3<DT>(make_uint2(t.k[i][0], t.k[i][1]), ks), widen8_e4m3<DT>(make_uint2(t.k[i][2], t.k[i][3]), ks)};
-      uint4 v[2] = {widen8_e4m3<DT>(make_uint2(t.v[i][0], t.v[i][1]), vs), widen8_e4m3<DT>(make_uint2(t.v[i][2], t.v[i][3]), vs)};
-      if (fresh) {
-        bool odd = false;
-        if (base + row >= ctx)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) odd |= (finite(v[c].x) & finite(v[c].y) & finite(v[c].z) & finite(v[c].w)) != ~0u;
-        const uint64_t any = __ballot(odd);
-        if (lane % CH8 == 0 && row < KT) sOdd[buf * KT + row] = (any >> lane) & ((1ull << CH8) - 1) ? 1 : 0;
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t all = ((w[c] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // of seven ones a carry
+        odd |= all != 0;
+        w[c] &= ~((all - (all >> 7)) | all);
       }
-      if (KT * CH8 % (NW * kWave) == 0 || row < KT) {
-        const int place = place_of<CH>(row);
-        char *const kr = sKV + buf * TB + row * RB, *const vr = kr + NB * TB;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          *reinterpret_cast<uint4 *>(kr + ((chunk + c) ^ place) * 16) = k[c];
-          *reinterpret_cast<uint4 *>(vr + ((chunk + c) ^ place) * 16) = v[c];
-        }
-      }
+      odd &= base + row >= ctx;
+      const uint64_t any = __ballot(odd);
+      if (odd) *v = w;
+      if (lane % CH8 == 0) sOdd[row] = (any >> lane) & ((1ull << CH8) - 1) ? 1 : 0;
     }
   };
 
   // LDS offsets of a step's operands.  Keys: chunk 2 st + hw of row col.  Values: row 16h +
   // 8x + 4hw + i16/4, chunk 4t + 2dh + (i16%4)/2.  The permuted places depend on the low bits
   // of st, and of t and x; the rest are constants.
-  constexpr int NKA = NS < 8 ? NS : 8;
-  constexpr int NVT = NA < 4 ? NA : 4;
+  // Of 8 bits a chunk serves two steps of a score: 2 st + hw of row col, st = 0..NS/2-1, and elements
+  // 32 st + 16 hw + 0..15; and the values' rows 16h + 4hw + 0..3 and + 8..11, chunk 2t + dh, are one read.
+  constexpr int NKA = E4 ? 1 : NS < 8 ? NS : 8;
+  constexpr int NVT = E4 ? 1 : NA < 4 ? NA : 4;
   const int i16 = lane % 16, dh = (lane / 16) & 1;
   int ka[NKA], va[NVT][2];
+  uint32_t ka8 = 0, va8 = 0;
+  if constexpr (E4) {
+    const int row = (i16 / 8) * 8 + 4 * hw + (i16 / 2) % 4;
+    ka8 = (uint32_t)(uintptr_t)lds + col * DP + ((hw ^ place8_of<CH8>(col)) * 16);
+    va8 = (uint32_t)(uintptr_t)lds + NB8 * TB + row * DP + ((dh ^ place8_of<CH8>(row)) * 16) + (i16 & 1) * 8;
+  }
 #pragma unroll
   for (int st = 0; st < NKA; ++st) ka[st] = col * RB + (((2 * st + hw) ^ place_of<CH>(col)) * 16);
 #pragma unroll
@@ -533,16 +582,41 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     }
     return z;
   };
-  // A tile's keys, from position `base` on; ok: which may be read.
-  auto step = [&](int base, uint64_t ok) {
+  auto scores8 = [&](auto half, int code) {
+    f32x16 z = f32x16{};
+    constexpr int NR = NS / 2 < 4 ? NS / 2 : 4;
+#pragma unroll
+    for (int st = 0; st < NS / 2; st += NR) {
+      u32x4 kf[NR];
+      uint32_t at[NR];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) at[i] = ka8 ^ (uint32_t)((st + i) * 32);
+      read_rows8(kf, at, half * 32 * DP);
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          z = Mma<DT>::run(__builtin_bit_cast(V8, widen8_e4m3<DT>(make_uint2(kf[i][2 * e], kf[i][2 * e + 1]), code)), q[2 * (st + i) + e], z);
+    }
+    return z;
+  };
+  // 32 of a tile's keys, from position `base` on; ok: which may be read.  8 bits: the half of the tile that
+  // they are, the codes of the scales.
+  auto step = [&](int base, uint32_t ok, auto half, const Codes &codes) {
     auto sees = [&] {  // the tile's keys that this lane's row sees
       const int nb = ctx - base;  // so many of them are context
       uint32_t see = nb >= 32 ? 0xFFFFFFFFu : nb > 0 ? (1u << nb) - 1 : 0u;
       if (nb < 32) see |= nb >= 0 ? (uint32_t)(bits << nb) : (nb > -64 ? (uint32_t)(bits >> -nb) : 0u);
-      return see & (uint32_t)ok;
+      return see & ok;
     };
-    f32x16 z = scores();
-    if (ok != ~0ull || (!PREFIX && base + KT > ctx)) {
+    f32x16 z;
+    if constexpr (E4) {
+      const auto c = __builtin_amdgcn_permlane32_swap(codes.k, codes.k, false, false);
+      z = scores8(half, (int)(half == 0 ? c[0] : c[1]));  // of row 32 half + col
+    } else {
+      z = scores();
+    }
+    if (ok != ~0u || (!PREFIX && base + KT > ctx)) {
       asm volatile("");  // a branch, taken by few tiles: not to be computed by all
       const uint32_t mine = sees() >> (4 * hw);
 #pragma unroll
@@ -573,6 +647,31 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       // rounded for the product, as the matrix instruction takes them; l sums them unrounded.  Against 64
       // bits that makes 0.0023 of relative error in bf16 where fp32 probabilities leave 0.0017
       pr[h] = __builtin_convertvector(e, V8);
+      if constexpr (E4) {
+        int vc[8];  // the codes of the eight keys, or of the four that each half of them is
+        constexpr int NC = PG == kPages8 ? 2 : 8;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          vc[i] = __shfl(codes.v, 32 * half + 16 * h + 4 * hw + (NC == 2 ? 8 * i : 8 * (i / 4) + i % 4), kWave);
+        constexpr int NR = NA < 4 ? NA : 4;
+#pragma unroll
+        for (int t = 0; t < NA; t += NR) {
+          u32x2 vf[NR];
+          uint32_t at[NR];
+#pragma unroll
+          for (int i = 0; i < NR; ++i) at[i] = va8 ^ (uint32_t)((t + i) * 32);
+          read_columns8(vf, at, (32 * half + 16 * h) * DP);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const uint2 w = make_uint2(vf[i][0], vf[i][1]);
+            uint4 x;
+            if constexpr (NC == 2) x = widen8_e4m3<DT>(w, vc[0], vc[1]);
+            else x = widen8_e4m3<DT>(w, vc);
+            o[t + i] = Mma<DT>::run(__builtin_bit_cast(V8, x), pr[h], o[t + i]);
+          }
+        }
+        continue;
+      }
       // values: keys 16h + 8x + 4hw + 0..3 for operand element 4x + 0..3 of product h
 #pragma unroll
       for (int t = 0; t < NA; t += 2) {
@@ -600,35 +699,37 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       va[t][1] += d;
     }
   };
+  using Half0 = std::integral_constant<int, 0>;
+  using Half1 = std::integral_constant<int, 1>;
   if constexpr (E4) {
     if (k0 < k1) {
-      Tile even, uneven;
-      ask_tile(even, k0);
-      put_tile(even, 0, k0);
-      uint64_t ok = even.rows;
-      if (k0 + KT < k1) ask_tile(even, k0 + KT);
-      if (k0 + 2 * KT < k1) ask_tile(uneven, k0 + 2 * KT);
-      // the tile at `base` in buffer `buf`; `next`: the one behind it, then the one three further
-      auto turn = [&](Tile &next, int buf, int base) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      Codes next = fetch_tile8(0, k0);
+      int buf = 0;
+      for (int base = k0; base < k1; base += KT8) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const uint64_t now = ok;
-        if (!PREFIX && base + KT > ctx) {
-          const uint64_t rows = __ballot(lane < KT && sOdd[buf * KT + lane % KT]);
+        Codes now = next;
+        if (base + KT8 < k1) next = fetch_tile8(buf ^ 1, base + KT8);
+        __builtin_amdgcn_sched_barrier(0);  // the loads go out before, and nothing below moves up
+        if (!PREFIX && base + KT8 > ctx) {
+          mend8(buf, base);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          const bool nan = now.v == 255 && base + lane >= ctx;
+          const uint64_t rows = __ballot(sOdd[lane % KTP] || nan);
           odd |= base >= ctx ? rows << (base - ctx) : rows >> (ctx - base);
+          now.v = nan ? 127 : now.v;
         }
-        if (base + KT < k1) {
-          put_tile(next, buf ^ 1, base + KT);
-          ok = next.rows;
-          if (base + 3 * KT < k1) ask_tile(next, base + 3 * KT);
+        if (busy) {
+          step(base, (uint32_t)now.rows, Half0{}, now);
+          if (base + 32 < k1) step(base + 32, (uint32_t)(now.rows >> 32), Half1{}, now);
         }
-        if (busy) step(base, now);
-        turn_buffers(buf ? -TB : TB);
-      };
-      for (int base = k0; base < k1; base += 2 * KT) {
-        turn(even, 0, base);
-        if (base + KT < k1) turn(uneven, 1, base + KT);
+        const int d = buf ? -TB : TB;
+        ka8 += d;
+        va8 += d;
+        buf ^= 1;
       }
     }
   } else if (k0 < k1) {
@@ -649,7 +750,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
         const uint64_t rows = __ballot(lane < KT && sOdd[lane % KT]);
         odd |= base >= ctx ? rows << (base - ctx) : rows >> (ctx - base);
       }
-      if (busy) step(base, ok);
+      if (busy) step(base, (uint32_t)ok, Half0{}, Codes{});
       // the next buffer's offsets
       turn_buffers(buf ? -TB : TB);
       buf ^= 1;
@@ -810,25 +911,25 @@ __global__ __launch_bounds__(kJoinBlock) void k_attn_join(TreeAttnArgs a, Plan p
   }
 }
 
-template <int DT, int DP, bool PREFIX, bool E4>
+template <int DT, int DP, bool PREFIX, int PG>
 void launch_part(const TreeAttnArgs &a, const Plan &p, hipStream_t stream) {
   const Cut &c = PREFIX ? p.prefix : p.suffix;
   const int64_t units = PREFIX ? a.B : (int64_t)a.B * a.N;
   const dim3 grid((unsigned)(units * c.splits * c.tiles * a.Hkv)), block(c.waves * kWave);
   if (c.waves == 2)
-    hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX, E4>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 2, PREFIX, PG>), grid, block, 0, stream, a, p);
   else
-    hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX, E4>), grid, block, 0, stream, a, p);
+    hipLaunchKernelGGL((k_attn<DT, DP, 4, PREFIX, PG>), grid, block, 0, stream, a, p);
 }
 
-template <int DT, int DP, bool E4>
+template <int DT, int DP, int PG>
 void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStream_t stream) {
   const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
   if (p.prefix.splits > 0) {
     hipLaunchKernelGGL(k_shared_len, dim3(grid_blocks(a.B, kShareBlock)), dim3(kShareBlock), 0, stream, a, shared_len);
-    launch_part<DT, DP, true, E4>(a, p, stream);
+    launch_part<DT, DP, true, PG>(a, p, stream);
   }
-  launch_part<DT, DP, false, E4>(a, p, stream);
+  launch_part<DT, DP, false, PG>(a, p, stream);
   if (p.suffix.splits > 1) {
     // four parts or more to a group
     const int width = join_width(a.D), parts = p.prefix.splits + p.suffix.splits;
@@ -839,17 +940,18 @@ void launch_dp(const TreeAttnArgs &a, const Plan &p, int32_t *shared_len, hipStr
   }
 }
 
+template <int DT, int PG>
+void launch_head(const TreeAttnArgs &a, const Plan &p, int DP, int32_t *shared_len, hipStream_t stream) {
+  if (DP == 64) launch_dp<DT, 64, PG>(a, p, shared_len, stream);
+  else if (DP == 128) launch_dp<DT, 128, PG>(a, p, shared_len, stream);
+  else launch_dp<DT, 256, PG>(a, p, shared_len, stream);
+}
+
 template <int DT>
 void launch_pages(const TreeAttnArgs &a, const Plan &p, int DP, int32_t *shared_len, hipStream_t stream) {
-  if (a.k_scales) {
-    if (DP == 64) launch_dp<DT, 64, true>(a, p, shared_len, stream);
-    else if (DP == 128) launch_dp<DT, 128, true>(a, p, shared_len, stream);
-    else launch_dp<DT, 256, true>(a, p, shared_len, stream);
-  } else {
-    if (DP == 64) launch_dp<DT, 64, false>(a, p, shared_len, stream);
-    else if (DP == 128) launch_dp<DT, 128, false>(a, p, shared_len, stream);
-    else launch_dp<DT, 256, false>(a, p, shared_len, stream);
-  }
+  if (!a.k_scales) launch_head<DT, kPages16>(a, p, DP, shared_len, stream);
+  else if (a.cache.block_size % 4 == 0) launch_head<DT, kPages8>(a, p, DP, shared_len, stream);
+  else launch_head<DT, kPages8Any>(a, p, DP, shared_len, stream);
 }
 
 }  // namespace
