@@ -15,9 +15,11 @@
  * Model-Decoding-with-Speculative-Sampling", section 1 and section 4.2) define the
  * secondary SpS mode: modified rejection sampling on the same logits.
  * Beside that path stand the operators that a target's pass and a server need around it:
- * the new tokens' way into the paged cache, attention over it, log-probabilities with
- * alternatives, and the pages' admission, retirement, compaction and copies (the only
- * entry that copies KV data is smcsd_kv_copy, which runs the lists that others write).
+ * whole prompts' and new tokens' way into the paged cache (of 16 bits, or of 8 with a scale
+ * for each block and head), attention of prompts and of drafted trees over it,
+ * log-probabilities with alternatives, and the pages' admission, retirement, compaction and
+ * copies (the only entries that copy KV data are smcsd_kv_copy and smcsd_kv_copy_scaled,
+ * which run the lists that others write).
  *
  * Conventions for every entry point
  *   - Array arguments are DEVICE pointers owned by the caller; the library allocates
@@ -61,7 +63,8 @@ extern "C" {
 /* logits element type */
 #define SMCSD_DTYPE_F32 0
 #define SMCSD_DTYPE_BF16 1
-/* element type of queries, keys and values beside bf16 (smcsd_qk_norm_rope, smcsd_tree_attention) */
+/* element type of queries, keys and values beside bf16 (smcsd_qk_norm_rope, smcsd_kv_append,
+ * smcsd_tree_attention, smcsd_prompt_attention) */
 #define SMCSD_DTYPE_F16 2
 /* element type of 8-bit pages: e4m3 (OCP; no infinities), with a scale for each block and head:
  * a code x (E8M0) that stands for 2^(x - 127), 255 for NaN (smcsd_kv_append) */

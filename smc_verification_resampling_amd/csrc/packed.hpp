@@ -7,28 +7,9 @@
 
 namespace smcsd {
 
-// cu[s] held within [0, T], so that whatever stands there, what is derived from it stays small.
-__device__ __forceinline__ int held_cu(const int32_t *cu, int s, int T) { return max(0, min(cu[s], T)); }
-
-// The largest s in [0, S) with first(s) <= x, where first does not decrease (0 if there is
-// none): every wave for itself, two rounds of loads for up to 4096 sequences.
-template <class F>
-__device__ __forceinline__ int find_sequence(int S, int64_t x, F first) {
-  const int lane = threadIdx.x % kWave;
-  int lo = 0, n = S;
-  while (n > 1) {
-    const int step = (n + kWave - 1) / kWave;
-    const int at = lo + min(lane * step, n - 1);
-    const bool below = lane * step < n && first(at) <= x;
-    const int count = max(1, (int)__popcll(__ballot(below)));
-    lo += (count - 1) * step;
-    n = min(step, n - (count - 1) * step);
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-
-// The same with what stands there: a lane that looks at a sequence loads its bounds and context (ctx
-// null: 0) along, and the wave takes those of the one it finds.
+// The largest s in [0, S) with first(s, cu[s]) <= x, where first does not decrease (0 if there is none),
+// with its bounds and context (ctx null: 0): every wave for itself, two rounds of loads for up to 4096
+// sequences.  A lane that looks at a sequence loads all of it, and the wave takes what it finds from there.
 struct Sequence {
   int s, begin, end, ctx;
 };

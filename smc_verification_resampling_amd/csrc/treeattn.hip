@@ -13,6 +13,8 @@
 // loads that write to LDS directly: the next tile is on its way while the present one is
 // computed.  Rows of a tile are stored with their 16-byte chunks permuted by the row number,
 // so that reads of one chunk over many rows fall on different banks.
+// 8-bit pages lie in LDS as they are, in tiles of 64 tokens, and are widened with their blocks' scales
+// between LDS and the products: eight elements in four instructions that take the scale along.
 // Long contexts are split over workgroups (each a range of keys of equal length) and the
 // parts (m, l, O) joined in fp32.
 #include <cmath>
@@ -115,7 +117,10 @@ constexpr int kRowsWave = 32;
 // (256 sequences of 8 heads, 3.2 GB) 687 us against 661, four buffers 802: what the loads gain
 // in flight, the workgroups lose that no longer fit beside each other.
 constexpr int KT = 32, NB = 2;
-// Keys of a tile of 8-bit pages, and its buffers.
+// Keys of a tile of 8-bit pages (the bytes of 32 of 16 bits), and its buffers.  Tiles of 32 keys that came
+// through registers and were widened once for all waves on their way to LDS took 258 us for 32 prompts'
+// 2048 shared keys and 320 x 8 rows each with the particles' own, 480 for 256 sequences of 9 x 32 heads over up
+// to 4093 keys; 174 and 374 so: half the bytes through LDS, and nothing staged in registers.
 constexpr int KT8 = 64, NB8 = 2;
 constexpr int kWavesMax = 4;
 // Workgroups of one wave of rows that the splits of a launch aim at (half as many where two row tiles
@@ -314,6 +319,11 @@ __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothin
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 5.6 us, all of it latency.
+// 8-bit pages: the shared pass 130 us, the own keys 54; the 256 sequences, 1.65 GB, 374 us (4.4 TB/s).  Both
+// are bound by instructions: vector ones take about half of the SIMDs' time, the products a quarter, and
+// two or three waves cannot overlap them further.  Of some 200 vector instructions that 32 keys take a wave,
+// 64 widen.  Higher priority for the waves at a product gave 1 %; bounds for a third wave left the compiler
+// without a place for the 188 registers of NW = 2, and it fell to one wave (528 us for the 256 sequences).
 template <int DT, int DP, int NW, bool PREFIX, int PG>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
@@ -508,7 +518,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       c.k = a.k_scales[(int64_t)pg * a.Hkv + hk];
       c.v = a.v_scales[(int64_t)pg * a.Hkv + hk];
     }
-    constexpr int kPolicy = NW < 4 ? 2 : 0;  // as for 16 bits
+    constexpr int kPolicy = NW < 4 ? 2 : 0;  // as for 16 bits: 256 sequences of 9 x 32 heads 374 us, 406 without
 #pragma unroll
     for (int i = 0; i < NLD8; ++i) {
       const int first = (i * NW + wave) * RW8;
@@ -699,11 +709,40 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
       va[t][1] += d;
     }
   };
+  // The prompt's shared part of this row joined to m, l and O; `mine`: this lane's share of its sum.  8-bit
+  // pages begin with it, its loads beside those of the first tile: the batched round's own keys 54 us, 56 with it last.
+  const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
+  auto add_shared = [&](float mine) {
+    if (PREFIX || cut.splits > 1 || p.prefix.splits == 0 || lo == 0 || !live) return;
+    for (int i = 0; i < p.prefix.splits; ++i) {
+      const float mp = p.ml[2 * (i * rows + orow)], lp = p.ml[2 * (i * rows + orow) + 1];
+      if (lp == 0.0f) continue;
+      const float mn = fmaxf(m, mp);
+      const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn), fp = mp == kNegInf ? 0.0f : fast_exp2(mp - mn);
+      const float *acc = p.acc + (i * rows + orow) * a.D;
+      m = mn;
+      l = l * f + mine * (lp * fp);
+#pragma unroll
+      for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int d = 32 * t + 8 * b + 4 * hw;
+          if (d >= a.D) continue;
+          const float4 x = *reinterpret_cast<const float4 *>(acc + d);
+          o[t][4 * b] = o[t][4 * b] * f + x.x * fp;
+          o[t][4 * b + 1] = o[t][4 * b + 1] * f + x.y * fp;
+          o[t][4 * b + 2] = o[t][4 * b + 2] * f + x.z * fp;
+          o[t][4 * b + 3] = o[t][4 * b + 3] * f + x.w * fp;
+        }
+    }
+  };
   using Half0 = std::integral_constant<int, 0>;
   using Half1 = std::integral_constant<int, 1>;
   if constexpr (E4) {
+    Codes next{};
+    if (k0 < k1) next = fetch_tile8(0, k0);
+    add_shared(hw == 0 ? 1.0f : 0.0f);
     if (k0 < k1) {
-      Codes next = fetch_tile8(0, k0);
       int buf = 0;
       for (int base = k0; base < k1; base += KT8) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -786,7 +825,6 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
   l = sum_halves(l);
 
   // the row's part, or the row itself
-  const int64_t rows = (int64_t)a.B * a.N * a.R * a.Hq;
   const int part = PREFIX ? split : p.prefix.splits + split;
   if (PREFIX || cut.splits > 1) {
     if (!live) return;
@@ -809,29 +847,7 @@ __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 :
     return;
   }
   if (!live) return;
-  if (p.prefix.splits > 0 && lo > 0) {  // the prompt's shared part of this row
-    for (int i = 0; i < p.prefix.splits; ++i) {
-      const float mp = p.ml[2 * (i * rows + orow)], lp = p.ml[2 * (i * rows + orow) + 1];
-      if (lp == 0.0f) continue;
-      const float mn = fmaxf(m, mp);
-      const float f = m == kNegInf ? 0.0f : fast_exp2(m - mn), fp = mp == kNegInf ? 0.0f : fast_exp2(mp - mn);
-      const float *acc = p.acc + (i * rows + orow) * a.D;
-      m = mn;
-      l = l * f + lp * fp;
-#pragma unroll
-      for (int t = 0; t < NA; ++t)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int d = 32 * t + 8 * b + 4 * hw;
-          if (d >= a.D) continue;
-          const float4 x = *reinterpret_cast<const float4 *>(acc + d);
-          o[t][4 * b] = o[t][4 * b] * f + x.x * fp;
-          o[t][4 * b + 1] = o[t][4 * b + 1] * f + x.y * fp;
-          o[t][4 * b + 2] = o[t][4 * b + 2] * f + x.z * fp;
-          o[t][4 * b + 3] = o[t][4 * b + 3] * f + x.w * fp;
-        }
-    }
-  }
+  if constexpr (!E4) add_shared(1.0f);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t *out = a.out + orow * a.D;
 #pragma unroll
