@@ -650,7 +650,10 @@ def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Te
     dtype = caches[0].dtype
     ptrs = (ctypes.c_void_p * n)()
     for i, c in enumerate(caches):
-        if _pages(c, "caches[%d]" % i, dtype, dev) != (shape, strides):
+        # (the first one's checks hold for those that are like it)
+        if i and not (isinstance(c, torch.Tensor) and c.shape == shape and c.stride() == strides and
+                      c.dtype is dtype and c.get_device() == dev):
+            _pages(c, "caches[%d]" % i, dtype, dev)
             raise SmcsdError("caches must have one shape and layout")
         ptrs[i] = c.data_ptr()
     P, bs, H, D = shape
@@ -667,8 +670,13 @@ def kv_copy(caches: Sequence[torch.Tensor], moves: torch.Tensor, count: torch.Te
         if dtype is not _E4M3:
             raise SmcsdError("caches with scales must be float8_e4m3fn")
         codes = (ctypes.c_void_p * n)()
+        shape, u8 = torch.Size((P, H)), torch.uint8
         for i, x in enumerate(scales):
-            codes[i] = _codes(x, "scales[%d]" % i, P, H, dev)
+            if (isinstance(x, torch.Tensor) and x.shape == shape and x.dtype is u8 and
+                    x.get_device() == dev and x.is_contiguous()):
+                codes[i] = x.data_ptr()
+            else:
+                codes[i] = _codes(x, "scales[%d]" % i, P, H, dev)
         rc = _L().smcsd_kv_copy_scaled(ptrs, codes, n, H, page, segments, seg, tok, bs, mp, cp,
                                        moves.shape[0], P, sp, _queue(stream, dev))
         if rc:

@@ -290,13 +290,15 @@ struct CopyScales {
 };
 struct NoScales {};
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kCopyUnroll = 4;
 constexpr uint32_t kCopyWords = 1 << 20;
 
 // Workgroup = one (entry, cache) at a time, over all segments, four words of a thread in flight.
 // W: bytes moved at once.  Bound by memory: 1.6 GB of a compaction's moves take 320 us (5.0 TB/s
-// read and written, the rate of a large copy); 67 MB of copy-on-write tails 26 us (2.6 TB/s, their
-// pages lie scattered and each is a few KB).
+// read and written, the rate of a large copy); 67 MB of copy-on-write tails, a few KB each and
+// scattered, 12 us (22 with the words in uint4 arrays, which the compiler put into LDS); 34 MB of 8-bit pages'
+// tails and their scales 7.6 us in a graph, 7.1 without the scales.
 template <typename W, typename Scales>
 __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, Scales scales, int n_caches, int64_t block_stride,
                                                    int segments, int64_t segment_stride,
@@ -308,9 +310,13 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, Scales sca
   const int64_t entries = raw < 0 ? 0 : (raw > capacity ? capacity : raw);
   if (raw != entries && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, SMCSD_ST_BAD_INPUT);
   const int64_t items = entries * n_caches;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t e = it / n_caches;
-    const int c = (int)(it - e * n_caches);
+  // item e * n_caches + c; the grid's width in entries and caches, for one division in 32 bits
+  const int64_t wide = gridDim.x / (uint32_t)n_caches;
+  const int more = (int)(gridDim.x % (uint32_t)n_caches);
+  int64_t e = blockIdx.x / (uint32_t)n_caches;
+  int c = (int)(blockIdx.x % (uint32_t)n_caches);
+  for (int64_t it = blockIdx.x; it < items;
+       it += gridDim.x, e += wide + (c + more >= n_caches), c += c + more >= n_caches ? more - n_caches : more) {
     const int32_t src = list[3 * e], dst = list[3 * e + 1], tokens = list[3 * e + 2];
     if (dst == -1) continue;
     if (src < 0 || src >= P || dst < 0 || dst >= P || tokens < 0 || tokens > block_size) {
@@ -322,11 +328,9 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, Scales sca
     char *to = caches.p[c] + dst * block_stride;
     const uint32_t per = (uint32_t)(tokens * token_bytes / (int)sizeof(W));  // words of a segment
     if (per == 0) continue;
-    if constexpr (std::is_same<Scales, CopyScales>::value) {
-      const uint8_t *from_s = scales.p[c] + (int64_t)src * scales.Hkv;
-      uint8_t *to_s = scales.p[c] + (int64_t)dst * scales.Hkv;
-      for (int h = threadIdx.x; h < scales.Hkv; h += kPgBlock) to_s[h] = from_s[h];
-    }
+    int code = 0;  // this thread's, on its way while the data is copied
+    if constexpr (std::is_same<Scales, CopyScales>::value)
+      if ((int)threadIdx.x < scales.Hkv) code = scales.p[c][(int64_t)src * scales.Hkv + threadIdx.x];
     // some segments at a time, few enough for 32-bit word numbers
     const int most = (int)max(1u, kCopyWords / per);
     for (int h0 = 0; h0 < segments; h0 += most) {
@@ -345,6 +349,12 @@ __global__ __launch_bounds__(kPgBlock) void k_copy(CopyCaches caches, Scales sca
         for (int u = 0; u < kCopyUnroll; ++u)
           if (i0 + u * kPgBlock < words) *reinterpret_cast<W *>(to + off[u]) = v[u];
       }
+    }
+    if constexpr (std::is_same<Scales, CopyScales>::value) {
+      const uint8_t *from_s = scales.p[c] + (int64_t)src * scales.Hkv;
+      uint8_t *to_s = scales.p[c] + (int64_t)dst * scales.Hkv;
+      if ((int)threadIdx.x < scales.Hkv) to_s[threadIdx.x] = (uint8_t)code;
+      for (int h = threadIdx.x + kPgBlock; h < scales.Hkv; h += kPgBlock) to_s[h] = from_s[h];
     }
   }
 }
@@ -413,7 +423,7 @@ static hipError_t launch_copy(void *const *caches, const Scales &scales, int n_c
   }
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(capacity * n_caches, 2048)));
   if (low % 16 == 0)
-    hipLaunchKernelGGL((k_copy<uint4, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
+    hipLaunchKernelGGL((k_copy<u32x4, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
                        segment_stride, token_bytes, block_size, list, count, capacity, P, status);
   else if (low % 4 == 0)
     hipLaunchKernelGGL((k_copy<uint32_t, Scales>), grid, dim3(kPgBlock), 0, stream, cc, scales, n_caches, block_stride, segments,
