@@ -1,15 +1,20 @@
 // kvappend.hip - packed tokens' norms, rotation and way into pages of 16 or 8 bits (gfx950).
 //
-// Two kinds of waves in one launch.  A wave of the first kind takes one head's keys or values
-// of the tokens that one sequence puts into one block: an 8-bit block has one scale for them,
-// so the wave forms its tokens' values (in registers, up to kHold rounds of them; those of
-// longer blocks are formed twice), their largest magnitude, the scale, and only then the
-// rounded elements.  Nothing goes through LDS and no wave waits for another.  A wave of the
-// second kind takes the queries of one token, all heads, with one look at its position and
-// angles.  A head of D elements belongs to a group of lanes of 8 elements each, as in
-// k_qk_norm_rope: the sum of squares is a butterfly over the group.
+// Two kinds of workgroups in one launch.  One of the first kind takes the tokens that one sequence
+// puts into one block, its waves a head each in turn, keys and then values: an 8-bit block has one
+// scale for a head, so a wave forms its tokens' values (in registers, up to kHold rounds of them;
+// those of longer blocks are formed twice), their largest magnitude, the scale, and only then the
+// rounded elements.  Nothing goes through LDS and no wave waits for another.  A wave of the second
+// kind takes the queries of one token, all heads, with one look at its position and angles.  A head
+// of D elements belongs to a group of lanes of 8 elements each, as in k_qk_norm_rope: the sum of
+// squares is a butterfly over the group.
 // Blocks of all sequences are numbered with room to spare: sequence s's begin at
 // floor(cu[s] / block_size) + 2 s, since its n tokens touch at most floor(n / block_size) + 2.
+// Measured, bf16, 32 / 8 heads of 128, norms and rotation, blocks of 16: 40,262 tokens of 32 prompts into
+// 16-bit pages, 1.01 GB, 247 us (4.1 TB/s of a large copy's 4.9; without the arithmetic 190, without the
+// queries 89); 2560 tokens of 512 sequences into 8-bit pages, 59 MB, 27 us (2.2 TB/s; 18 without the
+// arithmetic): a chain of look-ups, loads, norm, scale and stores, which takes each workgroup as long as its
+// share of the bytes.  A wave to a block and head took 271 and 39, workgroups of 512 threads 283 and 40.
 #include <type_traits>
 
 #include "../../include/smcsd.h"

@@ -250,6 +250,43 @@ def test_row_tiles_of_three_waves(N, R, Hq):
     Case(B=2, N=N, R=R, Hq=Hq, Hkv=2 if Hq % 2 == 0 else 3, D=128, lens=(300, 311), shared=288 if N > 1 else 0, tree=True).call().check()
 
 
+@pytest.mark.parametrize("bs", [1, 3, 5, 6, 12])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("R,Hq", [(2, 2), (9, 8)])
+def test_shared_prefixes_of_blocks_of_any_length(bs, dt, R, Hq):
+    """Neighbouring keys of one product have scales of different blocks, also where the own keys begin."""
+    Case(dt, B=2, N=4, R=R, Hq=Hq, Hkv=2, D=64, bs=bs, lens=tuple(300 + x for x in (0, 1, 2, 3, 64)), shared=300).call().check()
+
+
+@pytest.mark.parametrize("ctx", [0, 1, 31, 32, 40, 63, 64, 100])
+@pytest.mark.parametrize("bs", [4, 16])
+def test_nodes_over_two_tiles_whose_values_are_no_numbers(ctx, bs):
+    """Every fifth node's value is NaN in one element: exactly the nodes behind it have NaN there, the rest
+    is as without."""
+    c, d = (Case(R=64, Hq=2, Hkv=2, D=64, bs=bs, lens=(ctx,)) for _ in range(2))
+    c.call()
+    where = torch.zeros(64, 64, dtype=torch.bool)
+    for j in range(2, 64, 5):
+        p = ctx + j
+        d.v.view(torch.uint8)[int(d.tables[0, p // bs]), p % bs, 1, j] = 0x7F
+        where[j:, j] = True
+    d.call()
+    assert int(d.status) == 0 and torch.equal(c.out[0, :, 0], d.out[0, :, 0]) and torch.equal(c.lse, d.lse)
+    got = d.out[0, :, 1].cpu()
+    assert torch.equal(got.isnan(), where)
+    assert torch.equal(got[~where], c.out[0, :, 1].cpu()[~where])
+
+
+def test_new_blocks_of_keys_that_are_no_numbers():
+    """Nodes 2 to 5 lie in a block whose keys' scale is NaN: a chain's nodes before them do not see it."""
+    c, d = (Case(R=6, lens=(30,)) for _ in range(2))
+    c.call()
+    d.sk[int(d.tables[0, 2]), 1] = 255
+    d.call()
+    assert torch.equal(c.out[0, :2], d.out[0, :2]) and torch.equal(c.out[0, :, :2], d.out[0, :, :2])
+    assert d.out[0, 2:, 2:].isnan().all()
+
+
 # ------------------------------------------------------------------------------------------------ copies with scales
 def copied(caches, scales, moves, bs):
     caches, scales = [c.view(torch.uint8).clone() for c in caches], [x.clone() for x in scales]
@@ -291,3 +328,29 @@ def test_copies_of_bad_entries_leave_scales_alone():
     sm.kv_copy([c], torch.tensor(moves, **I32), torch.tensor([6], **I32), st, scales=[x])
     assert int(st) == sm.ST_BAD_INPUT
     assert torch.equal(c.view(torch.uint8), want[0][0]) and torch.equal(x, want[1][0])
+
+
+@pytest.mark.parametrize("n", [3, 5, 128])
+def test_more_entries_than_workgroups(n):
+    """Entries x caches that no grid's width divides: every one is copied, once."""
+    g = torch.Generator().manual_seed(n)
+    P = 4200
+    caches, scales = zip(*(pages(P, 1, 1, 16, "bf16", True, "token", g) for _ in range(n)))
+    caches, scales = [on_gpu(c) for c in caches], [x.cuda() for x in scales]
+    ids = torch.randperm(P, generator=g).to(torch.int32)
+    moves = torch.stack([ids[:2100], ids[2100:], torch.ones(2100, dtype=torch.int32)], 1).cuda()
+    want = [c.view(torch.uint8).clone() for c in caches], [x.clone() for x in scales]
+    src, dst = ids[:2100].long().cuda(), ids[2100:].long().cuda()
+    for c in want[0] + want[1]:
+        c[dst] = c[src]
+    st = torch.zeros(1, **I32)
+    sm.kv_copy(caches, moves, torch.tensor([2100], **I32), st, scales=scales)
+    assert int(st) == 0
+    for c, x, wc, wx in zip(caches, scales, *want):
+        assert torch.equal(c.view(torch.uint8), wc) and torch.equal(x, wx)
+    plain = [torch.randn(P, 1, 1, 16, generator=g).cuda() for _ in range(n)]
+    want = [c.clone() for c in plain]
+    for c in want:
+        c[dst] = c[src]
+    sm.kv_copy(plain, moves, torch.tensor([2100], **I32), st)
+    assert int(st) == 0 and all(torch.equal(a, b) for a, b in zip(plain, want))
