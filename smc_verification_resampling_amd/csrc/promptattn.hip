@@ -585,9 +585,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_prompt(PromptAttnArgs a, Plan p
                    if (i == 0) pg = look_up(asked, block);
                  },
                  [&](int i) {
-                   const int n = i * NL / (NP / 2);
                    if (i < NP / 2) {
-                     if (i == n * (NP / 2) / NL) {
+#pragma unroll
+                     for (int n = 0; n < NL; ++n) {
+                       if (i != n * (NP / 2) / NL) continue;
                        uint4 k[PC], v[PC];
                        widened(next, n, k, v);
                        put_row(far, n, k, v);

@@ -104,6 +104,13 @@ def test_head_sizes(dt, e4m3, D):
     Case(dt, e4m3, D=D, new=(70, 3, 129), ctx=(0, 37), layout="head").call().check()
 
 
+@pytest.mark.parametrize("D,e4m3", [(D, e) for D in (16, 48, 64, 72, 80, 88, 96, 104, 128, 144, 192, 200, 256) for e in (False, True) if not (e and D % 16)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_head_sizes_over_many_tiles(dt, e4m3, D):
+    """Every part of every tile of keys, those beyond the first two among them, is in its place."""
+    Case(dt, e4m3, D=D, Hq=4, Hkv=2, new=(700, 301), ctx=(0, 520)).call().check()
+
+
 @pytest.mark.parametrize("D", [8, 24, 72, 136, 200])
 def test_head_sizes_of_16_bit_pages_alone(D):
     Case(D=D, new=(70, 3, 129), ctx=(0, 37)).call().check()
