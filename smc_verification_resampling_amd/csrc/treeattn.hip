@@ -319,11 +319,13 @@ __device__ const uint4 kNothing = {0, 0, 0, 0};  // loaded where there is nothin
 // to 4093 keys, 3.2 GB of pages, 608 us (5.4 TB/s: bound by the loads, which took as long without
 // any arithmetic, whatever the pages' order and the bytes in flight); f16, heads of 64,
 // one token of 4 sequences of 16 keys 5.6 us, all of it latency.
-// 8-bit pages: the shared pass 130 us, the own keys 54; the 256 sequences, 1.65 GB, 374 us (4.4 TB/s).  Both
-// are bound by instructions: vector ones take about half of the SIMDs' time, the products a quarter, and
-// two or three waves cannot overlap them further.  Of some 200 vector instructions that 32 keys take a wave,
-// 64 widen.  Higher priority for the waves at a product gave 1 %; bounds for a third wave left the compiler
-// without a place for the 188 registers of NW = 2, and it fell to one wave (528 us for the 256 sequences).
+// 8-bit pages: the shared pass 128 us, the own keys 54; the 256 sequences, 1.65 GB, 375 us (4.4 TB/s).  Vector
+// instructions take about half of the SIMDs' time (of some 200 for 32 keys of a wave, 64 widen), the products a
+// quarter, and of the 256 sequences a part is the loads': 128 bytes of a token's head lie together, and pages
+// laid out by head, 2048 bytes, take 11 % less.  Within 1 %: higher priority for the waves at a product, values read
+// while the scores are formed, addresses kept in registers, whole tiles loaded without a look at each row,
+// the heads of a sequence on one XCD.  Bounds for a third wave left the compiler without a place for the
+// registers of NW = 2, and it fell to one wave (528 us for the 256 sequences).
 template <int DT, int DP, int NW, bool PREFIX, int PG>
 __global__ __launch_bounds__(NW * kWave, DP == 256 ? 1 : NW == 4 && PREFIX ? 3 : 2) void k_attn(TreeAttnArgs a, Plan p) {
   typedef typename Half<DT>::V8 V8;
