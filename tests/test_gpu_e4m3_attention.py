@@ -258,6 +258,13 @@ def test_shared_prefixes_of_blocks_of_any_length(bs, dt, R, Hq):
     Case(dt, B=2, N=4, R=R, Hq=Hq, Hkv=2, D=64, bs=bs, lens=tuple(300 + x for x in (0, 1, 2, 3, 64)), shared=300).call().check()
 
 
+@pytest.mark.parametrize("bs", [1, 7, 8])
+@pytest.mark.parametrize("D", [48, 128, 176, 256])
+@pytest.mark.parametrize("R,Hq", [(1, 2), (20, 8)])
+def test_blocks_of_any_length_and_heads_of_any_size(bs, D, R, Hq):
+    Case(B=2, N=3, R=R, Hq=Hq, Hkv=2, D=D, bs=bs, lens=(280, 281, 299, 411), shared=280, tree=R > 1, layout="head").call().check()
+
+
 @pytest.mark.parametrize("ctx", [0, 1, 31, 32, 40, 63, 64, 100])
 @pytest.mark.parametrize("bs", [4, 16])
 def test_nodes_over_two_tiles_whose_values_are_no_numbers(ctx, bs):
